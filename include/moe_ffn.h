@@ -481,6 +481,137 @@ int moe_ffn_prefill_timed(moe_weights_t w, const float *hidden, const float *rou
                           int path, void *ws, size_t ws_bytes, cudaStream_t stream,
                           cudaEvent_t *stage_events);
 
+/* ---------------------------------------------------------------------------
+ * Token rows sorted by expert and back, for experts that run outside this
+ * library between the router and the combine, in training as well: element
+ * types fp32, fp16 and bf16, dropped entries, rows apart by any stride, and
+ * the gradients.  Sums and weights are fp32, each result is rounded to the
+ * element type once.
+ *   dtype       enum moe_dtype of every tensor that is not stated otherwise
+ *   D >= 1, N >= 1, 1 <= top_k <= min(E, 32), E <= 1024, N * top_k < 2^30
+ *   *_stride    elements from one row to the next (at most 2^30); an input's
+ *               may be 0 (one row for all), an output's is at least D
+ *   tokRow      [N][top_k] int32: the sorted row of each entry, or -1 for a
+ *               dropped one
+ * 16-byte accesses are used when pointers, strides and D allow, smaller ones
+ * otherwise; the results are the same.
+ * ws: status word and scratch, 256-byte aligned, moe_sort_workspace_size bytes
+ * for moe_sort_tokens and 256 for the others, initialised once by
+ * moe_workspace_init (any workspace of this library that is large enough).
+ * Outputs overlap no input and no other output (MOE_ERR_INVALID_ARG).
+ * ------------------------------------------------------------------------- */
+enum moe_dtype { MOE_DTYPE_F32 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_BF16 = 2 };
+
+size_t moe_sort_workspace_size(int N, int top_k, int E);
+
+/* moe_sort_tokens -- the CSR of moe_bucket with dropped entries, and the rows
+ * in its order ("gather tokens per expert", #406 "The work" item 2):
+ *   topk_idx [N][top_k] int32: an expert, or -1 for an entry that goes nowhere
+ *            (padding, an expert held elsewhere).  Unlike moe_bucket a token
+ *            may name an expert more than once.
+ *   expStart [E+1] int32 out: segment offsets; expStart[E] = entries kept
+ *   expTokI, expTokK [N*top_k] int32 out: token and slot of each sorted row,
+ *            by expert, then token, then slot; -1 from expStart[E] on
+ *   tokRow   [N][top_k] int32 out: the inverse, -1 where dropped
+ *   rows     [N*top_k][D] out: rows[r] = x[expTokI[r]], bit for bit; rows from
+ *            expStart[E] on are left as they were
+ * Any other negative index, or one of E and above, sets MOE_DEV_BAD_ROUTING
+ * and counts as dropped. */
+int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N,
+                    int top_k, int E, int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK,
+                    int32_t *tokRow, void *rows, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Its gradient: d_x[t][c] = sum over the slots s of t, in slot order, of
+ * d_rows[tokRow[t][s]][c] (dropped entries add nothing; a token without
+ * entries gets zeros).  d_rows [n_rows][D], d_x [N][D].  An entry of tokRow
+ * outside [-1, n_rows) sets MOE_DEV_BAD_CSR and counts as dropped, here and in
+ * the two functions below. */
+int moe_sort_tokens_grad(const void *d_rows, int64_t n_rows, int dtype, const int32_t *tokRow, int N,
+                         int top_k, int D, void *d_x, int64_t d_x_stride, void *ws, size_t ws_bytes,
+                         cudaStream_t stream);
+
+/* moe_unsort_tokens -- sorted rows back to their tokens, weighted (the combine
+ * of moe_combine for rows in CSR order and any element type):
+ *   acc = +0; for s = 0..top_k-1: if tokRow[t][s] >= 0:
+ *       acc = fmaf(topk_w[t][s], rows[tokRow[t][s]][c], acc);
+ *   out[t][c] = acc.
+ *   rows [n_rows][D], topk_w [N][top_k] fp32, out [N][D].  A dropped entry's
+ *   weight is not used; a weight of zero still multiplies its row. */
+int moe_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t *tokRow,
+                      const float *topk_w, int N, int top_k, int D, void *out, int64_t out_stride,
+                      void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Its gradients, for d_out [N][D]:
+ *   d_rows[tokRow[t][s]][c] = topk_w[t][s] * d_out[t][c]   (one rounding)
+ *   d_topk_w[t][s] = sum_c d_out[t][c] * rows[tokRow[t][s]][c]  (fp32; 0 where dropped)
+ * in one pass.  d_rows [n_rows][D]: rows that no entry names are left as they
+ * were; two entries that name one row (moe_sort_tokens gives none) leave
+ * either's value.  The dot's order is fixed for given N, D, type and
+ * alignment. */
+int moe_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const void *rows, int64_t n_rows,
+                           int dtype, const int32_t *tokRow, const float *topk_w, int N, int top_k,
+                           int D, void *d_rows, float *d_topk_w, void *ws, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/* moe_topk_grad -- the gradient of the routing weights (moe_router_topk's and
+ * moe_topk_from_logits' topk_w) to the router logits:
+ *   norm_topk_prob == 0: p = softmax(logits[t]), v[e] = sum of d_topk_w[t][s] over the
+ *       slots with topk_idx[t][s] == e:  d_logits[t][e] = p[e] * (v[e] - sum_j p[j] v[j])
+ *   norm_topk_prob != 0: the same with the softmax taken over the selected experts
+ *       alone, and d_logits 0 at the others.
+ * logits, d_logits [N][E] fp32, topk_idx [N][top_k] int32, d_topk_w [N][top_k] fp32.
+ * A slot of -1 counts as not selected; any other index outside [0, E) does too and
+ * sets MOE_DEV_BAD_ROUTING.  A token whose softmax has no logit above -inf gets zeros. */
+int moe_topk_grad(const float *logits, const int32_t *topk_idx, const float *d_topk_w, int N, int E,
+                  int top_k, int norm_topk_prob, float *d_logits, void *ws, size_t ws_bytes,
+                  cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Products with 4-bit weights and group scales, the activations unquantised
+ * (the decode matvecs of #408 levers 1 and 2 for weights that come as codes,
+ * scales and zero points, beside the K-quants above):
+ *   W[e][r][k] = scales[e][r][k/group] * (q[e][r][k] - zeros[e][r][k/group])
+ *   moe_w4_matvec: y[j][r] = sum_k W[e(j)][r][k] * x[j][k]
+ * moe_w4_weights_create lays the caller's arrays out for the kernel in a
+ * library-owned device copy (it allocates and synchronises `stream`; the
+ * caller's buffers may be freed afterwards).
+ *   q      [E][R][K/2] bytes: the code 0..15 of column 2b in the low, of 2b + 1
+ *          in the high four bits of byte b
+ *   scales [E][R][K/group] fp16 or bf16 (scale_dtype)
+ *   zeros  [E][R][K/group] bytes, 0..15 (the low four bits count), or NULL: 8
+ *   group  32, 64 or 128; K a multiple of it, at most 32768; R >= 1; E <= 1024
+ *   up_q, up_scales, up_zeros: NULL, or a second matrix of the same shape (up_zeros
+ *          NULL iff zeros is): the handle then holds gate and up, and the product is
+ *          y = SiLU(gate) * up, SiLU(z) = z / (1 + exp(-z)), in fp32 before the one
+ *          rounding to y's type.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_w4_weights_s *moe_w4_weights_t;
+
+int moe_w4_weights_create(moe_w4_weights_t *out, int E, int R, int K, int group, int scale_dtype,
+                          const uint8_t *q, const void *scales, const uint8_t *zeros,
+                          const uint8_t *up_q, const void *up_scales, const uint8_t *up_zeros,
+                          cudaStream_t stream);
+int moe_w4_weights_destroy(moe_w4_weights_t w);
+/* Shape of a handle; *pair is 1 when it holds gate and up (any output may be NULL; host pointers). */
+int moe_w4_weights_shape(moe_w4_weights_t w, int *E, int *R, int *K, int *group, int *pair);
+size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
+
+/* y[j] = the handle's product of row x[j], for rows in CSR order (moe_sort_tokens).
+ *   x [n_rows][K], y [n_rows][R] of `dtype`; strides as for moe_sort_tokens
+ *   expStart [E+1] int32 device: rows expStart[e]..expStart[e+1]-1 are expert e's;
+ *            rows from expStart[E] on are left as they were.  NULL (E == 1 only):
+ *            every row is expert 0's.  Offsets that do not start at 0, decrease or
+ *            pass n_rows set MOE_DEV_BAD_CSR and every row is left.
+ * fp16 and bf16 rows enter the products as they are, fp32 rows as the exact sum of three
+ * bf16 parts; codes less zero points are exact, products are summed in fp32 per group and
+ * the groups' sums, times their scales, in fp32 (their order is fixed for given shapes and
+ * types); a group's sum of (q - z) x itself has to stay in fp32's range.  Made for few rows an expert (decode): each 32 rows (fp32: 10) of an expert
+ * read its weights once more.
+ *   ws: status word (256 bytes). */
+int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype,
+                  const int32_t *expStart, int n_rows, void *y, int64_t y_stride, void *ws,
+                  size_t ws_bytes, cudaStream_t stream);
+
 /* Device pointers to the intermediates moe_ffn_prefill leaves in `ws`
  * (valid after it ran on that workspace with the same shape); any output
  * pointer may be NULL.  Host pointers to receive device addresses. */

@@ -4,8 +4,10 @@
 // host memory (the caller's hidden and output rows, in place).
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <new>
 
+#include "elem.cuh"
 #include "moe_internal.cuh"
 
 using namespace moe;
@@ -91,6 +93,55 @@ int check_ws(const void *ws, size_t ws_bytes, const WsLayout &L) {
     if (ws == nullptr) return MOE_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOE_ERR_INVALID_ARG;
     return ws_bytes >= L.total ? MOE_OK : MOE_ERR_WORKSPACE_TOO_SMALL;
+}
+
+// ---- token sort / unsort and 4-bit products
+constexpr int64_t MAX_STRIDE = (int64_t)1 << 30;
+constexpr int MAX_ROW = 1 << 24;  // elements of a token row
+
+bool dtype_ok(int dtype) { return dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_F16 || dtype == MOE_DTYPE_BF16; }
+
+// (N, top_k, E) of the token operators: shape_ok without a row length.
+bool token_shape_ok(int N, int top_k, int E) { return shape_ok(N, QK, E, top_k) && (int64_t)N * top_k < (1 << 30); }
+
+// N and top_k where the number of experts is not part of the call.
+bool entry_shape_ok(int N, int top_k, int D) {
+    return N >= 1 && top_k >= 1 && top_k <= 32 && (int64_t)N * top_k < (1 << 30) && D >= 1 && D <= MAX_ROW;
+}
+
+int check_ws(const void *ws, size_t ws_bytes, size_t need) {
+    if (ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOE_ERR_INVALID_ARG;
+    return ws_bytes >= need ? MOE_OK : MOE_ERR_WORKSPACE_TOO_SMALL;
+}
+
+// Bytes from the first to past the last element of `rows` rows of `cols`, `stride` apart.
+struct Span {
+    const char *p;
+    int64_t n;
+};
+Span span(const void *p, int64_t rows, int64_t stride, int64_t cols, int64_t elem) {
+    return {static_cast<const char *>(p), p && rows > 0 ? ((rows - 1) * stride + cols) * elem : 0};
+}
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+// No output overlaps another output or an input.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (auto a = outs.begin(); a != outs.end(); ++a) {
+        for (auto b = a + 1; b != outs.end(); ++b)
+            if (overlap(*a, *b)) return false;
+        for (const Span &b : ins)
+            if (overlap(*a, b)) return false;
+    }
+    return true;
+}
+// Element alignment.
+bool aligned(const void *p, size_t elem) { return reinterpret_cast<uintptr_t>(p) % elem == 0; }
+bool aligned4(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (!aligned(p, 4)) return false;
+    return true;
 }
 
 unsigned *status_word(void *ws) { return reinterpret_cast<unsigned *>(ws); }
@@ -689,6 +740,168 @@ int moe_ffn_prefill(moe_weights_t w, const float *hidden, const float *routerW, 
                     int top_k, int norm_topk_prob, float *out, void *ws, size_t ws_bytes, cudaStream_t stream) {
     return moe_ffn_prefill_ex(w, hidden, routerW, shexp_gate, N, top_k, norm_topk_prob, out, MOE_PATH_AUTO, ws,
                               ws_bytes, stream);
+}
+
+size_t moe_sort_workspace_size(int N, int top_k, int E) {
+    if (!token_shape_ok(N, top_k, E)) return 0;
+    return SORT_SCRATCH_OFFSET + align256(sort_scratch_bytes(N, E));
+}
+
+int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N, int top_k, int E,
+                    int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows,
+                    void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!x || !topk_idx || !expStart || !expTokI || !expTokK || !tokRow || !rows || !dtype_ok(dtype) || x_stride < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!token_shape_ok(N, top_k, E) || D < 1 || D > MAX_ROW || x_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_ws(ws, ws_bytes, moe_sort_workspace_size(N, top_k, E));
+    if (rc) return rc;
+    const int64_t Nk = (int64_t)N * top_k, b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(x, b) || !aligned(rows, b) || !aligned4({topk_idx, expStart, expTokI, expTokK, tokRow})) return MOE_ERR_INVALID_ARG;
+    if (!apart({span(expStart, 1, 0, E + 1, 4), span(expTokI, 1, 0, Nk, 4), span(expTokK, 1, 0, Nk, 4),
+                span(tokRow, 1, 0, Nk, 4), span(rows, Nk, D, D, b), span(ws, 1, 0, (int64_t)ws_bytes, 1)},
+               {span(x, N, x_stride, D, b), span(topk_idx, 1, 0, Nk, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_sort_tokens(x, x_stride, dtype, topk_idx, N, top_k, E, D, expStart, expTokI, expTokK, tokRow, rows,
+                              ws, stream);
+}
+
+int moe_sort_tokens_grad(const void *d_rows, int64_t n_rows, int dtype, const int32_t *tokRow, int N, int top_k,
+                         int D, void *d_x, int64_t d_x_stride, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!d_rows || !tokRow || !d_x || !dtype_ok(dtype) || n_rows < 1 || d_x_stride < D) return MOE_ERR_INVALID_ARG;
+    if (!entry_shape_ok(N, top_k, D) || n_rows >= (1 << 30) || d_x_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    const int64_t Nk = (int64_t)N * top_k, b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(d_rows, b) || !aligned(d_x, b) || !aligned4({tokRow})) return MOE_ERR_INVALID_ARG;
+    if (!apart({span(d_x, N, d_x_stride, D, b), span(ws, 1, 0, 256, 1)},
+               {span(d_rows, n_rows, D, D, b), span(tokRow, 1, 0, Nk, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_unsort_tokens(d_rows, n_rows, dtype, tokRow, nullptr, N, top_k, D, d_x, d_x_stride, status_word(ws),
+                                stream);
+}
+
+int moe_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t *tokRow, const float *topk_w, int N,
+                      int top_k, int D, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                      cudaStream_t stream) {
+    if (!rows || !tokRow || !topk_w || !out || !dtype_ok(dtype) || n_rows < 1 || out_stride < D)
+        return MOE_ERR_INVALID_ARG;
+    if (!entry_shape_ok(N, top_k, D) || n_rows >= (1 << 30) || out_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    const int64_t Nk = (int64_t)N * top_k, b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(rows, b) || !aligned(out, b) || !aligned4({tokRow, topk_w})) return MOE_ERR_INVALID_ARG;
+    if (!apart({span(out, N, out_stride, D, b), span(ws, 1, 0, 256, 1)},
+               {span(rows, n_rows, D, D, b), span(tokRow, 1, 0, Nk, 4), span(topk_w, 1, 0, Nk, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_unsort_tokens(rows, n_rows, dtype, tokRow, topk_w, N, top_k, D, out, out_stride, status_word(ws),
+                                stream);
+}
+
+int moe_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const void *rows, int64_t n_rows, int dtype,
+                           const int32_t *tokRow, const float *topk_w, int N, int top_k, int D, void *d_rows,
+                           float *d_topk_w, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!d_out || !rows || !tokRow || !topk_w || !d_rows || !d_topk_w || !dtype_ok(dtype) || n_rows < 1 ||
+        d_out_stride < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!entry_shape_ok(N, top_k, D) || n_rows >= (1 << 30) || d_out_stride > MAX_STRIDE)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    const int64_t Nk = (int64_t)N * top_k, b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(d_out, b) || !aligned(rows, b) || !aligned(d_rows, b) || !aligned4({tokRow, topk_w, d_topk_w}))
+        return MOE_ERR_INVALID_ARG;
+    if (!apart({span(d_rows, n_rows, D, D, b), span(d_topk_w, 1, 0, Nk, 4), span(ws, 1, 0, 256, 1)},
+               {span(d_out, N, d_out_stride, D, b), span(rows, n_rows, D, D, b), span(tokRow, 1, 0, Nk, 4),
+                span(topk_w, 1, 0, Nk, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_unsort_tokens_grad(d_out, d_out_stride, rows, n_rows, dtype, tokRow, topk_w, N, top_k, D, d_rows,
+                                     d_topk_w, status_word(ws), stream);
+}
+
+int moe_topk_grad(const float *logits, const int32_t *topk_idx, const float *d_topk_w, int N, int E, int top_k,
+                  int norm_topk_prob, float *d_logits, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!logits || !topk_idx || !d_topk_w || !d_logits) return MOE_ERR_INVALID_ARG;
+    if (!token_shape_ok(N, top_k, E)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    if (!aligned4({logits, topk_idx, d_topk_w, d_logits})) return MOE_ERR_INVALID_ARG;
+    const int64_t Nk = (int64_t)N * top_k;
+    if (!apart({span(d_logits, N, E, E, 4), span(ws, 1, 0, 256, 1)},
+               {span(logits, N, E, E, 4), span(topk_idx, 1, 0, Nk, 4), span(d_topk_w, 1, 0, Nk, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_topk_grad(logits, topk_idx, d_topk_w, N, E, top_k, norm_topk_prob ? 1 : 0, d_logits, status_word(ws),
+                            stream);
+}
+
+int moe_w4_weights_create(moe_w4_weights_t *out, int E, int R, int K, int group, int scale_dtype, const uint8_t *q,
+                          const void *scales, const uint8_t *zeros, const uint8_t *up_q, const void *up_scales,
+                          const uint8_t *up_zeros, cudaStream_t stream) {
+    if (out == nullptr) return MOE_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!q || !scales || (scale_dtype != MOE_DTYPE_F16 && scale_dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARG;
+    if ((up_q == nullptr) != (up_scales == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (up_q == nullptr ? up_zeros != nullptr : (up_zeros == nullptr) != (zeros == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(scales, 2) || !aligned(up_scales, 2)) return MOE_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (E < 1 || E > MAX_E || R < 1 || R > MAX_ROW || K < group || K % group || K > 32768)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED_DEVICE;
+    moe_w4_weights_s *w = new (std::nothrow) moe_w4_weights_s();
+    if (!w) return MOE_ERR_CUDA;
+    w->E = E;
+    w->R = R;
+    w->K = K;
+    w->group = group;
+    w->scale_dtype = scale_dtype;
+    w->pair = up_q != nullptr;
+    w->device = dev;
+    int rc = w4_repack(w, q, scales, zeros, up_q, up_scales, up_zeros, stream);
+    if (rc) {
+        moe_w4_weights_destroy(w);
+        return rc;
+    }
+    *out = w;
+    return MOE_OK;
+}
+
+int moe_w4_weights_destroy(moe_w4_weights_t w) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    if (w->codes) cudaFree(w->codes);
+    delete w;
+    return MOE_OK;
+}
+
+int moe_w4_weights_shape(moe_w4_weights_t w, int *E, int *R, int *K, int *group, int *pair) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    if (E) *E = w->E;
+    if (R) *R = w->R;
+    if (K) *K = w->K;
+    if (group) *group = w->group;
+    if (pair) *pair = w->pair;
+    return MOE_OK;
+}
+
+size_t moe_w4_weights_device_bytes(moe_w4_weights_t w) { return w ? w->bytes : 0; }
+
+int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype, const int32_t *expStart, int n_rows,
+                  void *y, int64_t y_stride, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!w || !x || !y || !dtype_ok(dtype) || n_rows < 1 || x_stride < 0 || y_stride < w->R) return MOE_ERR_INVALID_ARG;
+    if (expStart == nullptr && w->E != 1) return MOE_ERR_INVALID_ARG;
+    if (n_rows >= (1 << 30) || x_stride > MAX_STRIDE || y_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (current_device() != w->device) return MOE_ERR_INVALID_ARG;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    const int64_t b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(x, b) || !aligned(y, b) || !aligned4({expStart})) return MOE_ERR_INVALID_ARG;
+    if (!apart({span(y, n_rows, y_stride, w->R, b), span(ws, 1, 0, 256, 1)},
+               {span(x, n_rows, x_stride, w->K, b), span(expStart, 1, 0, w->E + 1, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_w4_matvec(w, x, x_stride, dtype, expStart, n_rows, y, y_stride, status_word(ws), stream);
 }
 
 int moe_workspace_views(void *ws, int N, int D, int E, int F, int top_k, int Fs, int32_t **topk_idx, float **topk_w,

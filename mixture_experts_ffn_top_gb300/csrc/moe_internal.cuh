@@ -60,6 +60,18 @@ struct moe_weights_s {
     void *tmaps = nullptr;   // host copy of the TMA descriptors (tensor path), owned
 };
 
+// 4-bit weights with group scales, in w4_matvec.cu's tile order (see moe_w4_weights_create).
+struct moe_w4_weights_s {
+    int E = 0, R = 0, K = 0, group = 0;
+    int scale_dtype = MOE_DTYPE_F16;
+    int pair = 0;               // gate and up
+    int ntiles = 0, nchunk = 0;  // tiles of 16 weight rows per expert, chunks of 128 columns
+    int device = -1;
+    size_t bytes = 0;
+    char *codes = nullptr;      // the device allocation; scales and zeros lie in it
+    char *scales = nullptr, *zeros = nullptr;
+};
+
 namespace moe {
 
 // ------------------------------------------------------------- workspace --
@@ -174,6 +186,26 @@ int launch_combine_rmsnorm(const float *partials, const float *topk_w, const flo
                            cudaStream_t s, bool early = false);
 // normed = RMSNorm(x) * gamma alone (launch_combine_rmsnorm with no slots and no out).
 int launch_rmsnorm(const float *x, const float *gamma, float eps, int N, int D, float *normed, cudaStream_t s);
+// token_sort.cu (scratch: the per-range count table, at SORT_SCRATCH_OFFSET of the workspace)
+constexpr size_t SORT_SCRATCH_OFFSET = 256;
+int sort_ranges(int N, int *tokens);
+size_t sort_scratch_bytes(int N, int E);
+int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *idx, int N, int top_k, int E, int D,
+                       int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows, void *ws,
+                       cudaStream_t s);
+// w == NULL: plain sums (the gradient of the sort)
+int launch_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t *tokRow, const float *w, int N,
+                         int top_k, int D, void *out, int64_t out_stride, unsigned *status, cudaStream_t s);
+int launch_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const void *rows, int64_t n_rows, int dtype,
+                              const int32_t *tokRow, const float *w, int N, int top_k, int D, void *d_rows, float *d_w,
+                              unsigned *status, cudaStream_t s);
+int launch_topk_grad(const float *logits, const int32_t *idx, const float *d_w, int N, int E, int top_k, int norm,
+                     float *d_logits, unsigned *status, cudaStream_t s);
+// w4_matvec.cu
+int w4_repack(moe_w4_weights_s *w, const uint8_t *q, const void *scales, const uint8_t *zeros, const uint8_t *up_q,
+              const void *up_scales, const uint8_t *up_zeros, cudaStream_t s);
+int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride, int dtype, const int32_t *expStart,
+                     int n_rows, void *y, int64_t y_stride, unsigned *status, cudaStream_t s);
 // weights.cu
 int repack_weights(moe_weights_s *w, const void *gate, const void *up, const void *down,
                    const void *sh_gate, const void *sh_up, const void *sh_down, cudaStream_t s);

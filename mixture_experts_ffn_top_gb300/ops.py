@@ -67,6 +67,17 @@ _SIGS = {
     "moe_ffn_prefill_residual_rmsnorm": (_I, [_P, _P, _P, _P, _P, _P, ctypes.c_float, _I, _I, _I, _P, _P, _I, _P,
                                                _SZ, _P]),
     "moe_workspace_views": (_I, [_P, _I, _I, _I, _I, _I, _I] + [ctypes.POINTER(_P)] * 10),
+    "moe_sort_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_sort_tokens": (_I, [_P, _I64, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_sort_tokens_grad": (_I, [_P, _I64, _I, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
+    "moe_unsort_tokens": (_I, [_P, _I64, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
+    "moe_unsort_tokens_grad": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_topk_grad": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_w4_weights_create": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_w4_weights_destroy": (_I, [_P]),
+    "moe_w4_weights_shape": (_I, [_P] + [ctypes.POINTER(_I)] * 5),
+    "moe_w4_weights_device_bytes": (_SZ, [_P]),
+    "moe_w4_matvec": (_I, [_P, _P, _I64, _I, _P, _I, _P, _I64, _P, _SZ, _P]),
     "moe_ffn_prefill_stack": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _SZ, _P]),
 }
 
@@ -578,6 +589,250 @@ def moe_workspace_views(ws, N, D, E, F, top_k, Fs=0):
         nbytes = int(torch.tensor([], dtype=dt).element_size()) * int(torch.Size(shape).numel())
         out[name] = ws[off:off + nbytes].view(dt).view(shape)
     return out
+
+
+# --------------------------------------------- token sort, 4-bit products ---
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # MOE_DTYPE_*
+
+
+def _on(device: int, stream, name: str, *args) -> None:
+    """Call entry point `name` on `stream` (default: the current stream of `device`) with `device` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device_index != device:
+        raise ValueError("stream must be of the tensors' device")
+    if torch.cuda.current_device() == device:
+        rc = getattr(lib(), name)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib(), name)(*args, stream.cuda_stream)
+    if rc != 0:
+        raise MoeError(rc, name)
+
+
+def _arg(t: torch.Tensor, dtype, shape, device: int, name: str) -> int:
+    """Address of a contiguous CUDA tensor of that type, shape and device."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got cuda:{t.get_device()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_arg(t: torch.Tensor, name: str, dtype=None, shape=None, device: int | None = None) -> tuple[int, int]:
+    """(address, row stride) of a 2-D CUDA tensor of a supported type with contiguous rows."""
+    if not t.is_cuda or (device is not None and t.get_device() != device):
+        raise ValueError(f"{name} must be " + ("a CUDA tensor" if device is None else f"on cuda:{device}"))
+    if t.dtype not in DTYPES or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{name} must be " + ("float32, float16 or bfloat16" if dtype is None else f"{dtype}") +
+                         f", got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape " + ("[rows, columns]" if shape is None else f"{tuple(shape)}") +
+                         f", got {tuple(t.shape)}")
+    n, d = t.shape
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (t.stride(0) if n > 1 else d)
+
+
+def moe_sort_workspace_size(N, top_k, E) -> int:
+    n = int(lib().moe_sort_workspace_size(N, top_k, E))
+    if n == 0:
+        raise MoeError(-2, "moe_sort_workspace_size")
+    return n
+
+
+def new_sort_workspace(N, top_k, E, device="cuda", stream=None) -> torch.Tensor:
+    """A workspace for moe_sort_tokens of that shape (and for every other function of this section)."""
+    ws = torch.empty(moe_sort_workspace_size(N, top_k, E), dtype=torch.uint8, device=device)
+    dev = ws.get_device()
+    _on(dev, stream, "moe_workspace_init", ws.data_ptr(), ws.numel())
+    return ws
+
+
+def _ws(ws: torch.Tensor, device: int) -> tuple[int, int]:
+    return _arg(ws, torch.uint8, ws.shape, device, "ws"), ws.numel()
+
+
+def moe_sort_tokens(x, topk_idx, E, ws, rows=None, stream=None):
+    """Rows of x [N, D] sorted by expert: -> (rows [N*top_k, D], expStart [E+1], expTokI, expTokK [N*top_k],
+    tokRow [N, top_k]).  topk_idx may hold -1 (dropped); rows from expStart[E] on are left as they were
+    (uninitialised when `rows` is not given).  x may be strided by rows."""
+    xp, xs = _rows_arg(x, "x")
+    N, D = x.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != N:
+        raise ValueError(f"topk_idx must have shape [{N}, top_k], got {tuple(topk_idx.shape)}")
+    k, dev, device = topk_idx.shape[1], x.get_device(), x.device
+    ip = _arg(topk_idx, torch.int32, topk_idx.shape, dev, "topk_idx")
+    if rows is None:
+        rows = torch.empty((N * k, D), dtype=x.dtype, device=device)
+    rp = _arg(rows, x.dtype, (N * k, D), dev, "rows")
+    start = torch.empty(E + 1, dtype=torch.int32, device=device)
+    tok = torch.empty(N * k, dtype=torch.int32, device=device)
+    slot = torch.empty(N * k, dtype=torch.int32, device=device)
+    row = torch.empty((N, k), dtype=torch.int32, device=device)
+    _on(dev, stream, "moe_sort_tokens", xp, xs, DTYPES[x.dtype], ip, N, k, E, D, start.data_ptr(), tok.data_ptr(),
+        slot.data_ptr(), row.data_ptr(), rp, *_ws(ws, dev))
+    return rows, start, tok, slot, row
+
+
+def moe_sort_tokens_grad(d_rows, tokRow, ws, d_x=None, stream=None):
+    """Gradient of moe_sort_tokens' rows to x: d_x[t] = the sum of d_rows over the entries of t."""
+    dev = d_rows.get_device()
+    if d_rows.dim() != 2 or tokRow.dim() != 2 or d_rows.dtype not in DTYPES:
+        raise ValueError("d_rows must be [rows, D] (float32, float16 or bfloat16), tokRow [N, top_k]")
+    (n, D), (N, k) = d_rows.shape, tokRow.shape
+    dp = _arg(d_rows, d_rows.dtype, (n, D), dev, "d_rows")
+    if d_x is None:
+        d_x = torch.empty((N, D), dtype=d_rows.dtype, device=d_rows.device)
+    xp, xs = _rows_arg(d_x, "d_x", d_rows.dtype, (N, D), dev)
+    _on(dev, stream, "moe_sort_tokens_grad", dp, n, DTYPES[d_rows.dtype], _arg(tokRow, torch.int32, (N, k), dev, "tokRow"),
+        N, k, D, xp, xs, *_ws(ws, dev))
+    return d_x
+
+
+def moe_unsort_tokens(rows, tokRow, topk_w, ws, out=None, stream=None):
+    """Sorted rows back to their tokens: out[t] = sum over the slots of topk_w[t, s] * rows[tokRow[t, s]]."""
+    dev = rows.get_device()
+    if rows.dim() != 2 or tokRow.dim() != 2 or rows.dtype not in DTYPES:
+        raise ValueError("rows must be [rows, D] (float32, float16 or bfloat16), tokRow [N, top_k]")
+    (n, D), (N, k) = rows.shape, tokRow.shape
+    rp = _arg(rows, rows.dtype, (n, D), dev, "rows")
+    if out is None:
+        out = torch.empty((N, D), dtype=rows.dtype, device=rows.device)
+    op, os_ = _rows_arg(out, "out", rows.dtype, (N, D), dev)
+    _on(dev, stream, "moe_unsort_tokens", rp, n, DTYPES[rows.dtype], _arg(tokRow, torch.int32, (N, k), dev, "tokRow"),
+        _arg(topk_w, torch.float32, (N, k), dev, "topk_w"), N, k, D, op, os_, *_ws(ws, dev))
+    return out
+
+
+def moe_unsort_tokens_grad(d_out, rows, tokRow, topk_w, ws, d_rows=None, stream=None):
+    """Gradients of moe_unsort_tokens: -> (d_rows like rows, d_topk_w [N, top_k] fp32).  d_out may be strided by
+    rows (or one row for all, as of a sum); rows that no entry names are left as they were in d_rows."""
+    dev = rows.get_device()
+    if rows.dim() != 2 or tokRow.dim() != 2 or rows.dtype not in DTYPES:
+        raise ValueError("rows must be [rows, D] (float32, float16 or bfloat16), tokRow [N, top_k]")
+    (n, D), (N, k) = rows.shape, tokRow.shape
+    rp = _arg(rows, rows.dtype, (n, D), dev, "rows")
+    gp, gs = _rows_arg(d_out, "d_out", rows.dtype, (N, D), dev)
+    if d_rows is None:
+        d_rows = torch.empty((n, D), dtype=rows.dtype, device=rows.device)
+    dp = _arg(d_rows, rows.dtype, (n, D), dev, "d_rows")
+    d_w = torch.empty((N, k), dtype=torch.float32, device=rows.device)
+    _on(dev, stream, "moe_unsort_tokens_grad", gp, gs, rp, n, DTYPES[rows.dtype],
+        _arg(tokRow, torch.int32, (N, k), dev, "tokRow"), _arg(topk_w, torch.float32, (N, k), dev, "topk_w"), N, k, D,
+        dp, d_w.data_ptr(), *_ws(ws, dev))
+    return d_rows, d_w
+
+
+def moe_topk_grad(logits, topk_idx, d_topk_w, norm_topk_prob, ws, d_logits=None, stream=None):
+    """Gradient of the routing weights (of moe_topk_from_logits) to the router logits: -> d_logits [N, E]."""
+    dev = logits.get_device()
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits must be [N, E], topk_idx [N, top_k]")
+    (N, E), k = logits.shape, topk_idx.shape[1]
+    lp = _arg(logits, torch.float32, (N, E), dev, "logits")
+    if d_logits is None:
+        d_logits = torch.empty((N, E), dtype=torch.float32, device=logits.device)
+    _on(dev, stream, "moe_topk_grad", lp, _arg(topk_idx, torch.int32, (N, k), dev, "topk_idx"),
+        _arg(d_topk_w, torch.float32, (N, k), dev, "d_topk_w"), N, E, k, int(norm_topk_prob),
+        _arg(d_logits, torch.float32, (N, E), dev, "d_logits"), *_ws(ws, dev))
+    return d_logits
+
+
+class MoeW4Weights:
+    """4-bit weights with group scales, laid out for moe_w4_matvec (moe_w4_weights_create / _destroy).
+
+    q uint8 [E, R, K/2] (or [R, K/2]: one matrix), the even column of a byte in its low four bits; scales
+    float16 or bfloat16 [E, R, K/group]; zeros uint8 of that shape, or None (8 everywhere).  With up_q,
+    up_scales (and up_zeros iff zeros) the handle holds gate and up."""
+
+    def __init__(self, q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
+                 up_q: torch.Tensor | None = None, up_scales: torch.Tensor | None = None,
+                 up_zeros: torch.Tensor | None = None, stream=None):
+        self.handle = None
+        if q.dim() == 2:
+            q, scales, zeros, up_q, up_scales, up_zeros = (
+                None if t is None else t.unsqueeze(0) for t in (q, scales, zeros, up_q, up_scales, up_zeros))
+        if q.dim() != 3 or scales.dim() != 3 or scales.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("q must be uint8 [E, R, K/2], scales float16 or bfloat16 [E, R, K/group]")
+        if not q.is_cuda:
+            raise ValueError("q must be a CUDA tensor")
+        self.E, self.R, self.K = q.shape[0], q.shape[1], 2 * q.shape[2]
+        self.pair, self.device = up_q is not None, q.device
+        groups = scales.shape[2]
+        if groups < 1 or self.K % groups:
+            raise ValueError(f"{groups} scales a row do not divide {self.K} columns")
+        self.group = self.K // groups
+        dev, shape = q.get_device(), (self.E, self.R, groups)
+        ptrs = []
+        for names, (a, b, c) in (("q", "scales", "zeros"), (q, scales, zeros)), (
+                ("up_q", "up_scales", "up_zeros"), (up_q, up_scales, up_zeros)):
+            ptrs += [None if a is None else _arg(a, torch.uint8, q.shape, dev, names[0]),
+                     None if b is None else _arg(b, scales.dtype, shape, dev, names[1]),
+                     None if c is None else _arg(c, torch.uint8, shape, dev, names[2])]
+        handle = _P()
+        _on(dev, stream, "moe_w4_weights_create", ctypes.byref(handle), self.E, self.R, self.K, self.group,
+            DTYPES[scales.dtype], *ptrs)
+        self.handle = handle
+
+    @property
+    def device_bytes(self) -> int:
+        return int(lib().moe_w4_weights_device_bytes(self.handle))
+
+    def close(self) -> None:
+        if self.handle is not None and self.handle.value:
+            lib().moe_w4_weights_destroy(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def moe_w4_weights_create(q, scales, zeros=None, up_q=None, up_scales=None, up_zeros=None, stream=None):
+    return MoeW4Weights(q, scales, zeros, up_q, up_scales, up_zeros, stream)
+
+
+def moe_w4_weights_destroy(w: MoeW4Weights) -> None:
+    w.close()
+
+
+def moe_w4_weights_shape(w: MoeW4Weights) -> dict:
+    v = [ctypes.c_int() for _ in range(5)]
+    _check(lib().moe_w4_weights_shape(w.handle, *[ctypes.byref(c) for c in v]), "moe_w4_weights_shape")
+    return dict(zip(("E", "R", "K", "group", "pair"), (c.value for c in v)))
+
+
+def moe_w4_weights_device_bytes(w: MoeW4Weights) -> int:
+    return w.device_bytes
+
+
+def moe_w4_matvec(w: MoeW4Weights, x, expStart, ws, y=None, stream=None):
+    """y [rows, R] = each row of x [rows, K] times its expert's matrix (gate/up handles: SiLU(gate) * up).
+    expStart [E+1] int32 as of moe_sort_tokens, or None for a single matrix; rows from expStart[E] on are
+    left as they were (uninitialised when `y` is not given)."""
+    if w.handle is None:
+        raise ValueError("the weights are closed")
+    dev = w.device.index
+    if x.dim() != 2 or x.shape[1] != w.K:
+        raise ValueError(f"x must have shape [rows, {w.K}], got {tuple(x.shape)}")
+    n = x.shape[0]
+    xp, xs = _rows_arg(x, "x", None, None, dev)
+    sp = None if expStart is None else _arg(expStart, torch.int32, (w.E + 1,), dev, "expStart")
+    if y is None:
+        y = torch.empty((n, w.R), dtype=x.dtype, device=x.device)
+    yp, ys = _rows_arg(y, "y", x.dtype, (n, w.R), dev)
+    _on(dev, stream, "moe_w4_matvec", w.handle, xp, xs, DTYPES[x.dtype], sp, n, yp, ys, *_ws(ws, dev))
+    return y
 
 
 # ------------------------------------------------------------------ layer ---

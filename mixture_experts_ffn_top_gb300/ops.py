@@ -595,34 +595,40 @@ def moe_workspace_views(ws, N, D, E, F, top_k, Fs=0):
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # MOE_DTYPE_*
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(device).cuda_stream, without the object
+
+
 def _on(device: int, stream, name: str, *args) -> None:
     """Call entry point `name` on `stream` (default: the current stream of `device`) with `device` current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = _raw_stream(device)
     elif stream.device_index != device:
         raise ValueError("stream must be of the tensors' device")
+    else:
+        raw = stream.cuda_stream
+    f = getattr(_lib or lib(), name)
     if torch.cuda.current_device() == device:
-        rc = getattr(lib(), name)(*args, stream.cuda_stream)
+        rc = f(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = getattr(lib(), name)(*args, stream.cuda_stream)
+            rc = f(*args, raw)
     if rc != 0:
         raise MoeError(rc, name)
 
 
 def _arg(t: torch.Tensor, dtype, shape, device: int, name: str) -> int:
     """Address of a contiguous CUDA tensor of that type, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0 and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_cuda or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, like the others")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device}, got cuda:{t.get_device()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows_arg(t: torch.Tensor, name: str, dtype=None, shape=None, device: int | None = None) -> tuple[int, int]:

@@ -604,8 +604,8 @@ size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
  *            pass n_rows set MOE_DEV_BAD_CSR and every row is left.
  * fp16 and bf16 rows enter the products as they are, fp32 rows as the exact sum of three
  * bf16 parts; codes less zero points are exact, products are summed in fp32 per group and
- * the groups' sums, times their scales, in fp32 (their order is fixed for given shapes and
- * types); a group's sum of (q - z) x itself has to stay in fp32's range.  Made for few rows an expert (decode): each 32 rows (fp32: 10) of an expert
+ * the groups' sums, times their scales, in fp32 (in an order that the weights' shape and the
+ * type fix: a row's result does not depend on the rows beside it); a group's sum of (q - z) x itself has to stay in fp32's range.  Made for few rows an expert (decode): each 32 rows (fp32: 10) of an expert
  * read its weights once more.
  *   ws: status word (256 bytes). */
 int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype,

@@ -20,7 +20,8 @@ namespace moe {
 namespace {
 
 constexpr int COUNT_THREADS = 256;
-constexpr int ROW_WARPS = 8;  // warps per CTA of the row kernels, a token each
+constexpr int ROW_WARPS = 8;      // warps per CTA of the router gradient, a token each
+constexpr int ROW_THREADS = 256;  // threads per CTA of the row kernels
 
 // ------------------------------------------------------------------ order --
 // Entries of each expert in token range blockIdx.x: table[range][e].
@@ -121,10 +122,11 @@ sort_place_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__re
         const int32_t *p = tokRow + (int64_t)t * top_k;  // this block's own stores above
         const T *src = x + (int64_t)t * x_stride;
         for (int c = lane * V; c < D; c += 32 * V) {
-            const Vec<T, V> v = *reinterpret_cast<const Vec<T, V> *>(src + c);
+            Pack<T, V> v;
+            v.load(src + c);
             for (int s = 0; s < top_k; ++s) {
                 const int r = p[s];
-                if (r >= 0) *reinterpret_cast<Vec<T, V> *>(rows + (int64_t)r * D + c) = v;
+                if (r >= 0) v.store(rows + (int64_t)r * D + c);
             }
         }
     }
@@ -138,73 +140,112 @@ __device__ __forceinline__ int checked_row(int r, int64_t n_rows, unsigned *stat
     return -1;
 }
 
-// out[t] = sum over the slots of w * row (w == NULL: of the row), in slot order; a warp per token.
+// out[t] = sum over the slots of w * row (w == NULL: of the row), in slot order.  Threads 0 .. tpt - 1 of a
+// token's group (tpt a power of two, ROW_THREADS / tpt tokens a CTA) own V consecutive columns each at a
+// time; SLOTS rows are loaded before the first is used.  HBM-bound: 8192 x 2048 bf16, top 8, takes 47.8 us
+// (302 MB: 6.3 TB/s, 93% of the copy rate), 4096 x 2048 fp32 46.8 us (95%).  The entries' rows and weights wait
+// in shared memory: held in registers by every thread they cost 57 us (a third of the warps).
+constexpr int SLOTS = 8;
+
 template <typename T, int V>
-__global__ void __launch_bounds__(ROW_WARPS * 32)
+__global__ void __launch_bounds__(ROW_THREADS, 4)
 unsort_kernel(const T *__restrict__ rows, int64_t n_rows, const int32_t *__restrict__ tokRow,
-              const float *__restrict__ w, int N, int top_k, int D, T *__restrict__ out, int64_t out_stride,
-              unsigned *__restrict__ status) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t t = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); t < N; t += (int64_t)gridDim.x * ROW_WARPS) {
-        int r = -1;
-        float ws = 1.0f;
-        if (lane < top_k) {
-            r = checked_row(tokRow[t * top_k + lane], n_rows, status);
-            if (w != nullptr) ws = w[t * top_k + lane];
-        }
-        for (int c0 = 0; c0 < D; c0 += 32 * V) {
-            const int c = c0 + lane * V;
-            float acc[V];
+              const float *__restrict__ w, int N, int top_k, int D, int tpt_log2, T *__restrict__ out,
+              int64_t out_stride, unsigned *__restrict__ status) {
+    extern __shared__ int2 entry[];  // [tokens of the CTA][top_k]: row (or -1), weight
+    const int tpt = 1 << tpt_log2, per = ROW_THREADS >> tpt_log2;
+    const int64_t t0 = (int64_t)blockIdx.x * per;
+    const int tokens = (int)min((int64_t)per, N - t0);
+    for (int i = threadIdx.x; i < tokens * top_k; i += ROW_THREADS)
+        entry[i] = make_int2(checked_row(tokRow[t0 * top_k + i], n_rows, status),
+                             __float_as_int(w != nullptr ? w[t0 * top_k + i] : 1.0f));
+    __syncthreads();
+    const int mine = threadIdx.x >> tpt_log2;
+    if (mine >= tokens) return;
+    const int2 *en = entry + mine * top_k;
+    T *dst = out + (t0 + mine) * out_stride;
+    for (int64_t c = ((int64_t)blockIdx.y * tpt + (threadIdx.x & (tpt - 1))) * V; c < D;
+         c += (int64_t)gridDim.y * tpt * V) {
+        float acc[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-            for (int s = 0; s < top_k; ++s) {
-                const int rs = __shfl_sync(0xffffffffu, r, s);
-                const float wv = __shfl_sync(0xffffffffu, ws, s);
-                if (rs >= 0 && c < D) {
-                    const Vec<T, V> v = *reinterpret_cast<const Vec<T, V> *>(rows + (int64_t)rs * D + c);
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+        for (int s0 = 0; s0 < top_k; s0 += SLOTS) {
+            Pack<T, V> v[SLOTS];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(wv, elem_f32(v.v[i]), acc[i]);
+            for (int s = 0; s < SLOTS; ++s)
+                if (s0 + s < top_k && en[s0 + s].x >= 0) v[s].load_once(rows + (int64_t)en[s0 + s].x * D + c);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                if (s0 + s < top_k && en[s0 + s].x >= 0) {
+                    const float ws = __int_as_float(en[s0 + s].y);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(ws, v[s].get(i), acc[i]);
                 }
-            }
-            if (c < D) {
-                Vec<T, V> o;
-#pragma unroll
-                for (int i = 0; i < V; ++i) o.v[i] = elem_of<T>(acc[i]);
-                *reinterpret_cast<Vec<T, V> *>(out + t * out_stride + c) = o;
-            }
         }
+        Pack<T, V> o;
+        o.set(acc);
+        o.store(dst + c);
     }
 }
 
-// d_rows of every entry of a token and the dots d_w; a warp per token.
-template <typename T, int V>
-__global__ void __launch_bounds__(ROW_WARPS * 32)
+// d_row = w * d_out and the dot d_w = <d_out, row> of one entry (t, s) at a time, by TPE threads: the rows are
+// read and written once, d_out's row comes from the caches for all but its first entry.  The dot: each thread's
+// columns in order, a butterfly over the warp, the warps in order.  2048 x 2048 bf16, top 8: 25.5 us (143 MB:
+// 83% of the copy rate); a token's threads holding all its entries at once took 35.8 us (registers, and a
+// reduction of eight dots through shared memory).
+template <typename T, int V, int TPE>
+__global__ void __launch_bounds__(ROW_THREADS)
 unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *__restrict__ rows, int64_t n_rows,
-                   const int32_t *__restrict__ tokRow, const float *__restrict__ w, int N, int top_k, int D,
+                   const int32_t *__restrict__ tokRow, const float *__restrict__ w, int n_entries, int top_k, int D,
                    T *__restrict__ d_rows, float *__restrict__ d_w, unsigned *__restrict__ status) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t t = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); t < N; t += (int64_t)gridDim.x * ROW_WARPS) {
-        const T *src = d_out + t * d_out_stride;
-        for (int s = 0; s < top_k; ++s) {
-            const int r = checked_row(tokRow[t * top_k + s], n_rows, status);
-            float dot = 0.0f;
-            if (r >= 0) {
-                const float ws = w[t * top_k + s];
-                for (int c = lane * V; c < D; c += 32 * V) {
-                    const Vec<T, V> dv = *reinterpret_cast<const Vec<T, V> *>(src + c);
-                    const Vec<T, V> rv = *reinterpret_cast<const Vec<T, V> *>(rows + (int64_t)r * D + c);
-                    Vec<T, V> o;
+    constexpr int UNROLL = 4;
+    __shared__ float part[ROW_THREADS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * (ROW_THREADS / TPE) + threadIdx.x / TPE;
+    if (i >= n_entries) return;  // whole warps; whole CTAs where TPE is the CTA
+    const int r = checked_row(tokRow[i], n_rows, status);
+    float dot = 0.0f;
+    if (r >= 0) {
+        const float ws = w[i];
+        const T *src = d_out + (i / top_k) * d_out_stride, *row = rows + (int64_t)r * D;
+        T *dst = d_rows + (int64_t)r * D;
+        for (int c0 = (threadIdx.x & (TPE - 1)) * V; c0 < D; c0 += UNROLL * TPE * V) {
+            Pack<T, V> dv[UNROLL], rv[UNROLL];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float d = elem_f32(dv.v[i]);
-                        dot = __fmaf_rn(d, elem_f32(rv.v[i]), dot);
-                        o.v[i] = elem_of<T>(__fmul_rn(ws, d));
-                    }
-                    *reinterpret_cast<Vec<T, V> *>(d_rows + (int64_t)r * D + c) = o;
+            for (int u = 0; u < UNROLL; ++u) {
+                const int c = c0 + u * TPE * V;
+                if (c < D) {
+                    rv[u].load_once(row + c);
+                    dv[u].load(src + c);
                 }
             }
-            dot = warp_sum(dot);
-            if (lane == 0) d_w[t * top_k + s] = dot;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int c = c0 + u * TPE * V;
+                if (c < D) {
+                    Pack<T, V> o;
+                    float f[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        dot = __fmaf_rn(dv[u].get(j), rv[u].get(j), dot);
+                        f[j] = __fmul_rn(ws, dv[u].get(j));
+                    }
+                    o.set(f);
+                    o.store(dst + c);
+                }
+            }
+        }
+    }
+    dot = warp_sum(dot);
+    if (TPE == 32) {
+        if (lane == 0) d_w[i] = dot;
+    } else {
+        if (lane == 0) part[warp] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int k = 1; k < TPE / 32; ++k) dot += part[k];
+            d_w[i] = dot;
         }
     }
 }
@@ -282,14 +323,28 @@ topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ i
     }
 }
 
-// Elements per access: 16 bytes when every address is a multiple of that, else the element alone.
-template <typename T>
-bool wide(std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> strides) {
-    for (const void *p : ptrs)
-        if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
-    for (int64_t st : strides)
-        if (st * (int64_t)sizeof(T) % 16 != 0) return false;
-    return true;
+// Bytes per access: the largest of 16, 8, 4 and 2 that divides every address and row stride.
+int access_bytes(std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> stride_bytes) {
+    uint64_t bits = 16;
+    for (const void *p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
+    for (int64_t st : stride_bytes) bits |= (uint64_t)st;
+    return (int)(bits & -bits);
+}
+
+// Calls f with the elements per access as a constant.
+template <typename T, typename F>
+int by_width(int bytes, F f) {
+    constexpr int E = sizeof(T);
+    if (bytes >= 16) return f(std::integral_constant<int, 16 / E>());
+    if (bytes >= 8) return f(std::integral_constant<int, 8 / E>());
+    if (bytes >= 4) return f(std::integral_constant<int, 4 / E>());
+    return f(std::integral_constant<int, 1>());
+}
+
+int log2_ceil(int64_t n, int most) {
+    int l = 0;
+    while (l < most && ((int64_t)1 << l) < n) ++l;
+    return l;
 }
 
 unsigned row_grid(int64_t N) {
@@ -336,40 +391,58 @@ int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t
                                                         static_cast<T *>(rows));
             return launch_status();
         };
-        constexpr int V = 16 / sizeof(T);
-        if (wide<T>({x, rows}, {x_stride, D})) return go(sort_place_kernel<T, V>);
-        return go(sort_place_kernel<T, 1>);
+        const int b = access_bytes({x, rows}, {x_stride * (int64_t)sizeof(T), D * (int64_t)sizeof(T)});
+        return by_width<T>(b, [&](auto v) { return go(sort_place_kernel<T, decltype(v)::value>); });
     });
 }
 
 int launch_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t *tokRow, const float *w, int N,
                          int top_k, int D, void *out, int64_t out_stride, unsigned *status, cudaStream_t s) {
+    const int sms = std::max(1, device_sm_count());
     return by_dtype(dtype, [&](auto *tp) {
         using T = std::remove_pointer_t<decltype(tp)>;
-        auto go = [&](auto kernel) {
-            kernel<<<row_grid(N), ROW_WARPS * 32, 0, s>>>(static_cast<const T *>(rows), n_rows, tokRow, w, N, top_k, D,
-                                                          static_cast<T *>(out), out_stride, status);
+        const int b = access_bytes({rows, out}, {D * (int64_t)sizeof(T), out_stride * (int64_t)sizeof(T)});
+        return by_width<T>(b, [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            const int64_t cols = (D + V - 1) / V;
+            // One access a thread until every SM has 2048 of them, then two, or four where they are narrow: 8192 x
+            // 2048 bf16 at 16 bytes measured 49.8 / 47.8 / 49.2 us with 1 / 2 / 4, 13620 x 373 fp16 at 2 bytes
+            // 45.9 / 39.1 / 35.0 us.
+            const int64_t most = sizeof(T) * V == 16 ? 2 : 4;
+            int64_t reps = 1;
+            while (reps < most && N * cols / (2 * reps) >= (int64_t)sms * 2048) reps *= 2;
+            const int tl = std::max(log2_ceil((cols + reps - 1) / reps, 8), 3);
+            const int per = ROW_THREADS >> tl;
+            const int64_t cta_cols = ((int64_t)1 << tl) * reps;
+            const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)std::min<int64_t>((cols + cta_cols - 1) / cta_cols, 65535));
+            unsort_kernel<T, V><<<grid, ROW_THREADS, (size_t)per * top_k * sizeof(int2), s>>>(static_cast<const T *>(rows), n_rows, tokRow, w, N, top_k,
+                                                             D, tl, static_cast<T *>(out), out_stride, status);
             return launch_status();
-        };
-        constexpr int V = 16 / sizeof(T);
-        return wide<T>({rows, out}, {D, out_stride}) ? go(unsort_kernel<T, V>) : go(unsort_kernel<T, 1>);
+        });
     });
 }
 
 int launch_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const void *rows, int64_t n_rows, int dtype,
                               const int32_t *tokRow, const float *w, int N, int top_k, int D, void *d_rows, float *d_w,
                               unsigned *status, cudaStream_t s) {
+    const int sms = std::max(1, device_sm_count());
     return by_dtype(dtype, [&](auto *tp) {
         using T = std::remove_pointer_t<decltype(tp)>;
-        auto go = [&](auto kernel) {
-            kernel<<<row_grid(N), ROW_WARPS * 32, 0, s>>>(static_cast<const T *>(d_out), d_out_stride,
-                                                          static_cast<const T *>(rows), n_rows, tokRow, w, N, top_k, D,
-                                                          static_cast<T *>(d_rows), d_w, status);
-            return launch_status();
-        };
-        constexpr int V = 16 / sizeof(T);
-        return wide<T>({d_out, rows, d_rows}, {d_out_stride, D}) ? go(unsort_grad_kernel<T, V>)
-                                                                 : go(unsort_grad_kernel<T, 1>);
+        const int b = access_bytes({d_out, rows, d_rows}, {d_out_stride * (int64_t)sizeof(T), D * (int64_t)sizeof(T)});
+        return by_width<T>(b, [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            const int64_t cols = (D + V - 1) / V;
+            const int64_t n = (int64_t)N * top_k;
+            auto go = [&](auto kernel, int per) {
+                kernel<<<(unsigned)((n + per - 1) / per), ROW_THREADS, 0, s>>>(
+                    static_cast<const T *>(d_out), d_out_stride, static_cast<const T *>(rows), n_rows, tokRow, w,
+                    (int)n, top_k, D, static_cast<T *>(d_rows), d_w, status);
+                return launch_status();
+            };
+            // a warp an entry, or a CTA where the entries are few and their rows long
+            if (n < (int64_t)sms * 8 && cols > 64) return go(unsort_grad_kernel<T, V, ROW_THREADS>, 1);
+            return go(unsort_grad_kernel<T, V, 32>, ROW_THREADS / 32);
+        });
     });
 }
 

@@ -14,120 +14,322 @@
 #include <type_traits>
 
 #include "elem.cuh"
+#include "tc_glue.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int COUNT_THREADS = 256;
+constexpr int COUNT_THREADS = 512;
 constexpr int ROW_WARPS = 8;      // warps per CTA of the router gradient, a token each
 constexpr int ROW_THREADS = 256;  // threads per CTA of the row kernels
 
 // ------------------------------------------------------------------ order --
+// The tokens are split into ranges, one per CTA.  A range's first rows follow from the entries of each expert
+// before it and in all: counted by every CTA itself where the entries are few (SORT_ONE_PASS), else taken from
+// the table that sort_count_kernel leaves (summed over the ranges before by sort_scan_kernel where E is large).
+constexpr int SORT_THREADS = 512;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_RANGES = 152;          // at most: a CTA per SM
+constexpr int SORT_ONE_PASS = 4096;       // entries that every CTA counts by itself: 7.1 us, by the table 8.1
+constexpr int SORT_SCAN_E = 256;          // experts from which the table is summed by a kernel of its own: 2048
+                                          // tokens over 1024 experts 19 us, summed by every CTA 55
+constexpr int SORT_RING = 12 * 1024;      // shared memory of a warp's rows in flight
+constexpr int SORT_SLOTS = 4;             // at most this many of them
+constexpr int SORT_POS = 2048;            // entries of a range whose rows wait in shared memory
+constexpr unsigned long long SORT_WAIT_NS = 2000000000ull;
+
+// f(i, idx[i]) for the entries lo .. hi - 1, four loads of a thread in flight.
+template <int THREADS, typename F>
+__device__ __forceinline__ void for_entries(const int32_t *__restrict__ idx, int lo, int hi, F f) {
+    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += 4 * THREADS) {
+        int e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[q] = i0 + q * THREADS < hi ? idx[i0 + q * THREADS] : -1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (i0 + q * THREADS < hi) f(i0 + q * THREADS, e[q]);
+    }
+}
+
 // Entries of each expert in token range blockIdx.x: table[range][e].
 __global__ void __launch_bounds__(COUNT_THREADS)
 sort_count_kernel(const int32_t *__restrict__ idx, int n_entries, int per_range, int E, int *__restrict__ table,
                   unsigned *__restrict__ status) {
+    // the row kernel may be scheduled now (it waits for this grid before it reads the table)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ int hist[];
     for (int e = threadIdx.x; e < E; e += COUNT_THREADS) hist[e] = 0;
     __syncthreads();
     const int lo = blockIdx.x * per_range, hi = min(lo + per_range, n_entries);
-    for (int i = lo + threadIdx.x; i < hi; i += COUNT_THREADS) {
-        const int e = idx[i];
+    for_entries<COUNT_THREADS>(idx, lo, hi, [&](int, int e) {
         if (e >= 0 && e < E)
             atomicAdd(&hist[e], 1);
         else if (e != -1)
             atomicOr(status, MOE_DEV_BAD_ROUTING);
-    }
+    });
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += COUNT_THREADS) table[(size_t)blockIdx.x * E + e] = hist[e];
 }
 
-// Row of every entry of range blockIdx.x, the CSR arrays, and the rows themselves.
-template <typename T, int V>
-__global__ void __launch_bounds__(ROW_WARPS * 32)
-sort_place_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ idx, int n_entries,
-                  int per_range, int top_k, int E, int D, const int *__restrict__ table, int n_ranges,
-                  int32_t *__restrict__ expStart, int32_t *__restrict__ expTokI, int32_t *__restrict__ expTokK,
-                  int32_t *tokRow, T *__restrict__ rows) {
-    extern __shared__ int sm[];
-    int *base = sm;           // [E]: next row of each expert for this range
-    int *total = sm + E;      // [E]: entries of each expert
-    __shared__ int kept_s;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int NT = ROW_WARPS * 32;
-    for (int e = tid; e < E; e += NT) {
-        int before = 0, all = 0;
-        for (int g = 0; g < n_ranges; ++g) {
-            const int c = table[(size_t)g * E + e];
-            before += g < (int)blockIdx.x ? c : 0;
-            all += c;
-        }
-        base[e] = before;
-        total[e] = all;
-    }
-    __syncthreads();
-    const int lo = blockIdx.x * per_range, hi = min(lo + per_range, n_entries);
-    if (warp == 0) {
-        // exclusive scan of the totals: expert e's segment start
-        int run = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            const int c = e < E ? total[e] : 0;
-            int inc = c;
+// The table's columns summed exclusively over the ranges, in place; row n_ranges receives the totals.  A warp
+// an expert: neighbouring lanes take neighbouring ranges.
+__global__ void __launch_bounds__(COUNT_THREADS) sort_scan_kernel(int *table, int n_ranges, int E) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, e = blockIdx.x * (COUNT_THREADS / 32) + (threadIdx.x >> 5);
+    if (e >= E) return;
+    constexpr int STEPS = (SORT_RANGES + 31) / 32;
+    int c[STEPS], run = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            if (e < E) {
-                base[e] += run + inc - c;
-                if (blockIdx.x == 0) expStart[e] = run + inc - c;
-            }
-            run += __shfl_sync(0xffffffffu, inc, 31);
+    for (int i = 0; i < STEPS; ++i) c[i] = i * 32 + lane < n_ranges ? table[(size_t)(i * 32 + lane) * E + e] : 0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        int inc = c[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
         }
+        if (i * 32 + lane < n_ranges) table[(size_t)(i * 32 + lane) * E + e] = run + inc - c[i];
+        run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) table[(size_t)n_ranges * E + e] = run;
+}
+
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// How a range's counts are known.
+enum SortCounts { COUNT_HERE, COUNT_TABLE, COUNT_SCANNED };
+
+// Row of every entry of token range blockIdx.x and the CSR arrays.  BULK: the rows as well, in pieces through
+// shared memory by bulk copies, one load and top_k stores each, the first loads issued before the order is
+// known; a warp has `slots` pieces of at most `piece` bytes in flight.  The stores' bytes bound it past some
+// 4 us for the order: 2048 x 2048 bf16, top 8 of 64, 17.0 us (76 MB: 66% of the copy rate), 16384 tokens
+// 106.5 us (84%; rows that lie apart cost the writes some of it, a plain scatter of such rows with the order
+// given takes 104 us).  Rows read by the sorted order instead measured 125 - 155 us there (x eight times
+// from L2).
+template <bool BULK, SortCounts COUNTS>
+__global__ void __launch_bounds__(SORT_THREADS)
+sort_rows_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ idx, int n_entries,
+                 int tokens, int top_k, int E, int row_bytes, const int *table, int32_t *__restrict__ expStart,
+                 int32_t *__restrict__ expTokI, int32_t *__restrict__ expTokK, int32_t *tokRow,
+                 char *__restrict__ rows, int piece, int slots, int ring, unsigned *__restrict__ status) {
+    // the copying kernel, if there is one, may be scheduled now
+    if (!BULK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ __align__(128) char smem[];
+    __shared__ int wsum[SORT_WARPS];
+    __shared__ int kept_s, abort_s, pos_s[SORT_POS];
+    __shared__ __align__(8) uint64_t bars[SORT_WARPS * SORT_SLOTS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *before = reinterpret_cast<int *>(smem + (BULK ? SORT_WARPS * ring : 0));  // [E]
+    int *rest = before + E;                                                       // [E]
+    int *seen = rest + E;  // [warps][E]: entries of each expert in a warp's share of the range, then their first row
+    const int N = n_entries / top_k, t0 = blockIdx.x * tokens, t1 = min(t0 + tokens, N);
+    const int lo = t0 * top_k, hi = t1 * top_k;
+    const int pieces = BULK ? (row_bytes + piece - 1) / piece : 1;
+    // this warp's units: token t0 + (u / pieces) * SORT_WARPS + warp, piece u % pieces
+    const int units = BULK ? (t1 - t0 > warp ? (t1 - t0 - warp + SORT_WARPS - 1) / SORT_WARPS : 0) * pieces : 0;
+    auto unit_bytes = [&](int u) { return min(piece, row_bytes - (u % pieces) * piece); };
+    auto load_unit = [&](int u) {
+        const uint32_t bar = tc::smem_u32(&bars[warp * SORT_SLOTS + u % slots]);
+        const int64_t t = t0 + (u / pieces) * SORT_WARPS + warp;
+        const int bytes = unit_bytes(u);
+        tc::mbar_expect_tx(bar, bytes);
+        tc::bulk_load(tc::smem_u32(smem + warp * ring + (u % slots) * piece),
+                      x + t * x_stride + (int64_t)(u % pieces) * piece, bytes, bar);
+    };
+    if (BULK) {
         if (lane == 0) {
-            kept_s = run;
-            if (blockIdx.x == 0) expStart[E] = run;
+            for (int i = 0; i < slots; ++i) tc::mbar_init(tc::smem_u32(&bars[warp * SORT_SLOTS + i]), 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            for (int u = 0; u < min(units, slots); ++u) load_unit(u);
         }
         __syncwarp();
-        // rank of each entry among the earlier ones of its expert, 32 entries at a time
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const int i = i0 + lane;
-            int e = i < hi ? idx[i] : -1;
-            if (e < 0 || e >= E) e = -1;
-            const unsigned same = __match_any_sync(0xffffffffu, e);
-            int r = -1;
-            if (e >= 0) r = base[e] + __popc(same & ((1u << lane) - 1));
-            __syncwarp();
-            if (e >= 0 && lane == __ffs(same) - 1) base[e] += __popc(same);
-            __syncwarp();
-            if (i < hi) {
-                tokRow[i] = r;
-                if (r >= 0) {
-                    expTokI[r] = i / top_k;
-                    expTokK[r] = i % top_k;
+    }
+    // a warp's share of the range: a multiple of 32 entries
+    const int share = ((hi - lo + SORT_WARPS - 1) / SORT_WARPS + 31) / 32 * 32, shares = (hi - lo + share - 1) / share;
+    const int my_lo = min(lo + warp * share, hi), my_hi = min(my_lo + share, hi);
+    int *mine = seen + warp * E;
+    // the entries' ranks, then rows: in shared memory, or where a range has too many in tokRow itself
+    int *pos = hi - lo <= SORT_POS ? pos_s : tokRow + lo;
+    if (tid == 0) abort_s = 0;
+    for (int e = tid; e < (2 + shares) * E; e += SORT_THREADS) before[e] = 0;
+    __syncthreads();
+    // rank of each entry among the earlier ones of its expert in this warp's share, 32 at a time
+    for (int i0 = my_lo; i0 < my_hi; i0 += 32) {
+        const int i = i0 + lane;
+        int e = i < my_hi ? idx[i] : -1;
+        if (e < 0 || e >= E) e = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int r = -1;
+        if (e >= 0) r = mine[e] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+        if (i < my_hi) pos[i - lo] = r;
+    }
+    if (COUNTS == COUNT_HERE) {
+        for_entries<SORT_THREADS>(idx, 0, n_entries, [&](int i, int e) {
+            if (e >= 0 && e < E)
+                atomicAdd(i < lo ? &before[e] : &rest[e], 1);
+            else if (e != -1 && i >= lo && i < hi)
+                atomicOr(status, MOE_DEV_BAD_ROUTING);
+        });
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (COUNTS == COUNT_SCANNED) {
+            for (int e = tid; e < E; e += SORT_THREADS) {
+                const int a = table[(size_t)blockIdx.x * E + e];
+                before[e] = a;
+                rest[e] = table[(size_t)gridDim.x * E + e] - a;
+            }
+        } else {
+            // a thread sums every `ways`-th range's count of its expert, 16 loads in flight
+            const int ways = max(1, SORT_THREADS / E), n = gridDim.x;
+            for (int j = tid; j < ways * E; j += SORT_THREADS) {
+                const int e = j % E;
+                int a = 0, b = 0;
+                for (int g0 = j / E; g0 < n; g0 += 16 * ways) {
+                    int c[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) c[q] = g0 + q * ways < n ? table[(size_t)(g0 + q * ways) * E + e] : 0;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (g0 + q * ways < (int)blockIdx.x)
+                            a += c[q];
+                        else
+                            b += c[q];
                 }
+                atomicAdd(&before[e], a);
+                atomicAdd(&rest[e], b);
             }
         }
     }
     __syncthreads();
+    // exclusive scan of the totals (two experts a thread): each expert's first row, then each share's
+    {
+        const int e = 2 * tid;
+        const int b0 = e < E ? before[e] : 0, b1 = e + 1 < E ? before[e + 1] : 0;
+        const int c0 = e < E ? b0 + rest[e] : 0, c1 = e + 1 < E ? b1 + rest[e + 1] : 0;
+        int inc = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int run = inc - c0 - c1, all = 0;
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            if (w < warp) run += wsum[w];
+            all += wsum[w];
+        }
+        if (blockIdx.x == 0) {
+            if (e < E) expStart[e] = run;
+            if (e + 1 < E) expStart[e + 1] = run + c0;
+            if (tid == 0) expStart[E] = all;
+        }
+        if (tid == 0) kept_s = all;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (e + h >= E) break;
+            int at = h ? run + c0 + b1 : run + b0;
+            for (int w = 0; w < shares; ++w) {
+                const int c = seen[w * E + e + h];
+                seen[w * E + e + h] = at;
+                at += c;
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = my_lo + lane; i < my_hi; i += 32) {
+        int r = pos[i - lo];
+        if (r >= 0) {
+            r += mine[idx[i]];
+            expTokI[r] = i / top_k;
+            expTokK[r] = i % top_k;
+        }
+        tokRow[i] = r;
+        pos[i - lo] = r;
+    }
     // CSR entries past the last row: every range clears its own positions among them
-    for (int i = max(lo, kept_s) + tid; i < hi; i += NT) {
+    for (int i = max(lo, kept_s) + tid; i < hi; i += SORT_THREADS) {
         expTokI[i] = -1;
         expTokK[i] = -1;
     }
-    const int t0 = lo / top_k, t1 = hi / top_k;
-    for (int t = t0 + warp; t < t1; t += ROW_WARPS) {
-        const int32_t *p = tokRow + (int64_t)t * top_k;  // this block's own stores above
-        const T *src = x + (int64_t)t * x_stride;
-        for (int c = lane * V; c < D; c += 32 * V) {
-            Pack<T, V> v;
-            v.load(src + c);
-            for (int s = 0; s < top_k; ++s) {
-                const int r = p[s];
-                if (r >= 0) v.store(rows + (int64_t)r * D + c);
+    if (BULK) {
+        __syncthreads();
+        int u = 0;
+        for (; u < units; ++u) {
+            const int slot = u % slots;
+            const uint32_t bar = tc::smem_u32(&bars[warp * SORT_SLOTS + slot]);
+            const int t = (u / pieces) * SORT_WARPS + warp;
+            const int r = lane < top_k ? pos[t * top_k + lane] : -1;
+            const bool here = tc::mbar_wait(bar, (u / slots) & 1, &abort_s, status, SORT_WAIT_NS);
+            if (!__all_sync(0xffffffffu, here)) break;  // a copy that never came: flagged, its rows are left
+            if (r >= 0)
+                bulk_store(rows + (int64_t)r * row_bytes + (int64_t)(u % pieces) * piece,
+                           tc::smem_u32(smem + warp * ring + slot * piece), unit_bytes(u));
+            bulk_commit();
+            if (u > 0 && u - 1 + slots < units) {  // the unit before has been read: its slot takes another
+                bulk_wait_read<1>();
+                __syncwarp();
+                if (lane == 0) load_unit(u - 1 + slots);
             }
+        }
+        // after a timeout: the loads still in flight, with a limit again
+        for (int p = u; p < min(units, u + slots - (u > 0)); ++p) {
+            const uint64_t since = tc::globaltimer();
+            while (!tc::mbar_try(tc::smem_u32(&bars[warp * SORT_SLOTS + p % slots]), (p / slots) & 1) &&
+                   tc::globaltimer() - since < SORT_WAIT_NS) {
+            }
+        }
+        bulk_wait_read<0>();
+    }
+}
+
+// rows[tokRow[t,s]] = x[t] in accesses of B bytes, for rows that bulk copies cannot take (a length, stride or
+// address that 16 bytes do not divide): threads as in unsort_kernel.  4096 x 1001 bf16, top 8: 30 us.
+template <int B>
+__global__ void __launch_bounds__(ROW_THREADS)
+sort_copy_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *tokRow, int N, int top_k, int row_bytes,
+                 int tpt_log2, char *__restrict__ rows) {
+    using A = std::conditional_t<B == 16, uint4,
+                                 std::conditional_t<B == 8, uint2, std::conditional_t<B == 4, uint32_t, uint16_t>>>;
+    extern __shared__ int row_s[];  // [tokens of the CTA][top_k]
+    const int tpt = 1 << tpt_log2, per = ROW_THREADS >> tpt_log2;
+    const int64_t t0 = (int64_t)blockIdx.x * per;
+    const int n = (int)min((int64_t)per, N - t0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i < n * top_k; i += ROW_THREADS) row_s[i] = tokRow[t0 * top_k + i];
+    __syncthreads();
+    const int mine = threadIdx.x >> tpt_log2;
+    if (mine >= n) return;
+    const char *src = x + (t0 + mine) * x_stride;
+    constexpr int UNROLL = 4;
+    const int64_t step = (int64_t)gridDim.y * tpt * B;
+    for (int64_t c0 = ((int64_t)blockIdx.y * tpt + (threadIdx.x & (tpt - 1))) * B; c0 < row_bytes; c0 += UNROLL * step) {
+        A v[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (c0 + u * step < row_bytes) v[u] = *reinterpret_cast<const A *>(src + c0 + u * step);
+        for (int s = 0; s < top_k; ++s) {
+            const int r = row_s[mine * top_k + s];
+            if (r < 0) continue;
+            char *dst = rows + (int64_t)r * row_bytes + c0;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+                if (c0 + u * step < row_bytes) *reinterpret_cast<A *>(dst + u * step) = v[u];
         }
     }
 }
@@ -365,35 +567,82 @@ int by_dtype(int dtype, F f) {
 }  // namespace
 
 int sort_ranges(int N, int *tokens) {
-    const int sms = 152;  // ranges of a fixed number, so that the workspace's size is the shape's alone
-    const int per = (N + sms - 1) / sms;
+    // a number that does not depend on the device, so that the workspace's size is the shape's alone
+    const int per = (N + SORT_RANGES - 1) / SORT_RANGES;
     if (tokens) *tokens = per;
     return (N + per - 1) / per;
 }
 
-size_t sort_scratch_bytes(int N, int E) { return (size_t)sort_ranges(N, nullptr) * E * 4; }
+// the ranges' counts and the totals
+size_t sort_scratch_bytes(int N, int E) { return (size_t)(sort_ranges(N, nullptr) + 1) * E * 4; }
 
 int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *idx, int N, int top_k, int E, int D,
                        int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows, void *ws,
                        cudaStream_t s) {
     int tokens = 0;
     const int ranges = sort_ranges(N, &tokens);
-    const int n = N * top_k, per = tokens * top_k;
+    const int n = N * top_k;
     int *table = ws_ptr<int>(ws, SORT_SCRATCH_OFFSET);
     unsigned *status = static_cast<unsigned *>(ws);
-    sort_count_kernel<<<ranges, COUNT_THREADS, (size_t)E * 4, s>>>(idx, n, per, E, table, status);
-    const size_t smem = (size_t)2 * E * 4;
-    return by_dtype(dtype, [&](auto *tp) {
-        using T = std::remove_pointer_t<decltype(tp)>;
-        auto go = [&](auto kernel) {  // E <= 1024: at most 8 KB of shared memory
-            kernel<<<ranges, ROW_WARPS * 32, smem, s>>>(static_cast<const T *>(x), x_stride, idx, n, per, top_k, E, D,
-                                                        table, ranges, expStart, expTokI, expTokK, tokRow,
-                                                        static_cast<T *>(rows));
-            return launch_status();
-        };
-        const int b = access_bytes({x, rows}, {x_stride * (int64_t)sizeof(T), D * (int64_t)sizeof(T)});
-        return by_width<T>(b, [&](auto v) { return go(sort_place_kernel<T, decltype(v)::value>); });
-    });
+    const int eb = (int)dtype_bytes(dtype), row_bytes = D * eb;
+    const int64_t xb = x_stride * eb;
+    const int width = access_bytes({x, rows}, {xb, row_bytes});
+    const bool bulk = width == 16;
+    // shared memory: the experts' counts, and the rest (at most SORT_RING a warp) for pieces of rows, as few as
+    // the ring holds at two a warp, of equal size
+    const int shares = std::min(SORT_WARPS, (tokens * top_k + 31) / 32);
+    const int counts = (2 + shares) * E * 4;
+    const int ring = std::min(SORT_RING, (216 * 1024 - counts) / SORT_WARPS / 256 * 256);
+    const int np = (row_bytes + ring / 2 - 1) / (ring / 2);
+    const int piece = ((row_bytes + np - 1) / np + 15) / 16 * 16;
+    const int slots = std::min(SORT_SLOTS, ring / piece);
+    const size_t smem = (size_t)counts + (bulk ? SORT_WARPS * ring : 0);
+    const int how = n <= SORT_ONE_PASS ? COUNT_HERE : E < SORT_SCAN_E ? COUNT_TABLE : COUNT_SCANNED;
+    if (how != COUNT_HERE) {
+        sort_count_kernel<<<ranges, COUNT_THREADS, (size_t)E * 4, s>>>(idx, n, tokens * top_k, E, table, status);
+        int rc = launch_status();
+        if (!rc && how == COUNT_SCANNED)
+            rc = launch_early(sort_scan_kernel, dim3((E + COUNT_THREADS / 32 - 1) / (COUNT_THREADS / 32)),
+                              dim3(COUNT_THREADS), 0, s, table, ranges, E);
+        if (rc) return rc;
+    }
+    const char *xc = static_cast<const char *>(x);
+    char *out = static_cast<char *>(rows);
+    auto go = [&](auto kernel, SmemOptIn *done) {
+        int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, done);
+        if (rc) return rc;
+        if (how != COUNT_HERE)
+            return launch_early(kernel, dim3(ranges), dim3(SORT_THREADS), smem, s, xc, xb, idx, n, tokens, top_k, E,
+                                row_bytes, table, expStart, expTokI, expTokK, tokRow, out, piece, slots, ring, status);
+        kernel<<<ranges, SORT_THREADS, smem, s>>>(xc, xb, idx, n, tokens, top_k, E, row_bytes, table, expStart, expTokI,
+                                                  expTokK, tokRow, out, piece, slots, ring, status);
+        return launch_status();
+    };
+    auto by_counts = [&](auto bc) {
+        constexpr bool B = decltype(bc)::value;
+        static SmemOptIn d[3];
+        if (how == COUNT_HERE) return go(sort_rows_kernel<B, COUNT_HERE>, &d[0]);
+        if (how == COUNT_TABLE) return go(sort_rows_kernel<B, COUNT_TABLE>, &d[1]);
+        return go(sort_rows_kernel<B, COUNT_SCANNED>, &d[2]);
+    };
+    if (bulk) return by_counts(std::true_type());
+    const int rc = by_counts(std::false_type());
+    if (rc) return rc;
+    auto copy = [&](auto bc) {
+        constexpr int B = decltype(bc)::value;
+        const int64_t cols = row_bytes / B;
+        const int tl = std::max(log2_ceil((cols + 3) / 4, 8), 3), per = ROW_THREADS >> tl;
+        const int64_t cta_cols = (int64_t)4 << tl;
+        const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)std::min<int64_t>((cols + cta_cols - 1) / cta_cols, 65535));
+        return launch_early(sort_copy_kernel<B>, grid, dim3(ROW_THREADS), (size_t)per * top_k * 4, s, xc, xb, tokRow, N,
+                            top_k, row_bytes, tl, out);
+    };
+    switch (width) {
+        case 16: return copy(std::integral_constant<int, 16>());
+        case 8: return copy(std::integral_constant<int, 8>());
+        case 4: return copy(std::integral_constant<int, 4>());
+        default: return copy(std::integral_constant<int, 2>());
+    }
 }
 
 int launch_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t *tokRow, const float *w, int N,

@@ -871,7 +871,7 @@ int moe_w4_weights_create(moe_w4_weights_t *out, int E, int R, int K, int group,
 
 int moe_w4_weights_destroy(moe_w4_weights_t w) {
     if (!w) return MOE_ERR_INVALID_ARG;
-    if (w->codes) cudaFree(w->codes);
+    if (w->records) cudaFree(w->records);
     delete w;
     return MOE_OK;
 }

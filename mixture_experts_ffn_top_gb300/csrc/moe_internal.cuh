@@ -68,8 +68,8 @@ struct moe_w4_weights_s {
     int ntiles = 0, nchunk = 0;  // tiles of 16 weight rows per expert, chunks of 128 columns
     int device = -1;
     size_t bytes = 0;
-    char *codes = nullptr;      // the device allocation; scales and zeros lie in it
-    char *scales = nullptr, *zeros = nullptr;
+    char *records = nullptr;    // the device allocation
+    bool zeros = false;         // the records hold zero points
 };
 
 namespace moe {

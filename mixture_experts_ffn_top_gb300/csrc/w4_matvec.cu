@@ -21,7 +21,7 @@
 // chunks of 128 columns, a record each: 1 KB of codes in the order the lanes hold them -- lane (g, t) =
 // (lane / 4, lane % 4) has row g's 16 bytes at 16 * lane and row g + 8's at 512 + 16 * lane, word b of them
 // holding columns 32 b + 8 t .. + 7 of the chunk, pair j of those 8 in bits 4j and 16 + 4j -- then the scales
-// (16 bits) and the zero points (8 bits, if any) as [g][row g, row g + 8][groups of the chunk].
+// (16 bits) and the zero points (if any, twice in 8 bits) as [g][row g, row g + 8][groups of the chunk].
 #include <algorithm>
 #include <new>
 
@@ -32,8 +32,9 @@ namespace moe {
 namespace {
 
 constexpr int W4_WARPS = 16;                   // at most; a CTA has 8 or 16
+constexpr int W4_SLOTS = 3;                    // pairs of records in a warp's ring
 constexpr int W4_CHUNK = 128;                  // columns of a chunk
-constexpr int W4_XPAD = 32;                    // staged rows lie 64 bytes past a multiple of 128: no bank conflicts
+constexpr int W4_XPAD = 64;                    // bytes past a multiple of 128 that staged rows lie apart: no bank conflicts
 constexpr size_t W4_SMEM_SM = 227 * 1024;      // shared memory of an SM's CTAs, less 1 KB each
 
 __host__ __device__ constexpr int w4_record(int group, bool zeros) { return 1024 + (zeros ? 48 : 32) * (W4_CHUNK / group); }
@@ -84,7 +85,7 @@ __global__ void w4_repack_kernel(const uint8_t *__restrict__ q, const uint16_t *
         } else {
             const int64_t at = (e * R + row) * (int64_t)ng + k0 / group;
             reinterpret_cast<uint16_t *>(dst + 1024)[in] = there ? (up ? usc : sc)[at] : (uint16_t)0;
-            if (zp) reinterpret_cast<uint8_t *>(dst + 1024 + 32 * nb)[in] = there ? (up ? uzp : zp)[at] & 15 : 0;
+            if (zp) reinterpret_cast<uint8_t *>(dst + 1024 + 32 * nb)[in] = there ? (uint8_t)(((up ? uzp : zp)[at] & 15) * 17) : (uint8_t)0;
         }
     }
 }
@@ -160,30 +161,6 @@ struct W4Args {
     unsigned *status;
 };
 
-// Eight values of row x from column k on (zero past K), as fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T *src, int k, int K, bool wide, float (&v)[8]) {
-    if (wide && k + 8 <= K) {
-#pragma unroll
-        for (int h = 0; h < 8; h += 16 / sizeof(T)) {
-            Pack<T, 16 / sizeof(T)> p;
-            p.load(src + k + h);
-#pragma unroll
-            for (int q = 0; q < 16 / (int)sizeof(T); ++q) v[h + q] = p.get(q);
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            Pack<T, 1> p;
-            v[q] = 0.0f;
-            if (k + q < K) {
-                p.load(src + k + q);
-                v[q] = p.get(0);
-            }
-        }
-    }
-}
-
 __device__ __forceinline__ float exp2_int(int e) {  // 2^e, e in [-149, 127]
     return __uint_as_float(e >= -126 ? (uint32_t)(e + 127) << 23 : 1u << (e + 149));
 }
@@ -193,62 +170,78 @@ __device__ __forceinline__ uint32_t half_pair(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Activation rows j0 .. j0 + rows - 1 into shared memory as fp16, zero past K, in one column (fp16, bf16) or
-// two (fp32); back[column] is the power of two that its sums are to be multiplied by.  top: a word per row.
-template <typename T>
-__device__ void stage_rows(const W4Args &a, int j0, int rows, uint16_t *xs, int KP, float *back, unsigned *top) {
-    const T *x = static_cast<const T *>(a.x) + (int64_t)j0 * a.x_stride;
-    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride * (int64_t)sizeof(T) % 16 == 0;
-    const int n8 = a.nchunk * (W4_CHUNK / 8);
-    if (!std::is_same_v<T, __half>) {  // largest finite magnitude of each row (as bits, which order alike)
-        for (int j = threadIdx.x; j < rows; j += blockDim.x) top[j] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows * n8; i += blockDim.x) {
-            const int j = i / n8, k = (i - j * n8) * 8;
-            float v[8];
-            load8(x + (int64_t)j * a.x_stride, k, a.K, wide, v);
-            unsigned m = 0;
+// Activation rows in shared memory: 8 values lie together as 16 bytes of fp16, or for fp32 rows as 16 bytes of
+// the first parts and 16 of the second, so that the caller's values are copied in as they are and turned in
+// place.  copy_rows starts the copies of rows j0 .. j0 + rows - 1 (zero past K); after they have arrived and a
+// barrier turn_rows makes the fp16 values; back[column] is the power of two that a column's sums are to be
+// multiplied by.  top: a word per row.
+__device__ __forceinline__ void copy_rows(const W4Args &a, int j0, int rows, char *xs, int row_bytes) {
+    const int eb = a.dtype == MOE_DTYPE_F32 ? 4 : 2, nt = blockDim.x;
+    const int64_t stride = a.x_stride * eb;
+    const char *x = static_cast<const char *>(a.x) + j0 * stride;
+    const int n16 = a.nchunk * W4_CHUNK * eb / 16, kb = a.K * eb;  // 16-byte pieces of a row, bytes of its values
+    const bool wide = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)stride) % 16 == 0;
+    for (int i = threadIdx.x; i < rows * n16; i += nt) {
+        const int j = i / n16, at = (i - j * n16) * 16;
+        char *dst = xs + j * row_bytes + at;
+        if (at >= kb)
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+        else if (wide)
+            cp_async16(smem32(dst), x + j * stride + at);
+        else if (eb == 4)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const unsigned b = __float_as_uint(v[q]) & 0x7fffffffu;
+            for (int q = 0; q < 4; ++q)
+                reinterpret_cast<uint32_t *>(dst)[q] = reinterpret_cast<const uint32_t *>(x + j * stride + at)[q];
+        else
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                reinterpret_cast<uint16_t *>(dst)[q] = reinterpret_cast<const uint16_t *>(x + j * stride + at)[q];
+    }
+}
+
+template <typename T>  // float or bf16 (fp16 rows stay as they are)
+__device__ __forceinline__ void turn_rows(const W4Args &a, int rows, char *xs, int row_bytes, float *back, unsigned *top) {
+    constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1, V = 16 / sizeof(T);
+    const int n8 = a.nchunk * (W4_CHUNK / 8), n = rows * n8, nt = blockDim.x;
+    for (int j = threadIdx.x; j < rows; j += nt) top[j] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += nt) {  // the largest finite magnitude of each row, as bits
+        const int j = i / n8;
+        const T *src = reinterpret_cast<const T *>(xs + j * row_bytes) + (i - j * n8) * 8;
+        unsigned m = 0;
+#pragma unroll
+        for (int h = 0; h < 8; h += V) {
+            Pack<T, V> p;
+            p.load(src + h);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const unsigned b = __float_as_uint(p.get(q)) & 0x7fffffffu;
                 m = max(m, b < 0x7f800000u ? b : 0u);
             }
-            if (m) atomicMax(&top[j], m);
         }
-        __syncthreads();
+        if (m) atomicMax(&top[j], m);
     }
-    for (int i = threadIdx.x; i < rows * n8; i += blockDim.x) {
-        const int j = i / n8, k = (i - j * n8) * 8;
-        if (std::is_same_v<T, __half>) {
-            const uint16_t *src = reinterpret_cast<const uint16_t *>(x) + (int64_t)j * a.x_stride;
-            uint4 v;
-            if (wide && k + 8 <= a.K) {
-                v = *reinterpret_cast<const uint4 *>(src + k);
-            } else {
-                uint32_t u[4] = {};
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (k + q < a.K) u[q >> 1] |= (uint32_t)src[k + q] << (16 * (q & 1));
-                v = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-            *reinterpret_cast<uint4 *>(xs + (size_t)j * KP + k) = v;
-            if (k == 0) back[j] = 1.0f;
-            continue;
-        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += nt) {
+        const int j = i / n8;
+        char *at = xs + j * row_bytes + (i - j * n8) * 8 * sizeof(T);
         // 2^-ex times the row lies below 2^15; ex >= -126 keeps that factor a normal number
         const int ex = top[j] ? max((int)(top[j] >> 23) - 127 - 14, -126) : 0;
         const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
         float v[8];
-        load8(x + (int64_t)j * a.x_stride, k, a.K, wide, v);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], down);
-        constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1;
+        for (int h = 0; h < 8; h += V) {
+            Pack<T, V> p;
+            p.load(reinterpret_cast<const T *>(at) + h);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[h + q] = __fmul_rn(p.get(q), down);
+        }
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
             uint32_t u[4];
 #pragma unroll
             for (int q = 0; q < 8; q += 2) u[q >> 1] = half_pair(v[q], v[q + 1]);
-            *reinterpret_cast<uint4 *>(xs + (size_t)(PARTS * j + part) * KP + k) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4 *>(at + part * 16) = make_uint4(u[0], u[1], u[2], u[3]);
             if (part + 1 < PARTS)
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {  // what is left, 2^11 times; an infinity or NaN stays in the first
@@ -256,7 +249,7 @@ __device__ void stage_rows(const W4Args &a, int j0, int rows, uint16_t *xs, int 
                     v[q] = fabsf(v[q]) < INFINITY ? (v[q] - hi) * 2048.0f : 0.0f;
                 }
         }
-        if (k == 0) {
+        if (i - j * n8 == 0) {
             back[PARTS * j] = exp2_int(ex);
             if (PARTS == 2) back[PARTS * j + 1] = exp2_int(ex - 11);
         }
@@ -274,13 +267,14 @@ __device__ __forceinline__ void store_y(const W4Args &a, int64_t at, float v) {
 
 // One record (16 rows x 128 columns of weights) against NT tiles of 8 activation columns.  Offsets into smem:
 // rec, the record plus 16 * lane; scp and zpp, the lane's scales and zero points; x[n] + k0, the lane's column of
-// tile n at the record's first column (columns past the last are copies of it: their sums are not used).
+// tile n at the record's first column, kb bytes further for each 32 (columns past the last are copies of it: their
+// sums are not used).
 template <typename V>
 __device__ __forceinline__ V lds(const char *smem, uint32_t at) { return *reinterpret_cast<const V *>(smem + at); }
 
 template <int G, bool ZP, bool SBF, int NT, int NTM>
 __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32_t scp, uint32_t zpp,
-                                          const uint32_t (&x)[NTM], uint32_t k0, float (&sum)[NTM][4]) {
+                                          const uint32_t (&x)[NTM], uint32_t k0, uint32_t kb, float (&sum)[NTM][4]) {
     constexpr int NB = W4_CHUNK / G;
     const uint4 wl = lds<uint4>(smem, rec), wh = lds<uint4>(smem, rec + 512);
     const uint32_t lo[4] = {wl.x, wl.y, wl.z, wl.w}, hi[4] = {wh.x, wh.y, wh.z, wh.w};
@@ -316,18 +310,24 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
             zr[0] = lds<uint16_t>(smem, zpp);
         }
     }
-    auto zero = [&](int i) { return ZP ? ((zr[i >> 2] >> (8 * (i & 3))) & 0xffu) * 0x00010001u : 0x00080008u; };
+    // 1024 + z and -(64 + z) of the i-th zero point, twice each: its low four bits under 0x64.., its high ones
+    // under 0xd4..
+    auto off = [&](int i) {
+        return ZP ? __byte_perm(zr[i >> 2] & 0x0f0f0f0fu, 0x64, 0x4040u + 0x0101u * (i & 3)) : 0x64086408u;
+    };
+    auto off16 = [&](int i) {
+        return ZP ? __byte_perm(zr[i >> 2] & 0xf0f0f0f0u, 0xd4, 0x4040u + 0x0101u * (i & 3)) : 0xd480d480u;
+    };
     float acc[NT][4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         const int gi = b * 32 / G;
-        const uint32_t z0 = zero(gi), z1 = zero(NB + gi);
         uint32_t p[4], r[4];
-        unpack(lo[b], 0x64006400u + z0, 0xd400d400u + 16 * z0, p);
-        unpack(hi[b], 0x64006400u + z1, 0xd400d400u + 16 * z1, r);
+        unpack(lo[b], off(gi), off16(gi), p);
+        unpack(hi[b], off(NB + gi), off16(NB + gi), r);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint4 xv = lds<uint4>(smem, x[n] + k0 + b * 64);
+            const uint4 xv = lds<uint4>(smem, x[n] + k0 + b * kb);
             if (b * 32 % G == 0)
                 mma16816<true>(acc[n], p[0], r[0], p[1], r[1], xv.x, xv.y);
             else
@@ -352,24 +352,23 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
 // its chunks; their sums meet in shared memory in warp order (wk == 1: the lanes hold whole sums).  Every warp
 // streams its pairs of records through a ring of S slots of its own, filled by cp.async ahead of the tiles: the
 // stream does not stop at the end of a tile or a unit.  NTM: column tiles of 8 that the accumulators hold.
-template <int G, bool ZP, bool SBF, int NTM, int S>
+template <int G, bool ZP, bool SBF, int NTM>
 __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
-    constexpr int NB = W4_CHUNK / G, REC = w4_record(G, ZP), MORE = (REC - 1024) / 16, SLOT = 2 * REC;
+    constexpr int NB = W4_CHUNK / G, REC = w4_record(G, ZP), MORE = (REC - 1024) / 16, SLOT = 2 * REC, S = W4_SLOTS;
     extern __shared__ __align__(16) char smem[];
     __shared__ int wsum[W4_WARPS];
     __shared__ float back[NTM * 8];
     __shared__ unsigned top[NTM * 8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int warps = blockDim.x >> 5;
-    const int KP = a.nchunk * W4_CHUNK + W4_XPAD;
     const int cpr = a.dtype == MOE_DTYPE_F32 ? 2 : 1;
+    const int row_bytes = a.nchunk * W4_CHUNK * 2 * cpr + W4_XPAD;  // of a staged row
+    const uint32_t kb = 64 * cpr;                                   // bytes of 32 of its values
     const int wt = warp / a.wk, wk = warp - wt * a.wk, per = warps / a.wk;
     const uint32_t ring = warp * S * SLOT;  // offsets into smem, as below
-    // the sums: `bufs` buffers, [warps][nt_max * 8 columns][20 (16 rows, padded against bank conflicts)]
-    const int red_warp = a.nt_max * 8 * 20;
-    float *red = reinterpret_cast<float *>(smem + warps * S * SLOT);
-    uint16_t *xs = reinterpret_cast<uint16_t *>(red + a.bufs * warps * red_warp);
-    int *first = reinterpret_cast<int *>(xs + (size_t)a.pass_rows * cpr * KP);  // [E + 1]: each expert's first pass
+    float4 *red = reinterpret_cast<float4 *>(smem + warps * S * SLOT);  // the sums: [bufs][warps][nt_max][lanes]
+    char *xs = reinterpret_cast<char *>(red + a.bufs * warps * a.nt_max * 32);
+    int *first = reinterpret_cast<int *>(xs + a.pass_rows * row_bytes);  // [E + 1]: each expert's first pass
 
     int units = (a.n_rows + a.pass_rows - 1) / a.pass_rows;
     if (a.expStart != nullptr) {
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
     uint32_t slot = ring0, free_slot = ring1, at[NTM];  // the slot to read, and the one read before it
     // the lane's scales and zero points, from its 16 bytes of codes
     const int sc_off = 1024 + g * 4 * NB - lane * 16, zp_off = 1024 + 32 * NB + g * 2 * NB - lane * 16;
-    const uint32_t x0 = (uint32_t)(reinterpret_cast<char *>(xs) - smem);
+    const uint32_t x0 = (uint32_t)(xs - smem);
     const int sh = a.pair ? 3 : 4;  // a tile's rows: 8 or 16
     int u = u0, tile0 = t0;
     while (todo > 0) {
@@ -499,16 +498,24 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
             const int cols = rows * cpr;
             nt = (cols + 7) >> 3;
 #pragma unroll
-            for (int n = 0; n < NTM; ++n)
-                at[n] = x0 + (min(n * 8 + g, cols - 1) * KP + t * 8 + wk * 2 * W4_CHUNK) * 2;
+            for (int n = 0; n < NTM; ++n) {
+                const int c = min(n * 8 + g, cols - 1);
+                at[n] = x0 + (cpr == 2 ? (c >> 1) * row_bytes + (c & 1) * 16 : c * row_bytes) + t * 16 * cpr + wk * 8 * kb;
+            }
             __syncthreads();
-            if (a.dtype == MOE_DTYPE_F32)
-                stage_rows<float>(a, j0, rows, xs, KP, back, top);
-            else if (a.dtype == MOE_DTYPE_F16)
-                stage_rows<__half>(a, j0, rows, xs, KP, back, top);
-            else
-                stage_rows<__nv_bfloat16>(a, j0, rows, xs, KP, back, top);
+            copy_rows(a, j0, rows, xs, row_bytes);
+            cp_async_commit();
+            cp_async_wait<0>();
             __syncthreads();
+            if (a.dtype == MOE_DTYPE_F32) {
+                turn_rows<float>(a, rows, xs, row_bytes, back, top);
+                __syncthreads();
+            } else if (a.dtype == MOE_DTYPE_BF16) {
+                turn_rows<__nv_bfloat16>(a, rows, xs, row_bytes, back, top);
+                __syncthreads();
+            } else if (tid < rows) {
+                back[tid] = 1.0f;
+            }
         }
         const int now = min(per, min(a.ntiles - tile0, todo)), tile = tile0 + wt;
         float sum[NTM][4];
@@ -524,92 +531,78 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 fetch(free_slot);  // every lane has read it before this point
                 const bool both = !(odd && c == per_tile - 1);
                 if (NTM == 1 || nt == 1) {
-                    chunk_mma<G, ZP, SBF, 1, NTM>(smem, slot, slot + sc_off, slot + zp_off, at, k0, sum);
+                    chunk_mma<G, ZP, SBF, 1, NTM>(smem, slot, slot + sc_off, slot + zp_off, at, k0, kb, sum);
                     if (both)
                         chunk_mma<G, ZP, SBF, 1, NTM>(smem, slot + REC, slot + REC + sc_off, slot + REC + zp_off, at,
-                                                      k0 + 2 * W4_CHUNK, sum);
+                                                      k0 + 4 * kb, kb, sum);
                 } else {
 #pragma unroll 1
                     for (int h = 0; h < 1 + both; ++h) {
-                        const uint32_t rec = slot + h * REC, k = k0 + h * 2 * W4_CHUNK;
+                        const uint32_t rec = slot + h * REC, k = k0 + h * 4 * kb;
                         if (nt == 2)
-                            chunk_mma<G, ZP, SBF, NTM < 2 ? 1 : 2, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, sum);
+                            chunk_mma<G, ZP, SBF, NTM < 2 ? 1 : 2, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, kb, sum);
                         else if (nt == 3)
-                            chunk_mma<G, ZP, SBF, NTM < 3 ? 1 : 3, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, sum);
+                            chunk_mma<G, ZP, SBF, NTM < 3 ? 1 : 3, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, kb, sum);
                         else
-                            chunk_mma<G, ZP, SBF, NTM, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, sum);
+                            chunk_mma<G, ZP, SBF, NTM, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, kb, sum);
                     }
                 }
-                k0 += a.wk * W4_CHUNK * 4;
+                k0 += a.wk * 8 * kb;
                 free_slot = slot;
                 slot = slot == ring1 ? ring0 : slot + SLOT;
             }
         }
-        if (a.wk == 1) {
-            // the lane's sums are whole: rows g and g + 8 of the tile (gate and up) times columns 2t and 2t + 1 (of
-            // an fp32 row both its parts)
-            if (wt < now) {
-                const int r = (tile << sh) + g;
-#pragma unroll
-                for (int n = 0; n < NTM; ++n) {
-                    if (n >= nt) break;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = n * 8 + 2 * t + h, j = cpr == 2 ? c >> 1 : c;
-                        if ((cpr == 2 && h) || j >= rows) continue;
-                        float v0 = __fmul_rn(sum[n][h], back[c]), v1 = __fmul_rn(sum[n][2 + h], back[c]);
-                        if (cpr == 2) {
-                            v0 = __fmaf_rn(sum[n][1], back[c + 1], v0);
-                            v1 = __fmaf_rn(sum[n][3], back[c + 1], v1);
-                        }
-                        const int64_t to = (int64_t)(j0 + j) * a.y_stride;
-                        if (a.pair) {
-                            if (r < a.R) store_y(a, to + r, __fdiv_rn(v0, 1.0f + expf(-v0)) * v1);
-                        } else {
-                            if (r < a.R) store_y(a, to + r, v0);
-                            if (r + 8 < a.R) store_y(a, to + r + 8, v1);
-                        }
-                    }
-                }
-            }
-        } else {
-            float *mine = red + (buf * warps + warp) * red_warp;
-            const float *all = red + (buf * warps + wt * a.wk) * red_warp;
+        if (a.wk > 1) {
+            // the sharing warps' sums, lane by lane: column tile n is finished by warp n % wk, which adds the
+            // others' in warp order
+            float4 *all = red + (buf * warps + wt * a.wk) * a.nt_max * 32 + lane;
 #pragma unroll
             for (int n = 0; n < NTM; ++n)
-                if (n < nt) {
-                    float *dst = mine + (n * 8 + 2 * t) * 20 + g;
-                    dst[0] = sum[n][0];
-                    dst[20] = sum[n][1];
-                    dst[8] = sum[n][2];
-                    dst[28] = sum[n][3];
-                }
+                if (n < nt) all[(wk * a.nt_max + n) * 32] = make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]);
             asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(a.wk * 32) : "memory");
-            if (wt < now) {
-                for (int i = wk * 32 + lane; i < rows << sh; i += a.wk * 32) {
-                    const int j = i >> sh, rr = i & ((1 << sh) - 1), r = (tile << sh) + rr;
-                    if (r >= a.R) continue;
-                    float v = 0.0f, up = 0.0f;
-                    for (int part = 0; part < cpr; ++part) {
-                        const float *p = all + (j * cpr + part) * 20 + rr;
-                        float s0 = p[0], s1 = a.pair ? p[8] : 0.0f;
 #pragma unroll
-                        for (int w = 1; w < 8; ++w)
-                            if (w < a.wk) {
-                                s0 += p[w * red_warp];
-                                if (a.pair) s1 += p[w * red_warp + 8];
-                            }
-                        v = __fmaf_rn(s0, back[j * cpr + part], v);
-                        up = __fmaf_rn(s1, back[j * cpr + part], up);
-                    }
-                    if (a.pair) v = __fdiv_rn(v, 1.0f + expf(-v)) * up;
-                    store_y(a, (int64_t)(j0 + j) * a.y_stride + r, v);
+            for (int n = 0; n < NTM; ++n)
+                if (n < nt && (n & (a.wk - 1)) == wk) {
+                    float4 v = all[n * 32];
+#pragma unroll
+                    for (int w = 1; w < 8; ++w)
+                        if (w < a.wk) {
+                            const float4 o = all[(w * a.nt_max + n) * 32];
+                            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                        }
+                    sum[n][0] = v.x, sum[n][1] = v.y, sum[n][2] = v.z, sum[n][3] = v.w;
                 }
-            }
             if (a.bufs == 2)
                 buf ^= 1;  // the next sums go elsewhere, those after them behind the next barrier
             else
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(a.wk * 32) : "memory");
+        }
+        // the lane's sums: rows g and g + 8 of the tile (gate and up) times columns 2t and 2t + 1 (of an fp32 row
+        // both its parts)
+        if (wt < now) {
+            const int r = (tile << sh) + g;
+#pragma unroll
+            for (int n = 0; n < NTM; ++n) {
+                if (n >= nt) break;
+                if ((n & (a.wk - 1)) != wk) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = n * 8 + 2 * t + h, j = cpr == 2 ? c >> 1 : c;
+                    if ((cpr == 2 && h) || j >= rows) continue;
+                    float v0 = __fmul_rn(sum[n][h], back[c]), v1 = __fmul_rn(sum[n][2 + h], back[c]);
+                    if (cpr == 2) {
+                        v0 = __fmaf_rn(sum[n][1], back[c + 1], v0);
+                        v1 = __fmaf_rn(sum[n][3], back[c + 1], v1);
+                    }
+                    const int64_t to = (int64_t)(j0 + j) * a.y_stride;
+                    if (a.pair) {
+                        if (r < a.R) store_y(a, to + r, __fdiv_rn(v0, 1.0f + expf(-v0)) * v1);
+                    } else {
+                        if (r < a.R) store_y(a, to + r, v0);
+                        if (r + 8 < a.R) store_y(a, to + r + 8, v1);
+                    }
+                }
+            }
         }
         todo -= now;
         tile0 += now;
@@ -665,7 +658,7 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     a.status = status;
     const int sms = std::max(1, device_sm_count());
     const int cpr = dtype == MOE_DTYPE_F32 ? 2 : 1;
-    const size_t row_bytes = (size_t)(a.nchunk * W4_CHUNK + W4_XPAD) * 2 * cpr;
+    const size_t row_bytes = (size_t)a.nchunk * W4_CHUNK * 2 * cpr + W4_XPAD;
     const size_t record = w4_record(w->group, w->zeros);
     // Warps a tile: the fewest that leave the GPU's 16 warps an SM six tiles each in turn (a tile that is shared
     // costs a barrier and a reduction, long turns a longer tail), but no more than have a pair of chunks each.
@@ -675,29 +668,29 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     int wk = 1;
     while (wk < 8 && wk < pairs && tiles * wk < (int64_t)sms * 16 * 6) wk *= 2;
     a.wk = wk;
-    auto smem_for = [&](int rows, int warps, int depth, int bufs) {
+    // shared memory of a CTA
+    auto smem_for = [&](int rows, int warps, int bufs) {
         const size_t nt = (rows * cpr + 7) / 8;
-        return (size_t)warps * depth * 2 * record + (wk > 1 ? (size_t)bufs * warps * nt * 8 * 20 * 4 : 0) +
+        return (size_t)warps * W4_SLOTS * 2 * record + (wk > 1 ? (size_t)bufs * warps * nt * 512 : 0) +
                row_bytes * rows + (size_t)(w->E + 1) * 4;
     };
-    // most rows a pass of a CTA of so many warps (16 warps an SM) with a ring of `depth`
-    auto fit = [&](int warps, int depth, int bufs) {
+    struct Shape {
+        int warps, ctas, bufs;  // CTAs an SM
+    };
+    auto fit = [&](const Shape &o) {  // most rows a pass
         int rows = 32 / cpr;
-        while (rows > 0 && smem_for(rows, warps, depth, bufs) > W4_SMEM_SM / (16 / warps) - 1536) --rows;
+        while (rows > 0 && smem_for(rows, o.warps, o.bufs) > W4_SMEM_SM / o.ctas - 1536) --rows;
         return rows;
     };
-    // Rows wanted a pass: all of a single matrix; of many experts four times the mean, their segments being
-    // uneven (a longer segment takes a pass more).
-    const int want = std::min({32 / cpr, n_rows, w->E == 1 ? n_rows : std::max(8 / cpr, 4 * ((n_rows + w->E - 1) / w->E))});
-    // two CTAs of 8 warps an SM where their rows fit; one of 16, the rows staged once, where they are long
-    struct Shape {
-        int warps, depth, bufs;
-    };
-    Shape shape{8, 3, 2};
-    int rows = std::min(want, fit(8, 3, 2));
-    for (const Shape &o : {Shape{16, 3, 2}, Shape{16, 3, 1}, Shape{16, 2, 1}, Shape{8, 2, 1}}) {
-        if (rows == want) break;
-        const int more = std::min(want, o.warps == 8 ? (smem_for(1, 8, 2, 1) <= W4_SMEM_SM - 1536 ? 1 : 0) : fit(o.warps, o.depth, o.bufs));
+    // Rows wanted a pass: all of a single matrix; of many experts twice the mean, their segments being uneven (a
+    // longer segment takes a pass more), and a column tile at least.
+    const int want = std::min({32 / cpr, n_rows, w->E == 1 ? n_rows : std::max(8 / cpr, 2 * ((n_rows + w->E - 1) / w->E))});
+    // Two CTAs of 8 warps an SM where their rows fit; one of 16, the rows staged once, where they are long and that
+    // saves passes; one of 8 for the longest.
+    Shape shape{8, 2, 2};
+    int rows = std::min(want, fit(shape));
+    for (const Shape &o : {Shape{16, 1, 2}, Shape{16, 1, 1}, Shape{8, 1, 1}}) {
+        const int more = std::min(want, fit(o));
         if (more > 0 && (rows == 0 || (n_rows + more - 1) / more < (n_rows + rows - 1) / rows)) shape = o, rows = more;
     }
     if (rows == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -705,11 +698,11 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     a.pass_rows = rows;
     a.nt_max = (rows * cpr + 7) / 8;
     a.bufs = wk > 1 ? shape.bufs : 0;
-    const int depth = shape.depth, per = shape.warps / wk;
+    const int per = shape.warps / wk;
     const int64_t most = (int64_t)((a.ntiles + per - 1) / per) *
                          (w->E == 1 ? (n_rows + rows - 1) / rows : (int64_t)n_rows);
-    const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)sms * (16 / shape.warps));
-    const size_t smem = smem_for(rows, shape.warps, shape.depth, shape.bufs);
+    const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)sms * shape.ctas);
+    const size_t smem = smem_for(rows, shape.warps, shape.bufs);
     auto go = [&](auto kernel, SmemOptIn *done) {
         int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, done);
         if (rc) return rc;
@@ -719,10 +712,8 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     auto by_types = [&](auto gc, auto zc, auto bc) {
         constexpr int G = decltype(gc)::value;
         constexpr bool ZP = decltype(zc)::value, SBF = decltype(bc)::value;
-        static SmemOptIn d[4];
-        if (a.nt_max > 1)
-            return depth == 3 ? go(w4_kernel<G, ZP, SBF, 4, 3>, &d[0]) : go(w4_kernel<G, ZP, SBF, 4, 2>, &d[1]);
-        return depth == 3 ? go(w4_kernel<G, ZP, SBF, 1, 3>, &d[2]) : go(w4_kernel<G, ZP, SBF, 1, 2>, &d[3]);
+        static SmemOptIn d[2];
+        return a.nt_max > 1 ? go(w4_kernel<G, ZP, SBF, 4>, &d[0]) : go(w4_kernel<G, ZP, SBF, 1>, &d[1]);
     };
     auto by_zeros = [&](auto gc, auto bc) {
         return w->zeros ? by_types(gc, std::true_type(), bc) : by_types(gc, std::false_type(), bc);

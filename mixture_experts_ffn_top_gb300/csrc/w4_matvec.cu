@@ -32,7 +32,9 @@ namespace moe {
 namespace {
 
 constexpr int W4_WARPS = 16;                   // at most; a CTA has 8 or 16
-constexpr int W4_SLOTS = 3;                    // pairs of records in a warp's ring
+#ifndef W4_TURNS
+#define W4_TURNS 6
+#endif
 constexpr int W4_CHUNK = 128;                  // columns of a chunk
 constexpr int W4_XPAD = 64;                    // bytes past a multiple of 128 that staged rows lie apart: no bank conflicts
 constexpr size_t W4_SMEM_SM = 227 * 1024;      // shared memory of an SM's CTAs, less 1 KB each
@@ -144,15 +146,27 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void wait_all_but(int n) {  // the n (0 .. 3) groups begun last
+    if (n == 2)
+        cp_async_wait<2>();
+    else if (n == 1)
+        cp_async_wait<1>();
+    else if (n == 3)
+        cp_async_wait<3>();
+    else
+        cp_async_wait<0>();
+}
 
 struct W4Args {
     const char *records;  // [E][ntiles][nchunk]
-    int pair, E, R, K, nchunk, ntiles;
+    int scale_bf, pair, E, R, K, nchunk, ntiles;
     const void *x;
     int64_t x_stride;
     int dtype;
     const int32_t *expStart;
     int n_rows, pass_rows;  // rows of an expert taken at a time
+    int stage_rows;         // rows that shared memory holds
+    int slots;              // of a warp's ring: 2 to 4 pairs of records
     int wk;                 // warps that share a tile's chunks; the CTA's other warps take the next tiles
     int nt_max;             // column tiles of 8 that pass_rows rows fill
     int bufs;               // buffers for the sums
@@ -181,22 +195,21 @@ __device__ __forceinline__ void copy_rows(const W4Args &a, int j0, int rows, cha
     const char *x = static_cast<const char *>(a.x) + j0 * stride;
     const int n16 = a.nchunk * W4_CHUNK * eb / 16, kb = a.K * eb;  // 16-byte pieces of a row, bytes of its values
     const bool wide = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)stride) % 16 == 0;
-    for (int i = threadIdx.x; i < rows * n16; i += nt) {
-        const int j = i / n16, at = (i - j * n16) * 16;
-        char *dst = xs + j * row_bytes + at;
-        if (at >= kb)
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
-        else if (wide)
-            cp_async16(smem32(dst), x + j * stride + at);
-        else if (eb == 4)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                reinterpret_cast<uint32_t *>(dst)[q] = reinterpret_cast<const uint32_t *>(x + j * stride + at)[q];
-        else
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                reinterpret_cast<uint16_t *>(dst)[q] = reinterpret_cast<const uint16_t *>(x + j * stride + at)[q];
-    }
+    for (int j = 0; j < rows; ++j, x += stride, xs += row_bytes)
+        for (int at = threadIdx.x * 16; at < n16 * 16; at += nt * 16) {
+            if (at >= kb) {
+                *reinterpret_cast<uint4 *>(xs + at) = make_uint4(0, 0, 0, 0);
+            } else if (wide) {
+                cp_async16(smem32(xs + at), x + at);
+            } else {
+#pragma unroll 1
+                for (int q = 0; q < 16; q += eb)
+                    if (eb == 4)
+                        *reinterpret_cast<uint32_t *>(xs + at + q) = *reinterpret_cast<const uint32_t *>(x + at + q);
+                    else
+                        *reinterpret_cast<uint16_t *>(xs + at + q) = *reinterpret_cast<const uint16_t *>(x + at + q);
+            }
+        }
 }
 
 template <typename T>  // float or bf16 (fp16 rows stay as they are)
@@ -272,10 +285,10 @@ __device__ __forceinline__ void store_y(const W4Args &a, int64_t at, float v) {
 template <typename V>
 __device__ __forceinline__ V lds(const char *smem, uint32_t at) { return *reinterpret_cast<const V *>(smem + at); }
 
-template <int G, bool ZP, bool SBF, int NT, int NTM>
-__device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32_t scp, uint32_t zpp,
-                                          const uint32_t (&x)[NTM], uint32_t k0, uint32_t kb, float (&sum)[NTM][4]) {
-    constexpr int NB = W4_CHUNK / G;
+template <int G, bool ZP, bool F32, int NT, int NTM>
+__device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32_t scp, uint32_t zpp, bool sbf,
+                                          const uint32_t (&x)[NTM], uint32_t k0, float (&sum)[NTM][4]) {
+    constexpr int NB = W4_CHUNK / G, KB = F32 ? 128 : 64;
     const uint4 wl = lds<uint4>(smem, rec), wh = lds<uint4>(smem, rec + 512);
     const uint32_t lo[4] = {wl.x, wl.y, wl.z, wl.w}, hi[4] = {wh.x, wh.y, wh.z, wh.w};
     // this row's and row + 8's scales (16 bits) and zero points (8 bits), NB each
@@ -292,7 +305,7 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
     float sc[2 * NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-        if (SBF) {
+        if (sbf) {
             sc[2 * i] = __uint_as_float(sw[i] << 16), sc[2 * i + 1] = __uint_as_float(sw[i] & 0xffff0000u);
         } else {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&sw[i]));
@@ -327,7 +340,7 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
         unpack(hi[b], off(NB + gi), off16(NB + gi), r);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint4 xv = lds<uint4>(smem, x[n] + k0 + b * kb);
+            const uint4 xv = lds<uint4>(smem, x[n] + k0 + b * KB);
             if (b * 32 % G == 0)
                 mma16816<true>(acc[n], p[0], r[0], p[1], r[1], xv.x, xv.y);
             else
@@ -352,46 +365,42 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
 // its chunks; their sums meet in shared memory in warp order (wk == 1: the lanes hold whole sums).  Every warp
 // streams its pairs of records through a ring of S slots of its own, filled by cp.async ahead of the tiles: the
 // stream does not stop at the end of a tile or a unit.  NTM: column tiles of 8 that the accumulators hold.
-template <int G, bool ZP, bool SBF, int NTM>
+template <int G, bool ZP, bool F32, int NTM>
 __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
-    constexpr int NB = W4_CHUNK / G, REC = w4_record(G, ZP), MORE = (REC - 1024) / 16, SLOT = 2 * REC, S = W4_SLOTS;
+    constexpr int NB = W4_CHUNK / G, REC = w4_record(G, ZP), MORE = (REC - 1024) / 16, SLOT = 2 * REC;
+    constexpr int cpr = F32 ? 2 : 1;  // columns per row
+    constexpr uint32_t KB = 64 * cpr;  // bytes of 32 values of a staged row
     extern __shared__ __align__(16) char smem[];
     __shared__ int wsum[W4_WARPS];
-    __shared__ float back[NTM * 8];
-    __shared__ unsigned top[NTM * 8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int warps = blockDim.x >> 5;
-    const int cpr = a.dtype == MOE_DTYPE_F32 ? 2 : 1;
     const int row_bytes = a.nchunk * W4_CHUNK * 2 * cpr + W4_XPAD;  // of a staged row
-    const uint32_t kb = 64 * cpr;                                   // bytes of 32 of its values
+    const int S = a.slots;
     const int wt = warp / a.wk, wk = warp - wt * a.wk, per = warps / a.wk;
     const uint32_t ring = warp * S * SLOT;  // offsets into smem, as below
     float4 *red = reinterpret_cast<float4 *>(smem + warps * S * SLOT);  // the sums: [bufs][warps][nt_max][lanes]
     char *xs = reinterpret_cast<char *>(red + a.bufs * warps * a.nt_max * 32);
-    int *first = reinterpret_cast<int *>(xs + a.pass_rows * row_bytes);  // [E + 1]: each expert's first pass
+    int *first = reinterpret_cast<int *>(xs + a.stage_rows * row_bytes);  // [E + 1]: each expert's first pass
+    float *back = reinterpret_cast<float *>(first + a.E + 1);             // [stage_rows][cpr]
+    unsigned *top = reinterpret_cast<unsigned *>(back + a.stage_rows * cpr);  // [stage_rows]
 
     int units = (a.n_rows + a.pass_rows - 1) / a.pass_rows;
     if (a.expStart != nullptr) {
-        // passes of each expert, exclusive scan (four experts a thread); every offset is checked
+        // passes of each expert, exclusive scan; every offset is checked
+        const int each = (a.E + blockDim.x - 1) / blockDim.x, e0 = tid * each;  // a thread's experts
         bool bad = false;
-        int cnt[4], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid * 4 + i;
-            cnt[i] = 0;
-            if (e < a.E) {
-                const int p = a.expStart[e], q = a.expStart[e + 1];
-                if (p < 0 || q < p || q > a.n_rows || (e == 0 && p != 0))
-                    bad = true;
-                else
-                    cnt[i] = (q - p + a.pass_rows - 1) / a.pass_rows;
+        auto passes = [&](int e) {
+            if (e >= a.E) return 0;
+            const int p = a.expStart[e], q = a.expStart[e + 1];
+            if (p < 0 || q < p || q > a.n_rows || (e == 0 && p != 0)) {
+                bad = true;
+                return 0;
             }
-            mine += cnt[i];
-        }
-        if (__syncthreads_or(bad)) {
-            if (tid == 0) atomicOr(a.status, MOE_DEV_BAD_CSR);
-            return;
-        }
+            return (int)((unsigned)(q - p + a.pass_rows - 1) / (unsigned)a.pass_rows);
+        };
+        int mine = 0;
+#pragma unroll 1
+        for (int i = 0; i < each; ++i) mine += passes(e0 + i);
         int inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -399,17 +408,21 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
             if (lane >= o) inc += v;
         }
         if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) atomicOr(a.status, MOE_DEV_BAD_CSR);
+            return;
+        }
         int run = inc - mine;
         units = 0;
+#pragma unroll 1
         for (int w = 0; w < warps; ++w) {
             if (w < warp) run += wsum[w];
             units += wsum[w];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (tid * 4 + i < a.E) first[tid * 4 + i] = run;
-            run += cnt[i];
+#pragma unroll 1
+        for (int i = 0; i < each && e0 + i < a.E; ++i) {
+            first[e0 + i] = run;
+            run += each == 1 ? mine : passes(e0 + i);
         }
         if (tid == 0) first[a.E] = units;
         __syncthreads();
@@ -426,12 +439,13 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
         }
         return lo;
     };
-    const int64_t items = (int64_t)units * a.ntiles;
-    const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
-    if (i0 >= i1) return;
-    // tiles of this CTA, and its first
-    int todo = (int)min(i1 - i0, (int64_t)0x7fffffff);
-    const int u0 = (int)(i0 / a.ntiles), t0 = (int)(i0 - (int64_t)u0 * a.ntiles);
+    // tiles of this CTA (the host keeps their number below 2^31), and its first
+    const unsigned items = (unsigned)units * (unsigned)a.ntiles, share = items / gridDim.x, more = items % gridDim.x;
+    const unsigned i0 = blockIdx.x * share + min(blockIdx.x, more);
+    int todo = (int)(share + (blockIdx.x < more));
+    if (todo == 0) return;
+    const int u0 = (int)(i0 / (unsigned)a.ntiles), t0 = (int)(i0 - (unsigned)u0 * a.ntiles);
+    const int last_unit = (int)((i0 + todo - 1) / (unsigned)a.ntiles);
 
     // The CTA takes `per` tiles of a unit at a time.  The fetching position runs ahead of the computing one:
     // ftile of unit fu (fleft tiles to come), the pair at fsrc, fnum more of this warp's tile, the last of them
@@ -477,44 +491,81 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
         }
         cp_async_commit();
     };
+    // rows of a unit: the first, and how many
+    auto unit_rows = [&](int v, int *begin) {
+        const int e = expert_of(v);
+        const int lo = a.expStart ? a.expStart[e] : 0, hi = a.expStart ? a.expStart[e + 1] : a.n_rows;
+        *begin = lo + (v - (a.expStart ? first[e] : 0)) * a.pass_rows;
+        return min(hi - *begin, a.pass_rows);
+    };
+    // The rows of the first unit are asked for before any weights; those of each next one while a unit is at
+    // work, into the part of the staging room that it leaves, so that the warps need not stop for them.
+    int j0, rows = unit_rows(u0, &j0), x_at = 0;
+    int next_rows = 0, next_j0 = 0, next_at = -1;  // the next unit's (next_at < 0: not asked for)
+    int since = 0;                                 // groups of copies begun after its rows'
+    copy_rows(a, j0, rows, xs, row_bytes);
+    cp_async_commit();
     const uint32_t ring0 = ring + lane * 16, ring1 = ring0 + (S - 1) * SLOT;  // the first and the last slot
-#pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch(ring0 + i * SLOT);
+    if (!F32 && a.dtype == MOE_DTYPE_F16)
+        for (int i = tid; i < a.stage_rows; i += blockDim.x) back[i] = 1.0f;
 
-    int cur = -1, j0 = 0, rows = 0, nt = 0, buf = 0;
+    int cur = -1, nt = 0, buf = 0;
     uint32_t slot = ring0, free_slot = ring1, at[NTM];  // the slot to read, and the one read before it
     // the lane's scales and zero points, from its 16 bytes of codes
     const int sc_off = 1024 + g * 4 * NB - lane * 16, zp_off = 1024 + 32 * NB + g * 2 * NB - lane * 16;
     const uint32_t x0 = (uint32_t)(xs - smem);
     const int sh = a.pair ? 3 : 4;  // a tile's rows: 8 or 16
+    const bool sbf = a.scale_bf;
     int u = u0, tile0 = t0;
     while (todo > 0) {
         if (u != cur) {
+            if (cur < 0) {  // all but the weights asked for since
+                wait_all_but(S - 1);
+                __syncthreads();
+            } else if (next_at >= 0) {
+                if (since < 2)
+                    cp_async_wait<0>();
+                else
+                    cp_async_wait<2>();
+                __syncthreads();
+                j0 = next_j0, rows = next_rows, x_at = next_at;
+            } else {
+                rows = unit_rows(u, &j0), x_at = 0;
+                __syncthreads();
+                copy_rows(a, j0, rows, xs, row_bytes);
+                cp_async_commit();
+                cp_async_wait<0>();
+                __syncthreads();
+            }
             cur = u;
-            const int e = expert_of(u);
-            const int lo = a.expStart ? a.expStart[e] : 0, hi = a.expStart ? a.expStart[e + 1] : a.n_rows;
-            j0 = lo + (u - (a.expStart ? first[e] : 0)) * a.pass_rows;
-            rows = min(a.pass_rows, hi - j0);
+            if (F32) {
+                turn_rows<float>(a, rows, xs + x_at * row_bytes, row_bytes, back + x_at * cpr, top + x_at);
+                __syncthreads();
+            } else if (a.dtype == MOE_DTYPE_BF16) {
+                turn_rows<__nv_bfloat16>(a, rows, xs + x_at * row_bytes, row_bytes, back + x_at * cpr, top + x_at);
+                __syncthreads();
+            }
+            next_at = -1;
+            if (u < last_unit) {
+                next_rows = unit_rows(u + 1, &next_j0);
+                if (x_at + rows + next_rows <= a.stage_rows)
+                    next_at = x_at + rows;
+                else if (next_rows <= x_at)
+                    next_at = 0;
+                if (next_at >= 0) {
+                    copy_rows(a, next_j0, next_rows, xs + next_at * row_bytes, row_bytes);
+                    cp_async_commit();
+                    since = 0;
+                }
+            }
             const int cols = rows * cpr;
             nt = (cols + 7) >> 3;
 #pragma unroll
             for (int n = 0; n < NTM; ++n) {
                 const int c = min(n * 8 + g, cols - 1);
-                at[n] = x0 + (cpr == 2 ? (c >> 1) * row_bytes + (c & 1) * 16 : c * row_bytes) + t * 16 * cpr + wk * 8 * kb;
-            }
-            __syncthreads();
-            copy_rows(a, j0, rows, xs, row_bytes);
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncthreads();
-            if (a.dtype == MOE_DTYPE_F32) {
-                turn_rows<float>(a, rows, xs, row_bytes, back, top);
-                __syncthreads();
-            } else if (a.dtype == MOE_DTYPE_BF16) {
-                turn_rows<__nv_bfloat16>(a, rows, xs, row_bytes, back, top);
-                __syncthreads();
-            } else if (tid < rows) {
-                back[tid] = 1.0f;
+                at[n] = x0 + (F32 ? (x_at + (c >> 1)) * row_bytes + (c & 1) * 16 : (x_at + c) * row_bytes) + t * 16 * cpr +
+                        wk * 8 * KB;
             }
         }
         const int now = min(per, min(a.ntiles - tile0, todo)), tile = tile0 + wt;
@@ -526,28 +577,29 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
         if (wt < now) {
             uint32_t k0 = 0;
             for (int c = 0; c < per_tile; ++c) {
-                cp_async_wait<S - 2>();
+                wait_all_but(S - 2);
                 __syncwarp();
                 fetch(free_slot);  // every lane has read it before this point
+                ++since;
                 const bool both = !(odd && c == per_tile - 1);
                 if (NTM == 1 || nt == 1) {
-                    chunk_mma<G, ZP, SBF, 1, NTM>(smem, slot, slot + sc_off, slot + zp_off, at, k0, kb, sum);
+                    chunk_mma<G, ZP, F32, 1, NTM>(smem, slot, slot + sc_off, slot + zp_off, sbf, at, k0, sum);
                     if (both)
-                        chunk_mma<G, ZP, SBF, 1, NTM>(smem, slot + REC, slot + REC + sc_off, slot + REC + zp_off, at,
-                                                      k0 + 4 * kb, kb, sum);
+                        chunk_mma<G, ZP, F32, 1, NTM>(smem, slot + REC, slot + REC + sc_off, slot + REC + zp_off, sbf, at,
+                                                      k0 + 4 * KB, sum);
                 } else {
 #pragma unroll 1
                     for (int h = 0; h < 1 + both; ++h) {
-                        const uint32_t rec = slot + h * REC, k = k0 + h * 4 * kb;
-                        if (nt == 2)
-                            chunk_mma<G, ZP, SBF, NTM < 2 ? 1 : 2, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, kb, sum);
+                        const uint32_t rec = slot + h * REC, kh = k0 + h * 4 * KB;
+                        if (NTM == 2 || nt == 2)
+                            chunk_mma<G, ZP, F32, NTM < 2 ? 1 : 2, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, sum);
                         else if (nt == 3)
-                            chunk_mma<G, ZP, SBF, NTM < 3 ? 1 : 3, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, kb, sum);
+                            chunk_mma<G, ZP, F32, NTM < 3 ? 1 : 3, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, sum);
                         else
-                            chunk_mma<G, ZP, SBF, NTM, NTM>(smem, rec, rec + sc_off, rec + zp_off, at, k, kb, sum);
+                            chunk_mma<G, ZP, F32, NTM, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, sum);
                     }
                 }
-                k0 += a.wk * 8 * kb;
+                k0 += a.wk * 8 * KB;
                 free_slot = slot;
                 slot = slot == ring1 ? ring0 : slot + SLOT;
             }
@@ -589,10 +641,10 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 for (int h = 0; h < 2; ++h) {
                     const int c = n * 8 + 2 * t + h, j = cpr == 2 ? c >> 1 : c;
                     if ((cpr == 2 && h) || j >= rows) continue;
-                    float v0 = __fmul_rn(sum[n][h], back[c]), v1 = __fmul_rn(sum[n][2 + h], back[c]);
+                    float v0 = __fmul_rn(sum[n][h], back[x_at * cpr + c]), v1 = __fmul_rn(sum[n][2 + h], back[x_at * cpr + c]);
                     if (cpr == 2) {
-                        v0 = __fmaf_rn(sum[n][1], back[c + 1], v0);
-                        v1 = __fmaf_rn(sum[n][3], back[c + 1], v1);
+                        v0 = __fmaf_rn(sum[n][1], back[x_at * cpr + c + 1], v0);
+                        v1 = __fmaf_rn(sum[n][3], back[x_at * cpr + c + 1], v1);
                     }
                     const int64_t to = (int64_t)(j0 + j) * a.y_stride;
                     if (a.pair) {
@@ -642,6 +694,7 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
                      int n_rows, void *y, int64_t y_stride, unsigned *status, cudaStream_t s) {
     W4Args a{};
     a.records = w->records;
+    a.scale_bf = w->scale_dtype == MOE_DTYPE_BF16;
     a.pair = w->pair;
     a.E = w->E;
     a.R = w->R;
@@ -666,20 +719,20 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     const int64_t tiles = (int64_t)a.ntiles * a.E;
     const int pairs = (a.nchunk + 1) / 2;
     int wk = 1;
-    while (wk < 8 && wk < pairs && tiles * wk < (int64_t)sms * 16 * 6) wk *= 2;
+    while (wk < 8 && wk < pairs && tiles * wk < (int64_t)sms * 16 * W4_TURNS) wk *= 2;
     a.wk = wk;
-    // shared memory of a CTA
-    auto smem_for = [&](int rows, int warps, int bufs) {
-        const size_t nt = (rows * cpr + 7) / 8;
-        return (size_t)warps * W4_SLOTS * 2 * record + (wk > 1 ? (size_t)bufs * warps * nt * 512 : 0) +
-               row_bytes * rows + (size_t)(w->E + 1) * 4;
-    };
     struct Shape {
-        int warps, ctas, bufs;  // CTAs an SM
+        int warps, ctas, slots, bufs;  // CTAs an SM
+    };
+    const size_t per_row = row_bytes + 4 * cpr + 4;
+    auto smem_for = [&](int rows, const Shape &o) {  // of a CTA
+        const size_t nt = (rows * cpr + 7) / 8;
+        return (size_t)o.warps * o.slots * 2 * record + (wk > 1 ? (size_t)o.bufs * o.warps * nt * 512 : 0) +
+               per_row * rows + (size_t)(w->E + 1) * 4;
     };
     auto fit = [&](const Shape &o) {  // most rows a pass
         int rows = 32 / cpr;
-        while (rows > 0 && smem_for(rows, o.warps, o.bufs) > W4_SMEM_SM / o.ctas - 1536) --rows;
+        while (rows > 0 && smem_for(rows, o) > W4_SMEM_SM / o.ctas - 1536) --rows;
         return rows;
     };
     // Rows wanted a pass: all of a single matrix; of many experts twice the mean, their segments being uneven (a
@@ -687,9 +740,9 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     const int want = std::min({32 / cpr, n_rows, w->E == 1 ? n_rows : std::max(8 / cpr, 2 * ((n_rows + w->E - 1) / w->E))});
     // Two CTAs of 8 warps an SM where their rows fit; one of 16, the rows staged once, where they are long and that
     // saves passes; one of 8 for the longest.
-    Shape shape{8, 2, 2};
+    Shape shape{8, 2, 3, 2};
     int rows = std::min(want, fit(shape));
-    for (const Shape &o : {Shape{16, 1, 2}, Shape{16, 1, 1}, Shape{8, 1, 1}}) {
+    for (const Shape &o : {Shape{16, 1, 3, 2}, Shape{16, 1, 2, 1}, Shape{8, 1, 3, 1}}) {
         const int more = std::min(want, fit(o));
         if (more > 0 && (rows == 0 || (n_rows + more - 1) / more < (n_rows + rows - 1) / rows)) shape = o, rows = more;
     }
@@ -698,28 +751,36 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     a.pass_rows = rows;
     a.nt_max = (rows * cpr + 7) / 8;
     a.bufs = wk > 1 ? shape.bufs : 0;
+    if ((int64_t)a.ntiles * (w->E == 1 ? (n_rows + rows - 1) / rows : n_rows / rows + std::min(n_rows, w->E)) >= 0x7fffffff)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
     const int per = shape.warps / wk;
     const int64_t most = (int64_t)((a.ntiles + per - 1) / per) *
                          (w->E == 1 ? (n_rows + rows - 1) / rows : (int64_t)n_rows);
     const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)sms * shape.ctas);
-    const size_t smem = smem_for(rows, shape.warps, shape.bufs);
+    // room for the rows of the next experts beside those at work
+    const size_t used = smem_for(rows, shape), room = W4_SMEM_SM / shape.ctas - 1536;
+    const int64_t units = w->E == 1 ? (n_rows + rows - 1) / rows : n_rows;
+    a.stage_rows = (int)std::min<int64_t>({(int64_t)n_rows, units * rows, rows + (int64_t)((room - used) / per_row)});
+    a.slots = shape.slots;
+    const size_t smem = used + per_row * (a.stage_rows - rows);
     auto go = [&](auto kernel, SmemOptIn *done) {
         int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, done);
         if (rc) return rc;
         kernel<<<grid, shape.warps * 32, smem, s>>>(a);
         return launch_status();
     };
-    auto by_types = [&](auto gc, auto zc, auto bc) {
+    auto by_types = [&](auto gc, auto zc, auto fc) {
         constexpr int G = decltype(gc)::value;
-        constexpr bool ZP = decltype(zc)::value, SBF = decltype(bc)::value;
-        static SmemOptIn d[2];
-        return a.nt_max > 1 ? go(w4_kernel<G, ZP, SBF, 4>, &d[0]) : go(w4_kernel<G, ZP, SBF, 1>, &d[1]);
+        constexpr bool ZP = decltype(zc)::value, F32 = decltype(fc)::value;
+        static SmemOptIn d[3];
+        if (a.nt_max == 1) return go(w4_kernel<G, ZP, F32, 1>, &d[0]);
+        return a.nt_max == 2 ? go(w4_kernel<G, ZP, F32, 2>, &d[1]) : go(w4_kernel<G, ZP, F32, 4>, &d[2]);
     };
-    auto by_zeros = [&](auto gc, auto bc) {
-        return w->zeros ? by_types(gc, std::true_type(), bc) : by_types(gc, std::false_type(), bc);
+    auto by_zeros = [&](auto gc, auto fc) {
+        return w->zeros ? by_types(gc, std::true_type(), fc) : by_types(gc, std::false_type(), fc);
     };
     auto by_group = [&](auto gc) {
-        return w->scale_dtype == MOE_DTYPE_BF16 ? by_zeros(gc, std::true_type()) : by_zeros(gc, std::false_type());
+        return dtype == MOE_DTYPE_F32 ? by_zeros(gc, std::true_type()) : by_zeros(gc, std::false_type());
     };
     switch (w->group) {
         case 32: return by_group(std::integral_constant<int, 32>());

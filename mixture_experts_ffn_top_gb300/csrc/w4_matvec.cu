@@ -747,7 +747,13 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
         if (more > 0 && (rows == 0 || (n_rows + more - 1) / more < (n_rows + rows - 1) / rows)) shape = o, rows = more;
     }
     if (rows == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (w->E == 1) rows = (n_rows + (n_rows + rows - 1) / rows - 1) / ((n_rows + rows - 1) / rows);
+    if (w->E == 1) {
+        const int one = 8 / cpr;  // a column tile
+        // few tiles: a CTA for each of them and each column tile of rows, as long as all run at once (the weights
+        // come from L2 again, but no CTA stages all rows)
+        if (rows > one && (int64_t)a.ntiles * ((n_rows + one - 1) / one) <= (int64_t)sms * shape.ctas) rows = one;
+        rows = (n_rows + (n_rows + rows - 1) / rows - 1) / ((n_rows + rows - 1) / rows);
+    }
     a.pass_rows = rows;
     a.nt_max = (rows * cpr + 7) / 8;
     a.bufs = wk > 1 ? shape.bufs : 0;

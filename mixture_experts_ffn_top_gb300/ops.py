@@ -682,7 +682,7 @@ def moe_sort_tokens(x, topk_idx, E, ws, rows=None, stream=None):
     start = torch.empty(E + 1, dtype=torch.int32, device=device)
     tok = torch.empty(N * k, dtype=torch.int32, device=device)
     slot = torch.empty(N * k, dtype=torch.int32, device=device)
-    row = torch.empty((N, k), dtype=torch.int32, device=device)
+    row = torch.empty_like(topk_idx)
     _on(dev, stream, "moe_sort_tokens", xp, xs, DTYPES[x.dtype], ip, N, k, E, D, start.data_ptr(), tok.data_ptr(),
         slot.data_ptr(), row.data_ptr(), rp, *_ws(ws, dev))
     return rows, start, tok, slot, row

@@ -602,12 +602,13 @@ size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
  *            rows from expStart[E] on are left as they were.  NULL (E == 1 only):
  *            every row is expert 0's.  Offsets that do not start at 0, decrease or
  *            pass n_rows set MOE_DEV_BAD_CSR and every row is left.
- * Codes less zero points are exact, and so are fp16 rows; bf16 rows are kept down to 2^-29 of their
- * largest magnitude (2^-40 of it is lost of smaller values), fp32 rows to 2^-22 of each value.  Products
- * are summed in fp32 per group and the groups' sums, times their scales, in fp32, in an order that the
- * weights' shape and the type fix: a row's result does not depend on the rows beside it.  Made for few
- * rows an expert (decode): each 32 rows (fp32: 16) of an expert read its weights once more, and fewer
- * where K is long.
+ * Codes less zero points are exact, and so are fp16 rows; bf16 rows are exact down to 2^-29 of their
+ * largest magnitude (smaller values lose at most 2^-40 of it); of fp32 rows at most 2^-22 of each value, or
+ * 2^-50 of the row's largest, is lost.  Products are summed in fp32 per group and the groups' sums, times
+ * their scales, in fp32, in an order that the weights' shape and the type fix: a row's result does not
+ * depend on the rows beside it.  An infinity or NaN stays in its row.  Made for few rows an expert
+ * (decode): each 32 rows (fp32: 16) of an expert read its weights once more, and fewer where K is long.
+ * MOE_ERR_UNSUPPORTED_SHAPE past 2^31 pairs of 16 weight rows and such a pass.
  *   ws: status word (256 bytes). */
 int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype,
                   const int32_t *expStart, int n_rows, void *y, int64_t y_stride, void *ws,

@@ -35,6 +35,7 @@ constexpr int SORT_ONE_PASS = 4096;       // entries that every CTA counts by it
 constexpr int SORT_SCAN_E = 256;          // experts from which the table is summed by a kernel of its own: 2048
                                           // tokens over 1024 experts 19 us, summed by every CTA 55
 constexpr int SORT_RING = 12 * 1024;      // shared memory of a warp's rows in flight
+constexpr int SORT_SMEM = 216 * 1024;      // a CTA's shared memory at most, beside its static 9 KB
 constexpr int SORT_SLOTS = 4;             // at most this many of them
 constexpr int SORT_POS = 2048;            // entries of a range whose rows wait in shared memory
 constexpr unsigned long long SORT_WAIT_NS = 2000000000ull;
@@ -616,7 +617,7 @@ int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t
     // the ring holds at two a warp, of equal size
     const int shares = std::min(SORT_WARPS, (tokens * top_k + 31) / 32);
     const int counts = (2 + shares) * E * 4;
-    const int ring = std::min(SORT_RING, (216 * 1024 - counts) / SORT_WARPS / 256 * 256);
+    const int ring = std::min(SORT_RING, (SORT_SMEM - counts) / SORT_WARPS / 256 * 256);
     const int np = (row_bytes + ring / 2 - 1) / (ring / 2);
     const int piece = ((row_bytes + np - 1) / np + 15) / 16 * 16;
     const int slots = std::min(SORT_SLOTS, ring / piece);
@@ -633,7 +634,8 @@ int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t
     const char *xc = static_cast<const char *>(x);
     char *out = static_cast<char *>(rows);
     auto go = [&](auto kernel, SmemOptIn *done) {
-        int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, done);
+        // one limit for every call, so that calls at once from two threads set the same
+        int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), SORT_SMEM, done);
         if (rc) return rc;
         if (how != COUNT_HERE)
             return launch_early(kernel, dim3(ranges), dim3(SORT_THREADS), smem, s, xc, xb, idx, n, tokens, top_k, E,

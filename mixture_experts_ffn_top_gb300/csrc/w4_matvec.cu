@@ -770,7 +770,8 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     a.slots = shape.slots;
     const size_t smem = used + per_row * (a.stage_rows - rows);
     auto go = [&](auto kernel, SmemOptIn *done) {
-        int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, done);
+        // one limit for every call, so that calls at once from two threads set the same
+        int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), W4_SMEM_SM - 1024, done);
         if (rc) return rc;
         kernel<<<grid, shape.warps * 32, smem, s>>>(a);
         return launch_status();

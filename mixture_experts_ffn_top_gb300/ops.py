@@ -595,7 +595,8 @@ def moe_workspace_views(ws, N, D, E, F, top_k, Fs=0):
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # MOE_DTYPE_*
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(device).cuda_stream, without the object
+# torch.cuda.current_stream(device).cuda_stream, without the object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(device: int, stream, name: str, *args) -> None:
@@ -614,6 +615,14 @@ def _on(device: int, stream, name: str, *args) -> None:
             rc = f(*args, raw)
     if rc != 0:
         raise MoeError(rc, name)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor, of `stream`'s memory where one is given (the call writes it there)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _arg(t: torch.Tensor, dtype, shape, device: int, name: str) -> int:
@@ -656,7 +665,7 @@ def moe_sort_workspace_size(N, top_k, E) -> int:
 
 def new_sort_workspace(N, top_k, E, device="cuda", stream=None) -> torch.Tensor:
     """A workspace for moe_sort_tokens of that shape (and for every other function of this section)."""
-    ws = torch.empty(moe_sort_workspace_size(N, top_k, E), dtype=torch.uint8, device=device)
+    ws = _new(moe_sort_workspace_size(N, top_k, E), torch.uint8, device, stream)
     dev = ws.get_device()
     _on(dev, stream, "moe_workspace_init", ws.data_ptr(), ws.numel())
     return ws
@@ -677,12 +686,12 @@ def moe_sort_tokens(x, topk_idx, E, ws, rows=None, stream=None):
     k, dev, device = topk_idx.shape[1], x.get_device(), x.device
     ip = _arg(topk_idx, torch.int32, topk_idx.shape, dev, "topk_idx")
     if rows is None:
-        rows = torch.empty((N * k, D), dtype=x.dtype, device=device)
+        rows = _new((N * k, D), x.dtype, device, stream)
     rp = _arg(rows, x.dtype, (N * k, D), dev, "rows")
-    start = torch.empty(E + 1, dtype=torch.int32, device=device)
-    tok = torch.empty(N * k, dtype=torch.int32, device=device)
-    slot = torch.empty(N * k, dtype=torch.int32, device=device)
-    row = torch.empty_like(topk_idx)
+    start = _new(E + 1, torch.int32, device, stream)
+    tok = _new(N * k, torch.int32, device, stream)
+    slot = _new(N * k, torch.int32, device, stream)
+    row = _new((N, k), torch.int32, device, stream)
     _on(dev, stream, "moe_sort_tokens", xp, xs, DTYPES[x.dtype], ip, N, k, E, D, start.data_ptr(), tok.data_ptr(),
         slot.data_ptr(), row.data_ptr(), rp, *_ws(ws, dev))
     return rows, start, tok, slot, row
@@ -696,7 +705,7 @@ def moe_sort_tokens_grad(d_rows, tokRow, ws, d_x=None, stream=None):
     (n, D), (N, k) = d_rows.shape, tokRow.shape
     dp = _arg(d_rows, d_rows.dtype, (n, D), dev, "d_rows")
     if d_x is None:
-        d_x = torch.empty((N, D), dtype=d_rows.dtype, device=d_rows.device)
+        d_x = _new((N, D), d_rows.dtype, d_rows.device, stream)
     xp, xs = _rows_arg(d_x, "d_x", d_rows.dtype, (N, D), dev)
     _on(dev, stream, "moe_sort_tokens_grad", dp, n, DTYPES[d_rows.dtype], _arg(tokRow, torch.int32, (N, k), dev, "tokRow"),
         N, k, D, xp, xs, *_ws(ws, dev))
@@ -711,7 +720,7 @@ def moe_unsort_tokens(rows, tokRow, topk_w, ws, out=None, stream=None):
     (n, D), (N, k) = rows.shape, tokRow.shape
     rp = _arg(rows, rows.dtype, (n, D), dev, "rows")
     if out is None:
-        out = torch.empty((N, D), dtype=rows.dtype, device=rows.device)
+        out = _new((N, D), rows.dtype, rows.device, stream)
     op, os_ = _rows_arg(out, "out", rows.dtype, (N, D), dev)
     _on(dev, stream, "moe_unsort_tokens", rp, n, DTYPES[rows.dtype], _arg(tokRow, torch.int32, (N, k), dev, "tokRow"),
         _arg(topk_w, torch.float32, (N, k), dev, "topk_w"), N, k, D, op, os_, *_ws(ws, dev))
@@ -728,9 +737,9 @@ def moe_unsort_tokens_grad(d_out, rows, tokRow, topk_w, ws, d_rows=None, stream=
     rp = _arg(rows, rows.dtype, (n, D), dev, "rows")
     gp, gs = _rows_arg(d_out, "d_out", rows.dtype, (N, D), dev)
     if d_rows is None:
-        d_rows = torch.empty((n, D), dtype=rows.dtype, device=rows.device)
+        d_rows = _new((n, D), rows.dtype, rows.device, stream)
     dp = _arg(d_rows, rows.dtype, (n, D), dev, "d_rows")
-    d_w = torch.empty((N, k), dtype=torch.float32, device=rows.device)
+    d_w = _new((N, k), torch.float32, rows.device, stream)
     _on(dev, stream, "moe_unsort_tokens_grad", gp, gs, rp, n, DTYPES[rows.dtype],
         _arg(tokRow, torch.int32, (N, k), dev, "tokRow"), _arg(topk_w, torch.float32, (N, k), dev, "topk_w"), N, k, D,
         dp, d_w.data_ptr(), *_ws(ws, dev))
@@ -745,7 +754,7 @@ def moe_topk_grad(logits, topk_idx, d_topk_w, norm_topk_prob, ws, d_logits=None,
     (N, E), k = logits.shape, topk_idx.shape[1]
     lp = _arg(logits, torch.float32, (N, E), dev, "logits")
     if d_logits is None:
-        d_logits = torch.empty((N, E), dtype=torch.float32, device=logits.device)
+        d_logits = _new((N, E), torch.float32, logits.device, stream)
     _on(dev, stream, "moe_topk_grad", lp, _arg(topk_idx, torch.int32, (N, k), dev, "topk_idx"),
         _arg(d_topk_w, torch.float32, (N, k), dev, "d_topk_w"), N, E, k, int(norm_topk_prob),
         _arg(d_logits, torch.float32, (N, E), dev, "d_logits"), *_ws(ws, dev))
@@ -835,7 +844,7 @@ def moe_w4_matvec(w: MoeW4Weights, x, expStart, ws, y=None, stream=None):
     xp, xs = _rows_arg(x, "x", None, None, dev)
     sp = None if expStart is None else _arg(expStart, torch.int32, (w.E + 1,), dev, "expStart")
     if y is None:
-        y = torch.empty((n, w.R), dtype=x.dtype, device=x.device)
+        y = _new((n, w.R), x.dtype, x.device, stream)
     yp, ys = _rows_arg(y, "y", x.dtype, (n, w.R), dev)
     _on(dev, stream, "moe_w4_matvec", w.handle, xp, xs, DTYPES[x.dtype], sp, n, yp, ys, *_ws(ws, dev))
     return y

@@ -87,6 +87,7 @@ SHAPES = [  # N, D, E, k, drop, pad, shift
     (64, 256, 8, 2, 0.0, 0, 0), (130, 1001, 60, 6, 0.25, 0, 0), (153, 40, 1024, 32, 0.1, 0, 0),
     (300, 72, 17, 17, 0.5, 8, 0), (511, 520, 128, 8, 0.0, 1, 0), (700, 96, 33, 4, 0.9, 0, 1), (2048, 2048, 64, 8, 0.0, 0, 0),
     (1537, 136, 300, 12, 0.05, 24, 3), (5000, 16, 3, 2, 0.2, 0, 0), (97, 9000, 4, 2, 0.0, 0, 0),
+    (3000, 37, 20, 3, 0.1, 0, 0), (2500, 44, 256, 2, 0.0, 2, 2),
 ]
 
 
@@ -431,6 +432,55 @@ def test_replayed_graph_and_side_stream(ops):
     side.synchronize()
     n = int((idx >= 0).sum())
     assert torch.equal(got[:n], ops.moe_sort_tokens(x, idx, E, ws)[0][:n])
+
+
+def test_two_threads_at_once(ops):
+    """Calls from two host threads, each on a stream and with a workspace of its own."""
+    import threading
+
+    got = {}
+
+    def work(seed):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            ws = ops.new_sort_workspace(3000, 4, 400)
+            for i in range(10):
+                E = (400, 12)[i % 2]
+                idx = routing(3000, E, 4, 0.1, seed + i)
+                x = values((3000, 64 + 8 * i), torch.bfloat16, seed)
+                rows, start, tok, _, row = ops.moe_sort_tokens(x, idx, E, ws)
+                w = torch.ones((3000, 4), device="cuda")
+                out = ops.moe_unsort_tokens(rows, row, w, ws)
+                kept = (idx >= 0).sum(1, keepdim=True)
+                got[seed, i] = bool(torch.equal(out, (x.float() * kept).bfloat16())) and int(start[-1]) == int(kept.sum())
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in (100, 200)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 20 and all(got.values())
+
+
+def test_stream_argument(ops):
+    """Work and outputs follow the stream that is passed, whatever the current one is."""
+    x, idx = values((900, 72), torch.float16, 1), routing(900, 20, 4, 0.1)
+    ws = ops.new_sort_workspace(900, 4, 20)
+    want = ops.moe_sort_tokens(x, idx, 20, ws)
+    n = int(want[1][-1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ops.moe_sort_tokens(x, idx, 20, ws, stream=side)
+    w = torch.rand((900, 4), generator=gen(2), device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    out = ops.moe_unsort_tokens(got[0], got[4], w, ws, stream=side)
+    d_rows, d_w = ops.moe_unsort_tokens_grad(out, got[0], got[4], w, ws, stream=side)
+    d_x = ops.moe_sort_tokens_grad(got[0], got[4], ws, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0][:n], want[0][:n]) and all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+    assert torch.equal(out, ops.moe_unsort_tokens(want[0], want[4], w, ws))
+    assert torch.equal(d_w, ops.moe_unsort_tokens_grad(out, want[0], want[4], w, ws)[1])
+    assert torch.equal(d_x, ops.moe_sort_tokens_grad(want[0], want[4], ws))
 
 
 def test_rows_past_32_bit_offsets(ops):

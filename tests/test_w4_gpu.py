@@ -132,6 +132,62 @@ def test_product(ops, E, R, K, G, rows, dtype, sdtype, zeros, pair):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_rows_at_any_address_and_stride(ops, dtype):
+    """Rows that 16-byte loads cannot take, one row for all (stride 0), and outputs at odd strides give the bits of
+    contiguous ones."""
+    mat = matrix(3, 50, 352, 32, F16, True, 1)
+    w = ops.MoeW4Weights(*mat)
+    es = torch.tensor([0, 4, 4, 21], dtype=torch.int32, device="cuda")
+    ws = ops.new_sort_workspace(1, 1, 1)
+    x = torch.randn((21, 352), generator=gen(2), device="cuda").to(dtype)
+    want = ops.moe_w4_matvec(w, x, es, ws)
+    for pad, shift in ((0, 1), (1, 0), (5, 3), (8, 8)):
+        buf = torch.full((21 * (352 + pad) + shift,), float("nan"), dtype=dtype, device="cuda")
+        v = buf[shift:].view(21, 352 + pad)[:, :352]
+        v.copy_(x)
+        y = torch.empty((21, 50 + pad), dtype=dtype, device="cuda")[:, :50]
+        assert torch.equal(ops.moe_w4_matvec(w, v, es, ws, y=y), want)
+    one = x[:1].expand(21, 352)
+    assert torch.equal(ops.moe_w4_matvec(w, one, es, ws), ops.moe_w4_matvec(w, one.contiguous(), es, ws))
+    assert ops.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_a_row_does_not_depend_on_the_rows_beside_it(ops, dtype):
+    """One matrix with and without offsets, and any number of rows at once: the same bits."""
+    for R, K, G in ((2048, 2048, 128), (40, 640, 64), (20000, 256, 32)):
+        w = ops.MoeW4Weights(*matrix(1, R, K, G, BF16, False, 1))
+        ws = ops.new_sort_workspace(1, 1, 1)
+        x = torch.randn((70, K), generator=gen(2), device="cuda").to(dtype)
+        every = ops.moe_w4_matvec(w, x, None, ws)
+        for a, b in ((0, 1), (3, 5), (0, 8), (10, 27), (31, 64)):
+            assert torch.equal(ops.moe_w4_matvec(w, x[a:b], None, ws), every[a:b])
+        y = torch.full_like(every, 5.0)
+        ops.moe_w4_matvec(w, x, torch.tensor([0, 33], dtype=torch.int32, device="cuda"), ws, y=y)
+        assert torch.equal(y[:33], every[:33]) and torch.all(y[33:] == 5.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_rows_of_many_magnitudes(ops, dtype):
+    """Values over 60 binades in one row: each is kept to 2^-22 of itself (bf16: exactly), or 2^-50 (2^-40) of the
+    row's largest; the sums' own bound is test_product's."""
+    R, K, G = 64, 512, 64
+    mat = matrix(1, R, K, G, F16, False, 1)
+    w = ops.MoeW4Weights(*mat)
+    x = (torch.randn((6, K), generator=gen(2), device="cuda") * 2.0 ** torch.randint(-40, 20, (6, K), generator=gen(3), device="cuda").float()).to(dtype)
+    x[5] = 0
+    y = ops.moe_w4_matvec(w, x, None, ops.new_sort_workspace(1, 1, 1))
+    ref, mag = product(mat, x, [0, 6])
+    lost = torch.zeros_like(x, dtype=torch.float64)
+    if dtype is F32:
+        lost = torch.maximum(x.double().abs() * 2.0 ** -22, x.double().abs().amax(1, keepdim=True) * 2.0 ** -50)
+    else:
+        lost += x.double().abs().amax(1, keepdim=True) * 2.0 ** -40
+    err = (17 * G / 8 + K / G + 35) * U * mag + lost @ dense(*mat)[0].abs().t()
+    close(y, ref, err + HALF[dtype] * (ref.abs() + err) * 1.001 + TINY[dtype])
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
 @pytest.mark.parametrize("G", [32, 64, 128])
 def test_small_integers_are_exact(ops, G, dtype):
     """Codes, zero points and scales at their ends with integer rows: every sum is an integer below 2^24

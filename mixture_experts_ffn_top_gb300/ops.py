@@ -597,6 +597,7 @@ DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # MOE_DTYPE_*
 
 # torch.cuda.current_stream(device).cuda_stream, without the object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _on(device: int, stream, name: str, *args) -> None:
@@ -608,7 +609,7 @@ def _on(device: int, stream, name: str, *args) -> None:
     else:
         raw = stream.cuda_stream
     f = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         rc = f(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -672,7 +673,9 @@ def new_sort_workspace(N, top_k, E, device="cuda", stream=None) -> torch.Tensor:
 
 
 def _ws(ws: torch.Tensor, device: int) -> tuple[int, int]:
-    return _arg(ws, torch.uint8, ws.shape, device, "ws"), ws.numel()
+    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+        _arg(ws, torch.uint8, ws.shape, device, "ws")
+    return ws.data_ptr(), ws.numel()
 
 
 def moe_sort_tokens(x, topk_idx, E, ws, rows=None, stream=None):
@@ -687,7 +690,9 @@ def moe_sort_tokens(x, topk_idx, E, ws, rows=None, stream=None):
     ip = _arg(topk_idx, torch.int32, topk_idx.shape, dev, "topk_idx")
     if rows is None:
         rows = _new((N * k, D), x.dtype, device, stream)
-    rp = _arg(rows, x.dtype, (N * k, D), dev, "rows")
+        rp = rows.data_ptr()
+    else:
+        rp = _arg(rows, x.dtype, (N * k, D), dev, "rows")
     start = _new(E + 1, torch.int32, device, stream)
     tok = _new(N * k, torch.int32, device, stream)
     slot = _new(N * k, torch.int32, device, stream)
@@ -706,7 +711,9 @@ def moe_sort_tokens_grad(d_rows, tokRow, ws, d_x=None, stream=None):
     dp = _arg(d_rows, d_rows.dtype, (n, D), dev, "d_rows")
     if d_x is None:
         d_x = _new((N, D), d_rows.dtype, d_rows.device, stream)
-    xp, xs = _rows_arg(d_x, "d_x", d_rows.dtype, (N, D), dev)
+        xp, xs = d_x.data_ptr(), D
+    else:
+        xp, xs = _rows_arg(d_x, "d_x", d_rows.dtype, (N, D), dev)
     _on(dev, stream, "moe_sort_tokens_grad", dp, n, DTYPES[d_rows.dtype], _arg(tokRow, torch.int32, (N, k), dev, "tokRow"),
         N, k, D, xp, xs, *_ws(ws, dev))
     return d_x
@@ -721,7 +728,9 @@ def moe_unsort_tokens(rows, tokRow, topk_w, ws, out=None, stream=None):
     rp = _arg(rows, rows.dtype, (n, D), dev, "rows")
     if out is None:
         out = _new((N, D), rows.dtype, rows.device, stream)
-    op, os_ = _rows_arg(out, "out", rows.dtype, (N, D), dev)
+        op, os_ = out.data_ptr(), D
+    else:
+        op, os_ = _rows_arg(out, "out", rows.dtype, (N, D), dev)
     _on(dev, stream, "moe_unsort_tokens", rp, n, DTYPES[rows.dtype], _arg(tokRow, torch.int32, (N, k), dev, "tokRow"),
         _arg(topk_w, torch.float32, (N, k), dev, "topk_w"), N, k, D, op, os_, *_ws(ws, dev))
     return out
@@ -738,7 +747,9 @@ def moe_unsort_tokens_grad(d_out, rows, tokRow, topk_w, ws, d_rows=None, stream=
     gp, gs = _rows_arg(d_out, "d_out", rows.dtype, (N, D), dev)
     if d_rows is None:
         d_rows = _new((n, D), rows.dtype, rows.device, stream)
-    dp = _arg(d_rows, rows.dtype, (n, D), dev, "d_rows")
+        dp = d_rows.data_ptr()
+    else:
+        dp = _arg(d_rows, rows.dtype, (n, D), dev, "d_rows")
     d_w = _new((N, k), torch.float32, rows.device, stream)
     _on(dev, stream, "moe_unsort_tokens_grad", gp, gs, rp, n, DTYPES[rows.dtype],
         _arg(tokRow, torch.int32, (N, k), dev, "tokRow"), _arg(topk_w, torch.float32, (N, k), dev, "topk_w"), N, k, D,
@@ -755,9 +766,12 @@ def moe_topk_grad(logits, topk_idx, d_topk_w, norm_topk_prob, ws, d_logits=None,
     lp = _arg(logits, torch.float32, (N, E), dev, "logits")
     if d_logits is None:
         d_logits = _new((N, E), torch.float32, logits.device, stream)
+        gp = d_logits.data_ptr()
+    else:
+        gp = _arg(d_logits, torch.float32, (N, E), dev, "d_logits")
     _on(dev, stream, "moe_topk_grad", lp, _arg(topk_idx, torch.int32, (N, k), dev, "topk_idx"),
-        _arg(d_topk_w, torch.float32, (N, k), dev, "d_topk_w"), N, E, k, int(norm_topk_prob),
-        _arg(d_logits, torch.float32, (N, E), dev, "d_logits"), *_ws(ws, dev))
+        _arg(d_topk_w, torch.float32, (N, k), dev, "d_topk_w"), N, E, k, 1 if norm_topk_prob else 0,
+        gp, *_ws(ws, dev))
     return d_logits
 
 
@@ -845,7 +859,9 @@ def moe_w4_matvec(w: MoeW4Weights, x, expStart, ws, y=None, stream=None):
     sp = None if expStart is None else _arg(expStart, torch.int32, (w.E + 1,), dev, "expStart")
     if y is None:
         y = _new((n, w.R), x.dtype, x.device, stream)
-    yp, ys = _rows_arg(y, "y", x.dtype, (n, w.R), dev)
+        yp, ys = y.data_ptr(), w.R
+    else:
+        yp, ys = _rows_arg(y, "y", x.dtype, (n, w.R), dev)
     _on(dev, stream, "moe_w4_matvec", w.handle, xp, xs, DTYPES[x.dtype], sp, n, yp, ys, *_ws(ws, dev))
     return y
 

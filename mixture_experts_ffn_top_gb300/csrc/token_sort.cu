@@ -392,27 +392,26 @@ unsort_kernel(const T *__restrict__ rows, int64_t n_rows, const int32_t *__restr
 }
 
 // d_row = w * d_out and the dot d_w = <d_out, row> of one entry (t, s) at a time, by TPE threads: the rows are
-// read and written once, d_out's row comes from the caches for all but its first entry.  The dot: each thread's
-// columns in order, a butterfly over the warp, the warps in order.  2048 x 2048 bf16, top 8: 25.5 us (143 MB:
-// 83% of the copy rate); a token's threads holding all its entries at once took 35.8 us (registers, and a
-// reduction of eight dots through shared memory).
-template <typename T, int V, int TPE>
+// read and written once (evicted first: d_out's row comes from the caches for all but its first entry), UNROLL
+// accesses of each in flight.  The dot: each thread's columns in order, a butterfly over the warp, the warps in
+// order.  HBM-bound: 2048 x 2048 bf16, top 8: 23.2 us (143 MB: 91% of the copy rate; with plain stores 25.2).  A
+// token's threads holding all its entries at once took 35.8 us (registers, and a reduction of eight dots through
+// shared memory).
+template <typename T, int V, int TPE, int UNROLL>
 __global__ void __launch_bounds__(ROW_THREADS)
 unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *__restrict__ rows, int64_t n_rows,
                    const int32_t *__restrict__ tokRow, const float *__restrict__ w, int n_entries, int top_k, int D,
                    T *__restrict__ d_rows, float *__restrict__ d_w, unsigned *__restrict__ status) {
-    constexpr int UNROLL = 4;
     __shared__ float part[ROW_THREADS / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x & (TPE - 1);
     const int64_t i = (int64_t)blockIdx.x * (ROW_THREADS / TPE) + threadIdx.x / TPE;
-    if (i >= n_entries) return;  // whole warps; whole CTAs where TPE is the CTA
-    const int r = checked_row(tokRow[i], n_rows, status);
+    const int r = i < n_entries ? checked_row(tokRow[i], n_rows, status) : -1;
     float dot = 0.0f;
     if (r >= 0) {
         const float ws = w[i];
         const T *src = d_out + (i / top_k) * d_out_stride, *row = rows + (int64_t)r * D;
         T *dst = d_rows + (int64_t)r * D;
-        for (int c0 = (threadIdx.x & (TPE - 1)) * V; c0 < D; c0 += UNROLL * TPE * V) {
+        for (int c0 = me * V; c0 < D; c0 += UNROLL * TPE * V) {
             Pack<T, V> dv[UNROLL], rv[UNROLL];
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
@@ -434,14 +433,15 @@ unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *_
                         f[j] = __fmul_rn(ws, dv[u].get(j));
                     }
                     o.set(f);
-                    o.store(dst + c);
+                    o.store_once(dst + c);
                 }
             }
         }
     }
-    dot = warp_sum(dot);
-    if (TPE == 32) {
-        if (lane == 0) d_w[i] = dot;
+#pragma unroll
+    for (int o = (TPE < 32 ? TPE : 32) / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (TPE <= 32) {
+        if (me == 0 && i < n_entries) d_w[i] = dot;
     } else {
         if (lane == 0) part[warp] = dot;
         __syncthreads();
@@ -714,9 +714,12 @@ int launch_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const voi
                     (int)n, top_k, D, static_cast<T *>(d_rows), d_w, status);
                 return launch_status();
             };
-            // a warp an entry, or a CTA where the entries are few and their rows long
-            if (n < (int64_t)sms * 8 && cols > 64) return go(unsort_grad_kernel<T, V, ROW_THREADS>, 1);
-            return go(unsort_grad_kernel<T, V, 32>, ROW_THREADS / 32);
+            // Eight threads an entry where its row is short, a CTA where the entries are few and their rows long, else
+            // a warp.  Narrow accesses: more of them in flight (2048 x 1001 bf16 19.9 us with eight, 21.9 with four).
+            constexpr int U = sizeof(T) * V == 16 ? 4 : 8;
+            if (cols <= 32) return go(unsort_grad_kernel<T, V, 8, 4>, ROW_THREADS / 8);
+            if (n < (int64_t)sms * 8 && cols > 64) return go(unsort_grad_kernel<T, V, ROW_THREADS, U>, 1);
+            return go(unsort_grad_kernel<T, V, 32, U>, ROW_THREADS / 32);
         });
     });
 }

@@ -63,7 +63,6 @@ struct Pack {
     }
     __device__ __forceinline__ void load(const T *p) { a = *reinterpret_cast<const Access *>(p); }
     __device__ __forceinline__ void load_once(const T *p) { a = __ldcs(reinterpret_cast<const Access *>(p)); }
-    __device__ __forceinline__ void store_once(T *p) const { __stcs(reinterpret_cast<Access *>(p), a); }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Access *>(p) = a; }
 };
 

@@ -392,11 +392,12 @@ unsort_kernel(const T *__restrict__ rows, int64_t n_rows, const int32_t *__restr
 }
 
 // d_row = w * d_out and the dot d_w = <d_out, row> of one entry (t, s) at a time, by TPE threads: the rows are
-// read and written once (evicted first: d_out's row comes from the caches for all but its first entry), UNROLL
-// accesses of each in flight.  The dot: each thread's columns in order, a butterfly over the warp, the warps in
-// order.  HBM-bound: 2048 x 2048 bf16, top 8: 23.2 us (143 MB: 91% of the copy rate; with plain stores 25.2).  A
-// token's threads holding all its entries at once took 35.8 us (registers, and a reduction of eight dots through
-// shared memory).
+// read and written once (read to be evicted first: d_out's row comes from the caches for all but its first entry),
+// UNROLL accesses of each in flight.  The dot: each thread's columns in order, a butterfly over the warp, the warps
+// in order.  HBM-bound: 2048 x 2048 bf16, top 8: 25.3 us (143 MB: 83% of the copy rate).  Streaming stores take 23.2,
+// but leave less of d_rows in L2 for its reader: with the sort's gradient behind it 37.2 us against 35.1.  A token's
+// threads holding all its entries at once took 35.8 us (registers, and a reduction of eight dots through shared
+// memory).
 template <typename T, int V, int TPE, int UNROLL>
 __global__ void __launch_bounds__(ROW_THREADS)
 unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *__restrict__ rows, int64_t n_rows,
@@ -433,7 +434,7 @@ unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *_
                         f[j] = __fmul_rn(ws, dv[u].get(j));
                     }
                     o.set(f);
-                    o.store_once(dst + c);
+                    o.store(dst + c);
                 }
             }
         }
@@ -454,27 +455,38 @@ unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *_
 }
 
 // -------------------------------------------------------------- topk grad --
-// One warp per token, lane s on slot s: with p the softmax (over all experts, or over the selected ones) and
+// TPT threads a token, the s-th on slot s: with p the softmax (over all experts, or over the selected ones) and
 // c = sum_s p[idx_s] d_w_s,  d_l[e] = p[e] (v[e] - c), v[e] the sum of d_w over the slots of e: -p[e] c at every
 // expert that no slot names (0 with norm, where the other logits are not even read), then the slots' own values
-// over it.  VEC: four experts an access (E % 4 == 0, aligned).  EPL experts per lane (EPL * 32 >= E).
-// Latency and launch bound at a router's sizes: 2048 x 64 2.5 us; 16384 x 256 normalised 7.7 us (66%
-// of the copy rate over all logits and gradients; by comparing every slot with every expert, 20.8).
-template <int EPL, bool VEC>
+// over it.  VEC: four experts an access (E % 4 == 0, aligned).  EPL experts per thread (EPL * TPT >= E).
+// Latency and launch bound at a router's sizes (2048 x 64 2.5 us), issue-bound with many tokens: the slots' rounds and
+// the butterflies are the same for a warp's 32 / TPT tokens as for one.  16384 x 256 normalised 5.5 us (the logits
+// and gradients of all experts once are 5.1 us of the copy rate; only the gradients and the slots' logits move).
+template <int EPL, bool VEC, int TPT>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
 topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ d_w,
                  int N, int E, int top_k, int norm, float *d_logits, unsigned *__restrict__ status) {
-    const int lane = threadIdx.x & 31;
-    // the lane's i-th expert
-    auto expert = [&](int i) { return VEC ? 128 * (i / 4) + 4 * lane + i % 4 : 32 * i + lane; };
-    for (int64_t t = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); t < N; t += (int64_t)gridDim.x * ROW_WARPS) {
+    constexpr int PER = 32 / TPT;
+    const int lane = threadIdx.x & 31, me = lane & (TPT - 1);
+    const unsigned mine = (TPT == 32 ? 0xffffffffu : (1u << (TPT & 31)) - 1u) << (lane & ~(TPT - 1));
+    // the thread's i-th expert
+    auto expert = [&](int i) { return VEC ? 4 * TPT * (i / 4) + 4 * me + i % 4 : TPT * i + me; };
+    auto sum = [&](float v) {
+#pragma unroll
+        for (int o = TPT / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    for (int64_t t0 = ((int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5)) * PER; t0 < N;
+         t0 += (int64_t)gridDim.x * ROW_WARPS * PER) {
+        const int64_t t = t0 + lane / TPT;
+        const int experts = t < N ? E : 0;  // the last warp's threads without a token go along with the others
         const float *lt = logits + t * E;
         float *dt = d_logits + t * E;
         int e = -1;
         float d = 0.0f, ls = -INFINITY;
-        if (lane < top_k) {
-            e = idx[t * top_k + lane];
-            d = d_w[t * top_k + lane];
+        if (me < top_k && experts > 0) {
+            e = idx[t * top_k + me];
+            d = d_w[t * top_k + me];
             if (e < 0 || e >= E) {
                 if (e != -1) atomicOr(status, MOE_DEV_BAD_ROUTING);
                 e = -1;
@@ -487,10 +499,10 @@ topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ i
             for (int i = 0; i < EPL; i += VEC ? 4 : 1) {
                 if (VEC) {
                     float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    if (expert(i) < E) v = *reinterpret_cast<const float4 *>(lt + expert(i));
+                    if (expert(i) < experts) v = *reinterpret_cast<const float4 *>(lt + expert(i));
                     p[i] = v.x, p[(i + 1) % EPL] = v.y, p[(i + 2) % EPL] = v.z, p[(i + 3) % EPL] = v.w;
                 } else {
-                    p[i] = expert(i) < E ? lt[expert(i)] : -INFINITY;
+                    p[i] = expert(i) < experts ? lt[expert(i)] : -INFINITY;
                 }
             }
         }
@@ -499,11 +511,11 @@ topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ i
         float v = 0.0f;
         bool first = e >= 0;
         for (int s = 0; s < top_k; ++s) {
-            const int es = __shfl_sync(0xffffffffu, e, s);
-            const float ds = __shfl_sync(0xffffffffu, d, s);
+            const int es = __shfl_sync(0xffffffffu, e, s, TPT);
+            const float ds = __shfl_sync(0xffffffffu, d, s, TPT);
             if (es == e) {
                 v += ds;
-                first &= s >= lane;
+                first &= s >= me;
             }
         }
         float m = -INFINITY, z = 0.0f;
@@ -518,8 +530,9 @@ topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ i
                 nan |= p[i] != p[i];
             }
         }
-        m = warp_max(m);
-        nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+        for (int o = TPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        nan = (__ballot_sync(0xffffffffu, nan) & mine) != 0;
         const bool none = m == -INFINITY && !nan;  // nothing to take a softmax of
         float ps = e >= 0 && !none ? expf(ls - m) : 0.0f;
         if (norm) {
@@ -531,15 +544,17 @@ topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ i
                 z += p[i];
             }
         }
-        z = none ? 1.0f : warp_sum(z);
+        z = sum(z);  // by all of the warp, whose tokens may differ in `none`
+        if (none) z = 1.0f;
         ps = __fdiv_rn(ps, z);
-        const float c = warp_sum(e >= 0 ? __fmul_rn(ps, d) : 0.0f);
+        const float c = sum(e >= 0 ? __fmul_rn(ps, d) : 0.0f);
+        const float rest = __fdiv_rn(-c, z);  // of an expert without a slot, per exponential
 #pragma unroll
         for (int i = 0; i < EPL; i += VEC ? 4 : 1) {
-            if (expert(i) >= E) continue;
+            if (expert(i) >= experts) continue;
             float o[4];
 #pragma unroll
-            for (int q = 0; q < (VEC ? 4 : 1); ++q) o[q] = norm || none ? 0.0f : __fmul_rn(__fdiv_rn(p[(i + q) % EPL], z), -c);
+            for (int q = 0; q < (VEC ? 4 : 1); ++q) o[q] = norm || none ? 0.0f : __fmul_rn(p[(i + q) % EPL], rest);
             if (VEC)
                 *reinterpret_cast<float4 *>(dt + expert(i)) = make_float4(o[0], o[1], o[2], o[3]);
             else
@@ -572,11 +587,6 @@ int log2_ceil(int64_t n, int most) {
     int l = 0;
     while (l < most && ((int64_t)1 << l) < n) ++l;
     return l;
-}
-
-unsigned row_grid(int64_t N) {
-    const int64_t cap = (int64_t)std::max(1, device_sm_count()) * 8;
-    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((N + ROW_WARPS - 1) / ROW_WARPS, cap));
 }
 
 // Calls f with a null pointer of the element type.
@@ -715,7 +725,7 @@ int launch_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const voi
                 return launch_status();
             };
             // Eight threads an entry where its row is short, a CTA where the entries are few and their rows long, else
-            // a warp.  Narrow accesses: more of them in flight (2048 x 1001 bf16 19.9 us with eight, 21.9 with four).
+            // a warp.  Narrow accesses: more of them in flight (2048 x 1001 bf16 19.6 us with eight, 21.9 with four).
             constexpr int U = sizeof(T) * V == 16 ? 4 : 8;
             if (cols <= 32) return go(unsort_grad_kernel<T, V, 8, 4>, ROW_THREADS / 8);
             if (n < (int64_t)sms * 8 && cols > 64) return go(unsort_grad_kernel<T, V, ROW_THREADS, U>, 1);
@@ -726,23 +736,34 @@ int launch_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const voi
 
 int launch_topk_grad(const float *logits, const int32_t *idx, const float *d_w, int N, int E, int top_k, int norm,
                      float *d_logits, unsigned *status, cudaStream_t s) {
-    auto go = [&](auto kernel) {
-        kernel<<<row_grid(N), ROW_WARPS * 32, 0, s>>>(logits, idx, d_w, N, E, top_k, norm, d_logits, status);
+    auto go = [&](auto kernel, int tpt) {
+        const int64_t per = ROW_WARPS * 32 / tpt, cap = (int64_t)std::max(1, device_sm_count()) * 8;
+        kernel<<<(unsigned)std::max<int64_t>(1, std::min<int64_t>((N + per - 1) / per, cap)), ROW_WARPS * 32, 0, s>>>(
+            logits, idx, d_w, N, E, top_k, norm, d_logits, status);
         return launch_status();
     };
-    // below 128 experts a lane's access of four would leave lanes without any (2048 x 64: 2.8 us, single ones 2.5)
-    if (E >= 128 && access_bytes({logits, d_logits}, {(int64_t)E * 4}) == 16) {
-        if (E <= 128) return go(topk_grad_kernel<4, true>);
-        if (E <= 256) return go(topk_grad_kernel<8, true>);
-        if (E <= 512) return go(topk_grad_kernel<16, true>);
-        return go(topk_grad_kernel<32, true>);
-    }
-    if (E <= 32) return go(topk_grad_kernel<1, false>);
-    if (E <= 64) return go(topk_grad_kernel<2, false>);
-    if (E <= 128) return go(topk_grad_kernel<4, false>);
-    if (E <= 256) return go(topk_grad_kernel<8, false>);
-    if (E <= 512) return go(topk_grad_kernel<16, false>);
-    return go(topk_grad_kernel<32, false>);
+    // Few threads a token share the issue slots best, more answer a small batch sooner (8, 16 and 32 threads:
+    // 16384 x 64 3.9, 5.0 and 8.5 us, 16384 x 256 normalised 5.5, 6.9 and 8.1; 2048 x 128 3.2, 2.9 and 2.8).
+    const bool many = N >= std::max(1, device_sm_count()) * 32;
+    auto by_shape = [&](auto vec) {
+        constexpr bool V = decltype(vec)::value;
+        if (many && top_k <= 8 && E <= 256) {
+            if (E <= 64) return go(topk_grad_kernel<8, V, 8>, 8);
+            if (E <= 128) return go(topk_grad_kernel<16, V, 8>, 8);
+            return go(topk_grad_kernel<32, V, 8>, 8);
+        }
+        if (top_k <= 16 && E <= 256) {
+            if (E <= 64) return go(topk_grad_kernel<4, V, 16>, 16);
+            if (E <= 128) return go(topk_grad_kernel<8, V, 16>, 16);
+            return go(topk_grad_kernel<16, V, 16>, 16);
+        }
+        if (E <= 128) return go(topk_grad_kernel<4, V, 32>, 32);
+        if (E <= 256) return go(topk_grad_kernel<8, V, 32>, 32);
+        if (E <= 512) return go(topk_grad_kernel<16, V, 32>, 32);
+        return go(topk_grad_kernel<32, V, 32>, 32);
+    };
+    if (E % 4 == 0 && access_bytes({logits, d_logits}, {}) == 16) return by_shape(std::true_type());
+    return by_shape(std::false_type());
 }
 
 }  // namespace moe

@@ -285,6 +285,28 @@ def test_topk_grad(ops, N, E, k, norm):
 
 
 @pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("N,E,k", [(77, 65, 12), (13, 200, 16), (40, 250, 17), (5003, 33, 3), (6001, 64, 8), (4999, 96, 8),
+                                   (5001, 203, 7), (9999, 256, 1)])
+def test_topk_grad_tokens_of_a_warp(ops, N, E, k, norm):
+    """Several tokens a warp, some without anything to choose from."""
+    l = 3 * torch.randn((N, E), generator=gen(N), device="cuda")
+    l[::5] = -torch.inf
+    l[1::7, : E // 2] = -torch.inf
+    idx = torch.stack([torch.randperm(E, generator=gen(s), device="cuda")[:k] for s in range(8)]).int()
+    idx = idx[torch.arange(N, device="cuda") % 8].contiguous()
+    idx[2::3, 0] = -1
+    ws = ops.new_sort_workspace(1, 1, 1)
+    d_w = torch.randn((N, k), generator=gen(E), device="cuda")
+    got = ops.moe_topk_grad(l, idx, d_w, norm, ws)
+    lost = (l.gather(1, idx.clamp(min=0).long()).masked_fill(idx < 0, -torch.inf) == -torch.inf).all(1)
+    none = lost if norm else (l == -torch.inf).all(1)
+    assert torch.all(got[none] == 0)
+    ref, tol = topk_grad_reference(l[~none], idx[~none], d_w[~none], norm)
+    close(got[~none], ref, tol)
+    assert ops.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("norm", [False, True])
 def test_topk_grad_masked_and_extreme_logits(ops, norm):
     l = torch.randn((6, 40), generator=gen(1), device="cuda")
     l[0, 5:] = -torch.inf                      # experts masked out

@@ -165,13 +165,22 @@ struct W4Args {
     int n_rows, pass_rows;  // rows of an expert taken at a time
     int stage_rows;         // rows that shared memory holds
     int slots;              // of a warp's ring: 2 to 4 pairs of records
-    int wk;                 // warps that share a tile's chunks; the CTA's other warps take the next tiles
+    int wk, wk_log2;        // warps that share a tile's chunks; the CTA's other warps take the next tiles
+    int copy_log2, turn_log2;  // threads that share a row: as it is copied, as it is turned
+    uint64_t ntiles_inv, pass_inv, grid_inv;  // for div_by
     int nt_max;             // column tiles of 8 that pass_rows rows fill
     int bufs;               // buffers for the sums
     void *y;
     int64_t y_stride;
     unsigned *status;
 };
+
+// n / d by the inverse M = ceil(2^64 / d) (0 for d = 1): M d - 2^64 < d, so n M / 2^64 lies less than
+// n / 2^64 <= 1 / d above n / d for n, d < 2^32, and rounds down to the same.
+inline uint64_t inverse(uint32_t d) { return d == 1 ? 0 : ~(uint64_t)0 / d + 1; }
+__device__ __forceinline__ unsigned div_by(unsigned n, uint64_t inv) {
+    return inv != 0 ? (unsigned)__umul64hi(n, inv) : n;
+}
 
 __device__ __forceinline__ float exp2_int(int e) {  // 2^e, e in [-149, 127]
     return __uint_as_float(e >= -126 ? (uint32_t)(e + 127) << 23 : 1u << (e + 149));
@@ -191,78 +200,90 @@ __device__ __forceinline__ void copy_rows(const W4Args &a, int j0, int rows, cha
     const int eb = a.dtype == MOE_DTYPE_F32 ? 4 : 2, nt = blockDim.x;
     const int64_t stride = a.x_stride * eb;
     const char *x = static_cast<const char *>(a.x) + j0 * stride;
-    const int n16 = a.nchunk * W4_CHUNK * eb / 16, kb = a.K * eb;  // 16-byte pieces of a row, bytes of its values
+    const int end = a.nchunk * W4_CHUNK * eb, kb = a.K * eb;  // bytes of a row, and of its values
     const bool wide = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)stride) % 16 == 0;
-    for (int j = 0; j < rows; ++j, x += stride, xs += row_bytes)
-        for (int at = threadIdx.x * 16; at < n16 * 16; at += nt * 16) {
+    const int tpr = 1 << a.copy_log2, jstep = nt >> a.copy_log2;
+    for (int j = threadIdx.x >> a.copy_log2; j < rows; j += jstep) {
+        const char *src = x + j * stride;
+        char *dst = xs + j * row_bytes;
+        for (int at = (threadIdx.x & (tpr - 1)) * 16; at < end; at += tpr * 16) {
             if (at >= kb) {
-                *reinterpret_cast<uint4 *>(xs + at) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(dst + at) = make_uint4(0, 0, 0, 0);
             } else if (wide) {
-                cp_async16(smem32(xs + at), x + at);
+                cp_async16(smem32(dst + at), src + at);
             } else {
 #pragma unroll 1
                 for (int q = 0; q < 16; q += eb)
                     if (eb == 4)
-                        *reinterpret_cast<uint32_t *>(xs + at + q) = *reinterpret_cast<const uint32_t *>(x + at + q);
+                        *reinterpret_cast<uint32_t *>(dst + at + q) = *reinterpret_cast<const uint32_t *>(src + at + q);
                     else
-                        *reinterpret_cast<uint16_t *>(xs + at + q) = *reinterpret_cast<const uint16_t *>(x + at + q);
+                        *reinterpret_cast<uint16_t *>(dst + at + q) = *reinterpret_cast<const uint16_t *>(src + at + q);
             }
         }
+    }
 }
 
 template <typename T>  // float or bf16 (fp16 rows stay as they are)
 __device__ __forceinline__ void turn_rows(const W4Args &a, int rows, char *xs, int row_bytes, float *back, unsigned *top) {
     constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1, V = 16 / sizeof(T);
-    const int n8 = a.nchunk * (W4_CHUNK / 8), n = rows * n8, nt = blockDim.x;
+    const int n8 = a.nchunk * (W4_CHUNK / 8), nt = blockDim.x;
+    const int tpr = 1 << a.turn_log2, jstep = nt >> a.turn_log2, r0 = threadIdx.x >> a.turn_log2, i0 = threadIdx.x & (tpr - 1);
     for (int j = threadIdx.x; j < rows; j += nt) top[j] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += nt) {  // the largest finite magnitude of each row, as bits
-        const int j = i / n8;
-        const T *src = reinterpret_cast<const T *>(xs + j * row_bytes) + (i - j * n8) * 8;
+    for (int j = r0; j < rows; j += jstep) {  // the largest magnitude of each row, as bits
         unsigned m = 0;
+        for (int i = i0; i < n8; i += tpr) {
+            const char *src = xs + j * row_bytes + i * 8 * sizeof(T);
+            if constexpr (PARTS == 1) {
+                const uint4 p = *reinterpret_cast<const uint4 *>(src);
+                const unsigned mask = 0x7fff7fffu;
+                const unsigned q = __vmaxu2(__vmaxu2(p.x & mask, p.y & mask), __vmaxu2(p.z & mask, p.w & mask));
+                m = max(m, max(q << 16, q & 0xffff0000u));
+            } else {
 #pragma unroll
-        for (int h = 0; h < 8; h += V) {
-            Pack<T, V> p;
-            p.load(src + h);
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const unsigned b = __float_as_uint(p.get(q)) & 0x7fffffffu;
-                m = max(m, b < 0x7f800000u ? b : 0u);
+                for (int h = 0; h < 8; h += V) {
+                    const uint4 p = *reinterpret_cast<const uint4 *>(src + h * 4);
+                    m = max(m, max(max(p.x & 0x7fffffffu, p.y & 0x7fffffffu), max(p.z & 0x7fffffffu, p.w & 0x7fffffffu)));
+                }
             }
         }
-        if (m) atomicMax(&top[j], m);
+        if (tpr >= 32) m = __reduce_max_sync(0xffffffffu, m);  // the warp is in one row: one atomic instead of 32
+        if (m && (tpr < 32 || (threadIdx.x & 31) == 0)) atomicMax(&top[j], m);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += nt) {
-        const int j = i / n8;
-        char *at = xs + j * row_bytes + (i - j * n8) * 8 * sizeof(T);
-        // 2^-ex times the row lies below 2^15; ex >= -126 keeps that factor a normal number
-        const int ex = top[j] ? max((int)(top[j] >> 23) - 127 - 14, -126) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        float v[8];
+    for (int j = r0; j < rows; j += jstep) {
+        for (int i = i0; i < n8; i += tpr) {
+            char *at = xs + j * row_bytes + i * 8 * sizeof(T);
+            // 2^-ex times the row lies below 2^15; ex >= -126 keeps that factor a normal number.  With an infinity or
+            // NaN in it no sum of the row is finite, whatever becomes of the others.
+            const unsigned m = min(top[j], 0x7f7fffffu);
+            const int ex = m ? max((int)(m >> 23) - 127 - 14, -126) : 0;
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            float v[8];
 #pragma unroll
-        for (int h = 0; h < 8; h += V) {
-            Pack<T, V> p;
-            p.load(reinterpret_cast<const T *>(at) + h);
+            for (int h = 0; h < 8; h += V) {
+                Pack<T, V> p;
+                p.load(reinterpret_cast<const T *>(at) + h);
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[h + q] = __fmul_rn(p.get(q), down);
-        }
+                for (int q = 0; q < V; ++q) v[h + q] = __fmul_rn(p.get(q), down);
+            }
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
-            uint32_t u[4];
+            for (int part = 0; part < PARTS; ++part) {
+                uint32_t u[4];
 #pragma unroll
-            for (int q = 0; q < 8; q += 2) u[q >> 1] = half_pair(v[q], v[q + 1]);
-            *reinterpret_cast<uint4 *>(at + part * 16) = make_uint4(u[0], u[1], u[2], u[3]);
-            if (part + 1 < PARTS)
+                for (int q = 0; q < 8; q += 2) u[q >> 1] = half_pair(v[q], v[q + 1]);
+                *reinterpret_cast<uint4 *>(at + part * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                if (part + 1 < PARTS)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {  // what is left, 2^11 times; an infinity or NaN stays in the first
-                    const float hi = __half2float(__ushort_as_half((unsigned short)(u[q >> 1] >> (16 * (q & 1)))));
-                    v[q] = fabsf(v[q]) < INFINITY ? (v[q] - hi) * 2048.0f : 0.0f;
-                }
-        }
-        if (i - j * n8 == 0) {
-            back[PARTS * j] = exp2_int(ex);
-            if (PARTS == 2) back[PARTS * j + 1] = exp2_int(ex - 11);
+                    for (int q = 0; q < 8; ++q) {  // what is left, 2^11 times; an infinity or NaN stays in the first
+                        const float hi = __half2float(__ushort_as_half((unsigned short)(u[q >> 1] >> (16 * (q & 1)))));
+                        v[q] = fabsf(v[q]) < INFINITY ? (v[q] - hi) * 2048.0f : 0.0f;
+                    }
+            }
+            if (i == 0) {
+                back[PARTS * j] = exp2_int(ex);
+                if (PARTS == 2) back[PARTS * j + 1] = exp2_int(ex - 11);
+            }
         }
     }
 }
@@ -380,7 +401,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
     const int warps = blockDim.x >> 5;
     const int row_bytes = a.nchunk * W4_CHUNK * 2 * cpr + W4_XPAD;  // of a staged row
     const int S = a.slots;
-    const int wt = warp / a.wk, wk = warp - wt * a.wk, per = warps / a.wk;
+    const int wt = warp >> a.wk_log2, wk = warp & (a.wk - 1), per = warps >> a.wk_log2;
     const uint32_t ring = warp * S * SLOT;  // offsets into smem, as below
     float4 *red = reinterpret_cast<float4 *>(smem + warps * S * SLOT);  // the sums: [bufs][warps][nt_max][lanes]
     char *xs = reinterpret_cast<char *>(red + a.bufs * warps * a.nt_max * 32);
@@ -388,10 +409,10 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
     float *back = reinterpret_cast<float *>(first + a.E + 1);             // [stage_rows][cpr]
     unsigned *top = reinterpret_cast<unsigned *>(back + a.stage_rows * cpr);  // [stage_rows]
 
-    int units = (a.n_rows + a.pass_rows - 1) / a.pass_rows;
+    int units = (int)div_by((unsigned)(a.n_rows + a.pass_rows - 1), a.pass_inv);
     if (a.expStart != nullptr) {
         // passes of each expert, exclusive scan; every offset is checked
-        const int each = (a.E + blockDim.x - 1) / blockDim.x, e0 = tid * each;  // a thread's experts
+        const int each = (int)((a.E + blockDim.x - 1) >> (31 - __clz(blockDim.x))), e0 = tid * each;  // a thread's experts
         bool bad = false;
         auto passes = [&](int e) {
             if (e >= a.E) return 0;
@@ -400,7 +421,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 bad = true;
                 return 0;
             }
-            return (int)((unsigned)(q - p + a.pass_rows - 1) / (unsigned)a.pass_rows);
+            return (int)div_by((unsigned)(q - p + a.pass_rows - 1), a.pass_inv);
         };
         int mine = 0;
 #pragma unroll 1
@@ -444,19 +465,19 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
         return lo;
     };
     // tiles of this CTA (the host keeps their number below 2^31), and its first
-    const unsigned items = (unsigned)units * (unsigned)a.ntiles, share = items / gridDim.x, more = items % gridDim.x;
+    const unsigned items = (unsigned)units * (unsigned)a.ntiles, share = div_by(items, a.grid_inv), more = items - share * gridDim.x;
     const unsigned i0 = blockIdx.x * share + min(blockIdx.x, more);
     int todo = (int)(share + (blockIdx.x < more));
     if (todo == 0) return;
-    const int u0 = (int)(i0 / (unsigned)a.ntiles), t0 = (int)(i0 - (unsigned)u0 * a.ntiles);
-    const int last_unit = (int)((i0 + todo - 1) / (unsigned)a.ntiles);
+    const int u0 = (int)div_by(i0, a.ntiles_inv), t0 = (int)(i0 - (unsigned)u0 * a.ntiles);
+    const int last_unit = (int)div_by(i0 + todo - 1, a.ntiles_inv);
 
     // The CTA takes `per` tiles of a unit at a time.  The fetching position runs ahead of the computing one:
     // ftile of unit fu (fleft tiles to come), the pair at fsrc, fnum more of this warp's tile, the last of them
     // a single record where `odd`.
     const int pairs = (a.nchunk + 1) / 2;
-    const int per_tile = wk < pairs ? (pairs - wk + a.wk - 1) / a.wk : 0;  // this warp's pairs of a tile
-    const bool odd = (a.nchunk & 1) && (pairs - 1) % a.wk == wk;
+    const int per_tile = wk < pairs ? (pairs - wk + a.wk - 1) >> a.wk_log2 : 0;  // this warp's pairs of a tile
+    const bool odd = (a.nchunk & 1) && ((pairs - 1) & (a.wk - 1)) == wk;
     int fu = u0, ftile = t0, fleft = per_tile > 0 ? todo : 0, fnum = 0, fe = expert_of(u0);
     const char *fsrc = a.records;
     const int64_t fstep = (int64_t)a.wk * SLOT;
@@ -670,6 +691,12 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
     cp_async_wait<0>();
 }
 
+int log2_of(int n) {  // rounded up
+    int l = 0;
+    while (1 << l < n) ++l;
+    return l;
+}
+
 }  // namespace
 
 int w4_repack(moe_w4_weights_s *w, const uint8_t *q, const void *scales, const uint8_t *zeros, const uint8_t *up_q,
@@ -726,6 +753,8 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     int wk = 1;
     while (wk < 8 && wk < pairs && tiles * wk < (int64_t)sms * 16 * W4_TURNS) wk *= 2;
     a.wk = wk;
+    a.wk_log2 = log2_of(wk);
+    a.ntiles_inv = inverse(a.ntiles);
     struct Shape {
         int warps, ctas, slots, bufs;  // CTAs an SM
     };
@@ -773,6 +802,12 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     const int64_t units = w->E == 1 ? (n_rows + rows - 1) / rows : n_rows;
     a.stage_rows = (int)std::min<int64_t>({(int64_t)n_rows, units * rows, rows + (int64_t)((room - used) / per_row)});
     a.slots = shape.slots;
+    a.pass_inv = inverse(rows);
+    a.grid_inv = inverse(grid);
+    // a power of two of threads a row, so many that each has a piece of it where the CTA has as many
+    const int nt = shape.warps * 32;
+    a.turn_log2 = log2_of(std::min(nt, a.nchunk * (W4_CHUNK / 8)));
+    a.copy_log2 = log2_of(std::min(nt, a.nchunk * (W4_CHUNK / 8) * cpr));
     const size_t smem = used + per_row * (a.stage_rows - rows);
     auto go = [&](auto kernel, SmemOptIn *done) {
         // one limit for every call, so that calls at once from two threads set the same

@@ -384,12 +384,13 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
 // its chunks; their sums meet in shared memory in warp order (wk == 1: the lanes hold whole sums).  Every warp
 // streams its pairs of records through a ring of S slots of its own, filled by cp.async ahead of the tiles: the
 // stream does not stop at the end of a tile or a unit.  NTM: column tiles of 8 that the accumulators hold.
-// Measured: 131072 x 4096 fp16, groups of 128, for eight rows 52 us (279 MB, 5.3 TB/s: 79% of the copy rate; 277 MB
+// Measured: 131072 x 4096 fp16, groups of 128, for eight rows 53.1 us (279 MB, 5.3 TB/s: 78% of the copy rate; 277 MB
 // more take 40 us more, the copy rate; 3 us pass before the weights flow); gate and up of 64 experts (1024 x 2048,
-// groups of 32) for 64 rows of eight tokens 25.7 us (57%); 128 experts of 2048 x 768 with zero points for 256 fp32
-// rows 30.7 us (47%); one token through 2048 x 2048 4.0 us.  Without the products the same streams take 46.5, 20.4
+// groups of 32) for 64 rows of eight tokens 24.8 us (59%); 128 experts of 2048 x 768 with zero points for 256 fp32
+// rows 30.0 us (49%); one token through 2048 x 2048 3.7 us.  Without the products the same streams take 46.5, 20.4
 // and 21.4 us: 137 (with zero points 165) instructions a record and their dependences, on 16 warps an SM at 60% of
-// the issue slots, are what is left to hide.  24 warps of 80 registers measured the same.
+// the issue slots, are what is left to hide.  24 warps of 70 - 80 registers: 76.7, 28.2 and 31.1 us.  A bulk copy a
+// pair, counted on a barrier of its slot, in the place of the cp.async: 56.0, 25.6 and 30.9 us.
 template <int G, bool ZP, bool F32, int NTM>
 __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
     constexpr int NB = W4_CHUNK / G, REC = w4_record(G, ZP), MORE = (REC - 1024) / 16, SLOT = 2 * REC;
@@ -439,10 +440,11 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
         }
         int run = inc - mine;
         units = 0;
-#pragma unroll 1
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) run += wsum[w];
-            units += wsum[w];
+#pragma unroll
+        for (int w = 0; w < W4_WARPS; ++w) {
+            const int n = w < warps ? wsum[w] : 0;
+            run += w < warp ? n : 0;
+            units += n;
         }
 #pragma unroll 1
         for (int i = 0; i < each && e0 + i < a.E; ++i) {
@@ -517,15 +519,14 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
         cp_async_commit();
     };
     // rows of a unit: the first, and how many
-    auto unit_rows = [&](int v, int *begin) {
-        const int e = expert_of(v);
+    auto unit_rows = [&](int v, int e, int *begin) {
         const int lo = a.expStart ? a.expStart[e] : 0, hi = a.expStart ? a.expStart[e + 1] : a.n_rows;
         *begin = lo + (v - (a.expStart ? first[e] : 0)) * a.pass_rows;
         return min(hi - *begin, a.pass_rows);
     };
     // The rows of the first unit are asked for before any weights; those of each next one while a unit is at
     // work, into the part of the staging room that it leaves, so that the warps need not stop for them.
-    int j0, rows = unit_rows(u0, &j0), x_at = 0;
+    int j0, rows = unit_rows(u0, fe, &j0), x_at = 0;
     int next_rows = 0, next_j0 = 0, next_at = -1;  // the next unit's (next_at < 0: not asked for)
     int since = 0;                                 // groups of copies begun after its rows'
     copy_rows(a, j0, rows, xs, row_bytes);
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 __syncthreads();
                 j0 = next_j0, rows = next_rows, x_at = next_at;
             } else {
-                rows = unit_rows(u, &j0), x_at = 0;
+                rows = unit_rows(u, expert_of(u), &j0), x_at = 0;
                 __syncthreads();
                 copy_rows(a, j0, rows, xs, row_bytes);
                 cp_async_commit();
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
             }
             next_at = -1;
             if (u < last_unit) {
-                next_rows = unit_rows(u + 1, &next_j0);
+                next_rows = unit_rows(u + 1, expert_of(u + 1), &next_j0);
                 if (x_at + rows + next_rows <= a.stage_rows)
                     next_at = x_at + rows;
                 else if (next_rows <= x_at)
@@ -746,7 +747,7 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     const size_t record = w4_record(w->group, w->zeros);
     // Warps a tile: the fewest that leave the GPU's 16 warps an SM six tiles each in turn (a tile that is shared
     // costs a barrier and a reduction, long turns a longer tail: 131072 x 4096 fp16 52.6 / 52.2 / 57.9 us with
-    // 3 / 6 / 12 turns, 128 experts of 2048 x 768 30.8 / 30.7 / 36.4), but no more than have a pair of chunks each.
+    // 3 / 6 / 12 turns, 128 experts of 2048 x 768 30.8 / 30.7 / 36.4, when this was chosen), but no more than have a pair of chunks each.
     // The weights' shape alone decides, so that a row's sums do not depend on the rows beside it.
     const int64_t tiles = (int64_t)a.ntiles * a.E;
     const int pairs = (a.nchunk + 1) / 2;

@@ -187,6 +187,20 @@ def test_rows_of_many_magnitudes(ops, dtype):
     close(y, ref, err + HALF[dtype] * (ref.abs() + err) * 1.001 + TINY[dtype])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("K,rows", [(32, 1), (32, 37), (96, 7), (160, 33), (384, 20), (1024, 5), (4128, 3), (16416, 2)])
+def test_powers_of_two_pass_through(ops, K, rows, dtype):
+    """A row times a power of two gives its products times that power, bit for bit, whatever the rows beside it."""
+    w = ops.MoeW4Weights(*matrix(1, 40, K, 32, F16, True, K))
+    ws = ops.new_sort_workspace(1, 1, 1)
+    x = torch.randn((rows, K), generator=gen(rows), device="cuda").to(dtype)
+    power = torch.exp2(((torch.arange(rows, device="cuda") * 29) % 81 - 40).float()).unsqueeze(1)
+    y = ops.moe_w4_matvec(w, x, None, ws)
+    assert torch.equal(ops.moe_w4_matvec(w, (x * power).to(dtype), None, ws), (y * power).to(dtype))
+    for j in range(rows):
+        assert torch.equal(ops.moe_w4_matvec(w, x[j:j + 1], None, ws), y[j:j + 1])
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
 @pytest.mark.parametrize("G", [32, 64, 128])
 def test_small_integers_are_exact(ops, G, dtype):

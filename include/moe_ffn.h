@@ -516,7 +516,8 @@ size_t moe_sort_workspace_size(int N, int top_k, int E);
  *   rows     [N*top_k][D] out: rows[r] = x[expTokI[r]], bit for bit; rows from
  *            expStart[E] on are left as they were
  * Any other negative index, or one of E and above, sets MOE_DEV_BAD_ROUTING
- * and counts as dropped. */
+ * and counts as dropped.  A copy inside the kernel that takes more than two
+ * seconds sets MOE_DEV_TIMEOUT: rows are then incomplete. */
 int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N,
                     int top_k, int E, int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK,
                     int32_t *tokRow, void *rows, void *ws, size_t ws_bytes, cudaStream_t stream);
@@ -561,7 +562,8 @@ int moe_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const void *
  *       alone, and d_logits 0 at the others.
  * logits, d_logits [N][E] fp32, topk_idx [N][top_k] int32, d_topk_w [N][top_k] fp32.
  * A slot of -1 counts as not selected; any other index outside [0, E) does too and
- * sets MOE_DEV_BAD_ROUTING.  A token whose softmax has no logit above -inf gets zeros. */
+ * sets MOE_DEV_BAD_ROUTING.  A token whose softmax has no logit above -inf gets zeros.
+ * The sums' order is fixed for given N, E, top_k and alignment. */
 int moe_topk_grad(const float *logits, const int32_t *topk_idx, const float *d_topk_w, int N, int E,
                   int top_k, int norm_topk_prob, float *d_logits, void *ws, size_t ws_bytes,
                   cudaStream_t stream);
@@ -597,7 +599,7 @@ int moe_w4_weights_shape(moe_w4_weights_t w, int *E, int *R, int *K, int *group,
 size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
 
 /* y[j] = the handle's product of row x[j], for rows in CSR order (moe_sort_tokens).
- *   x [n_rows][K], y [n_rows][R] of `dtype`; strides as for moe_sort_tokens
+ *   x [n_rows][K], y [n_rows][R] of `dtype`, n_rows >= 1; strides as for moe_sort_tokens
  *   expStart [E+1] int32 device: rows expStart[e]..expStart[e+1]-1 are expert e's;
  *            rows from expStart[E] on are left as they were.  NULL (E == 1 only):
  *            every row is expert 0's.  Offsets that do not start at 0, decrease or

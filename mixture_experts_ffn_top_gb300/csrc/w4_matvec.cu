@@ -32,7 +32,7 @@ namespace moe {
 namespace {
 
 constexpr int W4_WARPS = 16;                   // at most; a CTA has 8 or 16
-constexpr int W4_TURNS = 6;                    // tiles that each warp should take in turn (see launch_w4_matvec)
+constexpr int W4_TURNS = 6;                    // tiles of all experts for each warp (see launch_w4_matvec)
 constexpr int W4_CHUNK = 128;                  // columns of a chunk
 constexpr int W4_XPAD = 64;                    // bytes past a multiple of 128 that staged rows lie apart: no bank conflicts
 constexpr size_t W4_SMEM_SM = 227 * 1024;      // shared memory of an SM's CTAs, less 1 KB each
@@ -745,14 +745,16 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     const int cpr = dtype == MOE_DTYPE_F32 ? 2 : 1;
     const size_t row_bytes = (size_t)a.nchunk * W4_CHUNK * 2 * cpr + W4_XPAD;
     const size_t record = w4_record(w->group, w->zeros);
-    // Warps a tile: the fewest that leave the GPU's 16 warps an SM six tiles each in turn (a tile that is shared
-    // costs a barrier and a reduction, long turns a longer tail: 131072 x 4096 fp16 52.6 / 52.2 / 57.9 us with
-    // 3 / 6 / 12 turns, 128 experts of 2048 x 768 30.8 / 30.7 / 36.4, when this was chosen), but no more than have a pair of chunks each.
+    // Warps a tile: the fewest that leave each of the GPU's 16 warps an SM a tile of a single matrix (28672 x 4096 17.0
+    // us with four, 19.4 with eight; a shared tile costs a barrier and a reduction), and of many experts six, as few of
+    // them may have rows (128 gates and ups of 768 x 2048, eight rows: 8.3 us with two, 10.3 with one; for the 64 rows
+    // of 64 experts 24.8 with two, 28 with four) -- but no more than have two pairs of chunks each unless warps would
+    // have no tile at all (35 experts of 5592 x 768 15.3 us with one, 17.4 with two).
     // The weights' shape alone decides, so that a row's sums do not depend on the rows beside it.
     const int64_t tiles = (int64_t)a.ntiles * a.E;
     const int pairs = (a.nchunk + 1) / 2;
     int wk = 1;
-    while (wk < 8 && wk < pairs && tiles * wk < (int64_t)sms * 16 * W4_TURNS) wk *= 2;
+    while (wk < 8 && wk < pairs && tiles * wk < (int64_t)sms * 16 * (a.E == 1 || pairs < 4 * wk ? 1 : W4_TURNS)) wk *= 2;
     a.wk = wk;
     a.wk_log2 = log2_of(wk);
     a.ntiles_inv = inverse(a.ntiles);

@@ -604,8 +604,8 @@ size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
  *            rows from expStart[E] on are left as they were.  NULL (E == 1 only):
  *            every row is expert 0's.  Offsets that do not start at 0, decrease or
  *            pass n_rows set MOE_DEV_BAD_CSR and every row is left.
- * Codes less zero points are exact, and so are fp16 rows; bf16 rows are exact down to 2^-29 of their
- * largest magnitude (smaller values lose at most 2^-40 of it); of fp32 rows at most 2^-22 of each value, or
+ * Codes less zero points are exact, and so are fp16 rows; bf16 rows are exact down to 2^-31 of their
+ * largest magnitude (smaller values lose at most 2^-39 of it); of fp32 rows at most 2^-22 of each value, or
  * 2^-50 of the row's largest, is lost.  Products are summed in fp32 per group and the groups' sums, times
  * their scales, in fp32, in an order that the weights' shape and the type fix: a row's result does not
  * depend on the rows beside it.  An infinity or NaN stays in its row.  Made for few rows an expert

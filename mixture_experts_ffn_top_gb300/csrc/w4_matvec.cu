@@ -12,10 +12,12 @@
 // times the packed stream's traffic, for columns that are not there.)
 //
 // The activations enter as fp16.  fp16 rows as they are; bf16 and fp32 rows times a power of two that brings
-// the row's largest magnitude to 2^14 .. 2^15, taken back out of the sums: a bf16 value keeps all its bits
-// down to 2^-29 of the row's largest (below that an error of 2^-40 of it), an fp32 value is the sum of two
-// columns, its upper 11 bits and 2^11 times the rest, which loses at most 2^-22 of itself (or 2^-50 of the
-// row's largest): of the order of the sums' own fp32 roundings, with two columns where an exact split takes three.
+// the row's largest magnitude to 2^14 .. 2^15, taken back out of the sums.  fp16's values end in multiples of
+// 2^-24: the 8 bits of a bf16 value from 2^-17 on are kept, so all down to 2^-31 of the row's largest, and a
+// smaller value moves by half a multiple at most, 2^-25, which is 2^-39 of a largest of 2^14.  An fp32 value is
+// the sum of two columns, its upper 11 bits and 2^11 times the rest, which loses at most 2^-22 of itself (or
+// 2^-25 / 2^11, 2^-50 of the row's largest): of the order of the sums' own fp32 roundings, with two columns
+// where an exact split takes three.
 //
 // Layout (w4_repack_kernel, once per weights): tiles of 16 rows (gate/up: 8 gate, then the same 8 up) by
 // chunks of 128 columns, a record each: 1 KB of codes in the order the lanes hold them -- lane (g, t) =

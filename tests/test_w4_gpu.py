@@ -359,3 +359,31 @@ def test_refused_tensors(ops):
     w.close()
     with pytest.raises(ValueError):
         ops.moe_w4_matvec(w, x, es, ws)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("largest", [1.0, 1.9921875, -1.5 * 2.0 ** -60, 2.0 ** 90])
+def test_small_values_beside_a_large_one(ops, dtype, largest):
+    """A value alone in the sum (weight 1), its row's largest at a weight of 0, over 60 binades: a bf16 value down to
+    2^-31 of the largest is exact and a smaller one loses at most 2^-39 of it; an fp32 value at most 2^-22 of itself or
+    2^-50 of the largest, and the last sum's rounding u.  (The bf16 results need no rounding: what is left of a value
+    below 2^-31 of the largest are multiples of a step that is 2^-39 of it or more, at most 2^8 of them.)"""
+    K = 64
+    codes = torch.full((3, K), 8, dtype=torch.uint8, device="cuda")
+    codes[0, 40] = codes[1, 5] = codes[2, 63] = 9
+    w = ops.MoeW4Weights(codes[:, 0::2] | codes[:, 1::2] << 4, torch.ones((3, 2), device="cuda").half())
+    e = torch.arange(-60, 1, device="cuda").float().repeat(40)
+    m = 1 + torch.rand(e.shape, generator=gen(1), device="cuda")
+    m[: 3 * 61] = torch.tensor([1.0, 1.5, 1.9921875], device="cuda").repeat_interleave(61)  # ties of the last steps
+    v = (abs(largest) / 2 * m * torch.exp2(e)).to(dtype)  # below the largest
+    v[::2] *= -1
+    x = torch.zeros((v.numel(), K), dtype=dtype, device="cuda")
+    x[:, 0] = largest
+    x[:, 40], x[:, 5], x[:, 63] = v, v, v
+    y = ops.moe_w4_matvec(w, x, None, ops.new_sort_workspace(1, 1, 1)).double()
+    v, top = v.double().unsqueeze(1), abs(largest)
+    if dtype is BF16:
+        tol = torch.where(v.abs() >= top * 2.0 ** -31, 0.0, top * 2.0 ** -39)
+    else:
+        tol = torch.maximum(v.abs() * 2.0 ** -22, torch.full_like(v, top * 2.0 ** -50)) + U * 1.001 * v.abs()
+    assert torch.all((y - v).abs() <= tol)

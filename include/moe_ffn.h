@@ -608,7 +608,8 @@ size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
  * largest magnitude (smaller values lose at most 2^-39 of it); of fp32 rows at most 2^-22 of each value, or
  * 2^-50 of the row's largest, is lost.  Products are summed in fp32 per group and the groups' sums, times
  * their scales, in fp32, in an order that the weights' shape and the type fix: a row's result does not
- * depend on the rows beside it.  An infinity or NaN stays in its row.  Made for few rows an expert
+ * depend on the rows beside it.  Sums leave fp32's range only where the definition's own do, whatever the
+ * magnitudes of scales and rows.  An infinity or NaN stays in its row.  Made for few rows an expert
  * (decode): each 32 rows (fp32: 16) of an expert read its weights once more, and fewer where K is long.
  * MOE_ERR_UNSUPPORTED_SHAPE past 2^31 pairs of 16 weight rows and such a pass.
  *   ws: status word (256 bytes). */

@@ -70,6 +70,7 @@ struct moe_w4_weights_s {
     size_t bytes = 0;
     char *records = nullptr;    // the device allocation
     bool zeros = false;         // the records hold zero points
+    bool wide = false;          // bf16 scales beyond 2^-100 .. 2^90 among them
 };
 
 namespace moe {

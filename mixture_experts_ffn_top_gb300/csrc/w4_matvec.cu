@@ -19,6 +19,13 @@
 // 2^-25 / 2^11, 2^-50 of the row's largest): of the order of the sums' own fp32 roundings, with two columns
 // where an exact split takes three.
 //
+// A group's sum of such a row is a multiple of 2^-24 below 128 * 15 * 2^15 < 2^26, whatever the row's own
+// magnitude, and meets the scale as it is: sums over K <= 2^15 columns stay below 2^34 times the largest scale,
+// and no product rounds among fp32's smallest numbers by more than 2^-150.  So fp16 scales, and bf16 ones of
+// 2^-100 up to 2^90, leave nothing else to lose.  Weights with a bf16 scale beyond those (`wide`, found when they
+// are laid out) take the power of two out of each group's sum before its scale, one multiplication more: the sums
+// have the magnitude of the definition's and leave fp32's range only where those do.
+//
 // Layout (w4_repack_kernel, once per weights): tiles of 16 rows (gate/up: 8 gate, then the same 8 up) by
 // chunks of 128 columns, a record each: 1 KB of codes in the order the lanes hold them -- lane (g, t) =
 // (lane / 4, lane % 4) has row g's 16 bytes at 16 * lane and row g + 8's at 512 + 16 * lane, word b of them
@@ -41,11 +48,13 @@ constexpr size_t W4_SMEM_SM = 227 * 1024;      // shared memory of an SM's CTAs,
 
 __host__ __device__ constexpr int w4_record(int group, bool zeros) { return 1024 + (zeros ? 48 : 32) * (W4_CHUNK / group); }
 
-// One thread per 32-bit word of codes and one per scale.
+// One thread per 32-bit word of codes and one per scale.  wide (bf16 scales): set where a finite one is not 0 and
+// lies outside 2^-100 .. 2^90.
 __global__ void w4_repack_kernel(const uint8_t *__restrict__ q, const uint16_t *__restrict__ sc,
                                  const uint8_t *__restrict__ zp, const uint8_t *__restrict__ uq,
                                  const uint16_t *__restrict__ usc, const uint8_t *__restrict__ uzp, int E, int R,
-                                 int K, int group, int ntiles, int nchunk, char *__restrict__ out) {
+                                 int K, int group, int ntiles, int nchunk, char *__restrict__ out,
+                                 unsigned *__restrict__ wide) {
     const bool pair = uq != nullptr;
     const int nb = W4_CHUNK / group, ng = K / group, record = w4_record(group, zp != nullptr);
     const int64_t chunks = (int64_t)E * ntiles * nchunk;
@@ -86,7 +95,10 @@ __global__ void w4_repack_kernel(const uint8_t *__restrict__ q, const uint16_t *
             reinterpret_cast<uint32_t *>(dst)[in] = w;
         } else {
             const int64_t at = (e * R + row) * (int64_t)ng + k0 / group;
-            reinterpret_cast<uint16_t *>(dst + 1024)[in] = there ? (up ? usc : sc)[at] : (uint16_t)0;
+            const uint16_t v = there ? (up ? usc : sc)[at] : (uint16_t)0;
+            const int ex = (v >> 7) & 255;  // of a bf16 scale
+            if (wide != nullptr && (v & 0x7fff) != 0 && ex != 255 && (ex < 127 - 100 || ex >= 127 + 90)) *wide = 1;
+            reinterpret_cast<uint16_t *>(dst + 1024)[in] = v;
             if (zp) reinterpret_cast<uint8_t *>(dst + 1024 + 32 * nb)[in] = there ? (uint8_t)(((up ? uzp : zp)[at] & 15) * 17) : (uint8_t)0;
         }
     }
@@ -302,13 +314,14 @@ __device__ __forceinline__ void store_y(const W4Args &a, int64_t at, float v) {
 // One record (16 rows x 128 columns of weights) against NT tiles of 8 activation columns.  Offsets into smem:
 // rec, the record plus 16 * lane; scp and zpp, the lane's scales and zero points; x[n] + k0, the lane's column of
 // tile n at the record's first column, kb bytes further for each 32 (columns past the last are copies of it: their
-// sums are not used).
+// sums are not used).  WIDE: f[n], what the sums of the lane's two columns of tile n are multiplied by.
 template <typename V>
 __device__ __forceinline__ V lds(const char *smem, uint32_t at) { return *reinterpret_cast<const V *>(smem + at); }
 
-template <int G, bool ZP, bool F32, int NT, int NTM>
+template <int G, bool ZP, bool F32, bool WIDE, int NT, int NTM>
 __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32_t scp, uint32_t zpp, bool sbf,
-                                          const uint32_t (&x)[NTM], uint32_t k0, float (&sum)[NTM][4]) {
+                                          const uint32_t (&x)[NTM], uint32_t k0, const float (&f)[WIDE ? NTM : 1][2],
+                                          float (&sum)[NTM][4]) {
     constexpr int NB = W4_CHUNK / G, KB = F32 ? 128 : 64;
     const uint4 wl = lds<uint4>(smem, rec), wh = lds<uint4>(smem, rec + 512);
     const uint32_t lo[4] = {wl.x, wl.y, wl.z, wl.w}, hi[4] = {wh.x, wh.y, wh.z, wh.w};
@@ -372,6 +385,9 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
             const float s0 = sc[gi], s1 = sc[NB + gi];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                if (WIDE)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = __fmul_rn(acc[n][i], f[WIDE ? n : 0][i & 1]);
                 sum[n][0] = __fmaf_rn(s0, acc[n][0], sum[n][0]);
                 sum[n][1] = __fmaf_rn(s0, acc[n][1], sum[n][1]);
                 sum[n][2] = __fmaf_rn(s1, acc[n][2], sum[n][2]);
@@ -393,7 +409,7 @@ __device__ __forceinline__ void chunk_mma(const char *smem, uint32_t rec, uint32
 // and 21.4 us: 137 (with zero points 165) instructions a record and their dependences, on 16 warps an SM at 60% of
 // the issue slots, are what is left to hide.  24 warps of 70 - 80 registers: 76.7, 28.2 and 31.1 us.  A bulk copy a
 // pair, counted on a barrier of its slot, in the place of the cp.async: 56.0, 25.6 and 30.9 us.
-template <int G, bool ZP, bool F32, int NTM>
+template <int G, bool ZP, bool F32, int NTM, bool WIDE>
 __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
     constexpr int NB = W4_CHUNK / G, REC = w4_record(G, ZP), MORE = (REC - 1024) / 16, SLOT = 2 * REC;
     constexpr int cpr = F32 ? 2 : 1;  // columns per row
@@ -540,6 +556,11 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
 
     int cur = -1, nt = 0, buf = 0;
     uint32_t slot = ring0, free_slot = ring1, at[NTM];  // the slot to read, and the one read before it
+    // WIDE: a column's power of two, as far as 2^100, goes into its groups' sums (below 2^26), the rest over it into
+    // the whole sums (rows with a value of 2^115 or more: their sums lie up to 2^13 below the definition's)
+    float f[WIDE ? NTM : 1][2];
+    auto inside = [&](int c) { return fminf(back[x_at * cpr + c], 0x1p100f); };
+    auto outside = [&](int c) { return WIDE ? __fdiv_rn(back[x_at * cpr + c], inside(c)) : back[x_at * cpr + c]; };
     // the lane's scales and zero points, from its 16 bytes of codes
     const int sc_off = 1024 + g * 4 * NB - lane * 16, zp_off = 1024 + 32 * NB + g * 2 * NB - lane * 16;
     const uint32_t x0 = (uint32_t)(xs - smem);
@@ -594,6 +615,9 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 const int c = min(n * 8 + g, cols - 1);
                 at[n] = x0 + (F32 ? (x_at + (c >> 1)) * row_bytes + (c & 1) * 16 : (x_at + c) * row_bytes) + t * 16 * cpr +
                         wk * 8 * KB;
+                if (WIDE)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) f[WIDE ? n : 0][h] = inside(min(n * 8 + 2 * t + h, cols - 1));
             }
         }
         const int now = min(per, min(a.ntiles - tile0, todo)), tile = tile0 + wt;
@@ -611,20 +635,20 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 ++since;
                 const bool both = !(odd && c == per_tile - 1);
                 if (NTM == 1 || nt == 1) {
-                    chunk_mma<G, ZP, F32, 1, NTM>(smem, slot, slot + sc_off, slot + zp_off, sbf, at, k0, sum);
+                    chunk_mma<G, ZP, F32, WIDE, 1, NTM>(smem, slot, slot + sc_off, slot + zp_off, sbf, at, k0, f, sum);
                     if (both)
-                        chunk_mma<G, ZP, F32, 1, NTM>(smem, slot + REC, slot + REC + sc_off, slot + REC + zp_off, sbf, at,
-                                                      k0 + 4 * KB, sum);
+                        chunk_mma<G, ZP, F32, WIDE, 1, NTM>(smem, slot + REC, slot + REC + sc_off, slot + REC + zp_off, sbf, at,
+                                                      k0 + 4 * KB, f, sum);
                 } else {
 #pragma unroll 1
                     for (int h = 0; h < 1 + both; ++h) {
                         const uint32_t rec = slot + h * REC, kh = k0 + h * 4 * KB;
                         if (NTM == 2 || nt == 2)
-                            chunk_mma<G, ZP, F32, NTM < 2 ? 1 : 2, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, sum);
+                            chunk_mma<G, ZP, F32, WIDE, NTM < 2 ? 1 : 2, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, f, sum);
                         else if (nt == 3)
-                            chunk_mma<G, ZP, F32, NTM < 3 ? 1 : 3, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, sum);
+                            chunk_mma<G, ZP, F32, WIDE, NTM < 3 ? 1 : 3, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, f, sum);
                         else
-                            chunk_mma<G, ZP, F32, NTM, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, sum);
+                            chunk_mma<G, ZP, F32, WIDE, NTM, NTM>(smem, rec, rec + sc_off, rec + zp_off, sbf, at, kh, f, sum);
                     }
                 }
                 k0 += a.wk * 8 * KB;
@@ -669,10 +693,10 @@ __global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_kernel(const W4Args a) {
                 for (int h = 0; h < 2; ++h) {
                     const int c = n * 8 + 2 * t + h, j = cpr == 2 ? c >> 1 : c;
                     if ((cpr == 2 && h) || j >= rows) continue;
-                    float v0 = __fmul_rn(sum[n][h], back[x_at * cpr + c]), v1 = __fmul_rn(sum[n][2 + h], back[x_at * cpr + c]);
+                    float v0 = __fmul_rn(sum[n][h], outside(c)), v1 = __fmul_rn(sum[n][2 + h], outside(c));
                     if (cpr == 2) {
-                        v0 = __fmaf_rn(sum[n][1], back[x_at * cpr + c + 1], v0);
-                        v1 = __fmaf_rn(sum[n][3], back[x_at * cpr + c + 1], v1);
+                        v0 = __fmaf_rn(sum[n][1], outside(c + 1), v0);
+                        v1 = __fmaf_rn(sum[n][3], outside(c + 1), v1);
                     }
                     const int64_t to = (int64_t)(j0 + j) * a.y_stride;
                     if (a.pair) {
@@ -707,7 +731,8 @@ int w4_repack(moe_w4_weights_s *w, const uint8_t *q, const void *scales, const u
     const int trows = w->pair ? 8 : 16;
     w->ntiles = (w->R + trows - 1) / trows;
     w->nchunk = (w->K + W4_CHUNK - 1) / W4_CHUNK;
-    const size_t bytes = (size_t)w->E * w->ntiles * w->nchunk * w4_record(w->group, zeros != nullptr);
+    const size_t records = (size_t)w->E * w->ntiles * w->nchunk * w4_record(w->group, zeros != nullptr);
+    const size_t bytes = records + 16;  // and the word that tells of far scales
     if (cudaMalloc(&w->records, bytes) != cudaSuccess) {
         (void)cudaGetLastError();
         w->records = nullptr;
@@ -715,12 +740,19 @@ int w4_repack(moe_w4_weights_s *w, const uint8_t *q, const void *scales, const u
     }
     w->bytes = bytes;
     w->zeros = zeros != nullptr;
+    unsigned *wide = reinterpret_cast<unsigned *>(w->records + records);
+    int rc = cuda_status(cudaMemsetAsync(wide, 0, sizeof(unsigned), s));
+    if (rc) return rc;
     const unsigned blocks = (unsigned)std::max(1, device_sm_count()) * 16;
     w4_repack_kernel<<<blocks, 256, 0, s>>>(q, static_cast<const uint16_t *>(scales), zeros, up_q,
                                             static_cast<const uint16_t *>(up_scales), up_zeros, w->E, w->R, w->K,
-                                            w->group, w->ntiles, w->nchunk, w->records);
-    int rc = launch_status();
+                                            w->group, w->ntiles, w->nchunk, w->records,
+                                            w->scale_dtype == MOE_DTYPE_BF16 ? wide : nullptr);
+    unsigned found = 0;
+    rc = launch_status();
+    if (!rc) rc = cuda_status(cudaMemcpyAsync(&found, wide, sizeof(found), cudaMemcpyDeviceToHost, s));
     if (!rc) rc = cuda_status(cudaStreamSynchronize(s));
+    w->wide = found != 0;
     return rc;
 }
 
@@ -824,9 +856,11 @@ int launch_w4_matvec(const moe_w4_weights_s *w, const void *x, int64_t x_stride,
     auto by_types = [&](auto gc, auto zc, auto fc) {
         constexpr int G = decltype(gc)::value;
         constexpr bool ZP = decltype(zc)::value, F32 = decltype(fc)::value;
-        static SmemOptIn d[3];
-        if (a.nt_max == 1) return go(w4_kernel<G, ZP, F32, 1>, &d[0]);
-        return a.nt_max == 2 ? go(w4_kernel<G, ZP, F32, 2>, &d[1]) : go(w4_kernel<G, ZP, F32, 4>, &d[2]);
+        static SmemOptIn d[4];
+        // scales of any magnitude: one form for any number of columns (fp16 rows have no power of two to take out)
+        if (w->wide && dtype != MOE_DTYPE_F16) return go(w4_kernel<G, ZP, F32, 4, true>, &d[3]);
+        if (a.nt_max == 1) return go(w4_kernel<G, ZP, F32, 1, false>, &d[0]);
+        return a.nt_max == 2 ? go(w4_kernel<G, ZP, F32, 2, false>, &d[1]) : go(w4_kernel<G, ZP, F32, 4, false>, &d[2]);
     };
     auto by_zeros = [&](auto gc, auto fc) {
         return w->zeros ? by_types(gc, std::true_type(), fc) : by_types(gc, std::false_type(), fc);

@@ -387,3 +387,71 @@ def test_small_values_beside_a_large_one(ops, dtype, largest):
     else:
         tol = torch.maximum(v.abs() * 2.0 ** -22, torch.full_like(v, top * 2.0 ** -50)) + U * 1.001 * v.abs()
     assert torch.all((y - v).abs() <= tol)
+
+
+def far_scales(mat, scale, seed):
+    """The matrix with bf16 scales of magnitude 0.5 .. 1.5 times `scale` (a number, or one per weight row)."""
+    q, s, z = mat
+    g = gen(seed)
+    v = (torch.rand(s.shape, generator=g, device="cuda", dtype=torch.float64) + 0.5) * torch.sign(s).double()
+    return q, (v * scale).float().to(BF16), z
+
+
+def far_close(y, x, mats, start, G, dtype):
+    """test_product's tolerance, and what the smallest fp32 numbers add: each of the K / G + 35 sums is off by up to
+    2^-150, 2^13 times that where the row's largest passes 2^115; compared where no sum can leave fp32's range."""
+    ref, err = reference(mats, x, start, G)
+    small = x.double().abs().amax(1, keepdim=True) < 2.0 ** 115
+    step = torch.where(small, 2.0 ** -13, 1.0).double() * 2.0 ** -137  # in float64: 2^-150 is 0 in fp32
+    err = err + (x.shape[1] / G + 35) * step
+    inside = product(mats[0], x, start)[1] < 2.0 ** 125
+    assert torch.all(torch.isfinite(y[inside])) and int(inside.sum()) > 0
+    tol = err + HALF[dtype] * (ref.abs() + err) * 1.001 + TINY[dtype]
+    close(torch.where(inside, y.double(), 0.0), torch.where(inside, ref, 0.0), tol)
+    return ref[inside]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("E,R,K,G,rows,zeros", [(1, 40, 256, 32, 1, False), (1, 33, 1280, 128, 20, True),
+                                                (3, 24, 160, 32, 25, True), (2, 50, 384, 64, 9, False)])
+@pytest.mark.parametrize("scale,value", [(100, -110), (125, -128), (-120, 100), (-125, 124), (60, -125), (-60, 60),
+                                         (-10, 120)])
+def test_scales_over_all_of_bf16(ops, scale, value, E, R, K, G, rows, zeros, dtype):
+    """Large scales with small rows and small scales with large rows: finite wherever the definition's sums are."""
+    mat = far_scales(matrix(E, R, K, G, BF16, zeros, 1), 2.0 ** scale, 2)
+    w = ops.MoeW4Weights(*mat)
+    start = segments(E, rows, K)
+    es = None if E == 1 else torch.tensor(start, dtype=torch.int32, device="cuda")
+    x = (torch.randn((rows, K), generator=gen(3), device="cuda", dtype=torch.float64) * 2.0 ** value).float().to(dtype)
+    y = ops.moe_w4_matvec(w, x, es, ops.new_sort_workspace(1, 1, 1))
+    assert float(far_close(y, x, [mat], start, G, dtype).abs().max()) > 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_scales_and_rows_of_many_magnitudes_together(ops, dtype):
+    """A power of two for each weight row and for each activation row, from one end of the types to the other; a
+    matrix of ordinary scales in the same handle keeps the bits that it has without the others."""
+    R, K, G, rows = 57, 320, 32, 38
+    near = matrix(1, R, K, G, BF16, True, 1)
+    power = torch.arange(R, device="cuda", dtype=torch.float64) * 4 - 112
+    far = far_scales(near, torch.exp2(power).view(1, R, 1), 2)
+    both = [torch.cat((a, b)) for a, b in zip(near, far)]
+    start = [0, rows, 2 * rows]
+    x = torch.randn((rows, K), generator=gen(3), device="cuda", dtype=torch.float64)
+    x = (x * torch.exp2(torch.arange(rows, device="cuda").double().view(-1, 1) * 6 - 112)).float().to(dtype)
+    x = torch.cat((x, x))
+    ws, es = ops.new_sort_workspace(1, 1, 1), torch.tensor(start, dtype=torch.int32, device="cuda")
+    y = ops.moe_w4_matvec(ops.MoeW4Weights(*both), x, es, ws)
+    far_close(y, x, [both], start, G, dtype)
+    plain = ops.moe_w4_matvec(ops.MoeW4Weights(*(torch.cat((a, a)) for a in near)), x, es, ws)
+    assert torch.equal(plain[4:rows], y[4:rows])  # from rows of 2^-88 on, where no sum nears the smallest numbers
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_gate_and_up_of_far_scales(ops, dtype):
+    R, K, G, rows = 40, 256, 64, 11
+    gate = far_scales(matrix(1, R, K, G, BF16, False, 1), 2.0 ** 98, 2)
+    up = far_scales(matrix(1, R, K, G, BF16, False, 4), 2.0 ** 120, 5)
+    x = (torch.randn((rows, K), generator=gen(3), device="cuda", dtype=torch.float64) * 2.0 ** -104).float().to(dtype)
+    y = ops.moe_w4_matvec(ops.MoeW4Weights(*gate, *up), x, None, ops.new_sort_workspace(1, 1, 1))
+    far_close(y, x, [gate, up], [0, rows], G, dtype)

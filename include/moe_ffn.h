@@ -498,7 +498,8 @@ int moe_ffn_prefill_timed(moe_weights_t w, const float *hidden, const float *rou
  * ws: status word and scratch, 256-byte aligned, moe_sort_workspace_size bytes
  * for moe_sort_tokens and 256 for the others, initialised once by
  * moe_workspace_init (any workspace of this library that is large enough).
- * Outputs overlap no input and no other output (MOE_ERR_INVALID_ARG).
+ * Outputs overlap no input and no other output (MOE_ERR_INVALID_ARG).  Column
+ * slices of one buffer, rows equally far apart, do not.
  * ------------------------------------------------------------------------- */
 enum moe_dtype { MOE_DTYPE_F32 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_BF16 = 2 };
 
@@ -599,7 +600,7 @@ int moe_w4_weights_shape(moe_w4_weights_t w, int *E, int *R, int *K, int *group,
 size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
 
 /* y[j] = the handle's product of row x[j], for rows in CSR order (moe_sort_tokens).
- *   x [n_rows][K], y [n_rows][R] of `dtype`, n_rows >= 1; strides as for moe_sort_tokens
+ *   x [n_rows][K], y [n_rows][R] of `dtype`, n_rows >= 1; strides and overlaps as for moe_sort_tokens
  *   expStart [E+1] int32 device: rows expStart[e]..expStart[e+1]-1 are expert e's;
  *            rows from expStart[E] on are left as they were.  NULL (E == 1 only):
  *            every row is expert 0's.  Offsets that do not start at 0, decrease or

@@ -114,17 +114,24 @@ int check_ws(const void *ws, size_t ws_bytes, size_t need) {
     return ws_bytes >= need ? MOE_OK : MOE_ERR_WORKSPACE_TOO_SMALL;
 }
 
-// Bytes from the first to past the last element of `rows` rows of `cols`, `stride` apart.
+// `rows` rows of `cols` elements, `stride` elements apart, in bytes: n from the first to past the last, `row` each.
 struct Span {
     const char *p;
-    int64_t n;
+    int64_t n, row, stride;
 };
 Span span(const void *p, int64_t rows, int64_t stride, int64_t cols, int64_t elem) {
-    return {static_cast<const char *>(p), p && rows > 0 ? ((rows - 1) * stride + cols) * elem : 0};
+    return {static_cast<const char *>(p), p && rows > 0 ? ((rows - 1) * stride + cols) * elem : 0, cols * elem,
+            rows > 1 ? stride * elem : 0};
 }
+// Rows that lie equally far apart, or a single row and such rows, may take turns (column slices of one buffer): they
+// are apart where their places within a stride are.
 bool overlap(const Span &a, const Span &b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+    if (a.n <= 0 || b.n <= 0 || x >= y + (uintptr_t)b.n || y >= x + (uintptr_t)a.n) return false;
+    const int64_t st = a.n == a.row ? b.stride : a.stride;
+    if (st <= 0 || (b.n != b.row && b.stride != st)) return true;
+    const int64_t at = y >= x ? (int64_t)((y - x) % st) : (st - (int64_t)((x - y) % st)) % st;  // of b, from a's place
+    return a.row > at || at + b.row > st;
 }
 // No output overlaps another output or an input.
 bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {

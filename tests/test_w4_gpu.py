@@ -455,3 +455,28 @@ def test_gate_and_up_of_far_scales(ops, dtype):
     x = (torch.randn((rows, K), generator=gen(3), device="cuda", dtype=torch.float64) * 2.0 ** -104).float().to(dtype)
     y = ops.moe_w4_matvec(ops.MoeW4Weights(*gate, *up), x, None, ops.new_sort_workspace(1, 1, 1))
     far_close(y, x, [gate, up], [0, rows], G, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("rows", [1, 2, 13])
+def test_rows_and_products_as_slices_of_one_buffer(ops, rows, dtype):
+    """Columns side by side do not overlap, in either order or a row further on; one shared column does."""
+    R, K = 48, 96
+    w = ops.MoeW4Weights(*matrix(1, R, K, 32, F16, False, 1))
+    ws = ops.new_sort_workspace(1, 1, 1)
+    v = torch.randn((rows, K), generator=gen(2), device="cuda").to(dtype)
+    want = ops.moe_w4_matvec(w, v, None, ws)
+    for at, to, later in ((0, K, 0), (R, 0, 0), (R + 7, 3, 0), (0, K + 5, 0), (R, 0, 1), (0, K, 1)):
+        buf = torch.full((rows + later, K + R + 16), 3.0, dtype=dtype, device="cuda")
+        x, y = buf[:rows, at:at + K], buf[later:, to:to + R]
+        x.copy_(v)
+        left = torch.ones_like(buf, dtype=torch.bool)
+        left[later:, to:to + R] = False
+        kept = buf.clone()
+        assert torch.equal(ops.moe_w4_matvec(w, x, None, ws, y=y), want)
+        assert torch.equal(buf[left], kept[left])
+    for at, to, later in ((0, K - 1, 0), (R - 1, 0, 0), (0, 0, 0)) + (((R - 1, 0, 1), (0, K - 1, 1)) if rows > 1 else ()):
+        buf = torch.zeros((rows + later, K + R + 16), dtype=dtype, device="cuda")
+        with pytest.raises(ops.MoeError) as err:
+            ops.moe_w4_matvec(w, buf[:rows, at:at + K], None, ws, y=buf[later:, to:to + R])
+        assert err.value.code == -1

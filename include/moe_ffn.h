@@ -497,7 +497,8 @@ int moe_ffn_prefill_timed(moe_weights_t w, const float *hidden, const float *rou
  * otherwise; the results are the same.
  * ws: status word and scratch, 256-byte aligned, moe_sort_workspace_size bytes
  * for moe_sort_tokens and 256 for the others, initialised once by
- * moe_workspace_init (any workspace of this library that is large enough).
+ * moe_workspace_init (any workspace of this library that is large enough: no
+ * more than those bytes at its start are used, and arguments may lie behind them).
  * Outputs overlap no input and no other output (MOE_ERR_INVALID_ARG).  Column
  * slices of one buffer, rows equally far apart, do not.
  * ------------------------------------------------------------------------- */

@@ -760,12 +760,13 @@ int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *t
     if (!x || !topk_idx || !expStart || !expTokI || !expTokK || !tokRow || !rows || !dtype_ok(dtype) || x_stride < 0)
         return MOE_ERR_INVALID_ARG;
     if (!token_shape_ok(N, top_k, E) || D < 1 || D > MAX_ROW || x_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
-    int rc = check_ws(ws, ws_bytes, moe_sort_workspace_size(N, top_k, E));
+    const size_t used = moe_sort_workspace_size(N, top_k, E);
+    int rc = check_ws(ws, ws_bytes, used);
     if (rc) return rc;
     const int64_t Nk = (int64_t)N * top_k, b = (int64_t)dtype_bytes(dtype);
     if (!aligned(x, b) || !aligned(rows, b) || !aligned4({topk_idx, expStart, expTokI, expTokK, tokRow})) return MOE_ERR_INVALID_ARG;
     if (!apart({span(expStart, 1, 0, E + 1, 4), span(expTokI, 1, 0, Nk, 4), span(expTokK, 1, 0, Nk, 4),
-                span(tokRow, 1, 0, Nk, 4), span(rows, Nk, D, D, b), span(ws, 1, 0, (int64_t)ws_bytes, 1)},
+                span(tokRow, 1, 0, Nk, 4), span(rows, Nk, D, D, b), span(ws, 1, 0, (int64_t)used, 1)},
                {span(x, N, x_stride, D, b), span(topk_idx, 1, 0, Nk, 4)}))
         return MOE_ERR_INVALID_ARG;
     return launch_sort_tokens(x, x_stride, dtype, topk_idx, N, top_k, E, D, expStart, expTokI, expTokK, tokRow, rows,

@@ -556,3 +556,26 @@ def test_refused_tensors(ops):
             call()
         assert err.value.code == code
     assert ops.moe_workspace_status(ws) == 0
+
+
+def test_sort_of_a_routing_that_lies_in_the_workspace(ops):
+    """A layer's workspace serves the sort of the routing that the layer left in it: only the scratch at its start may
+    not hold arguments."""
+    from mixture_experts_ffn_top_gb300.workloads import WORKLOADS, make_inputs
+
+    wl = WORKLOADS["tiny"]
+    inp = make_inputs(wl)
+    layer = ops.MoeLayer.from_numpy(inp, device="cuda:0", top_k=wl.top_k, max_tokens=wl.N)
+    x = torch.from_numpy(np.ascontiguousarray(inp["hidden"])).cuda()
+    layer.prefill(x, wl.top_k, wl.norm_topk_prob)
+    views = ops.moe_workspace_views(layer.ws, wl.N, wl.D, wl.E, wl.F, wl.top_k, layer.w.Fs)
+    idx, weights, start = (views[n].clone() for n in ("topk_idx", "topk_w", "expStart"))
+    got = ops.moe_sort_tokens(x, views["topk_idx"], wl.E, layer.ws)
+    ref = ops.moe_sort_tokens(x, idx, wl.E, ops.new_sort_workspace(wl.N, wl.top_k, wl.E))
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and torch.equal(got[1], start)
+    assert torch.equal(views["topk_idx"], idx) and torch.equal(views["topk_w"], weights)
+    assert layer.status() == 0
+    inside = layer.ws[256:256 + 4 * idx.numel()].view(torch.int32).view(wl.N, wl.top_k)
+    with pytest.raises(ops.MoeError) as err:
+        ops.moe_sort_tokens(x, inside, wl.E, layer.ws)
+    assert err.value.code == -1

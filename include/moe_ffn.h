@@ -524,6 +524,18 @@ int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *t
                     int top_k, int E, int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK,
                     int32_t *tokRow, void *rows, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/* Failure-detection check of the sort's copies: runs moe_sort_tokens with every
+ * copy in waiting for more bytes than it brings, so that no wait can end, and a
+ * limit of limit_ms (1..2000) instead of the normal two seconds (the copies
+ * waited for after the first timeout have that limit each again).  Sets
+ * MOE_DEV_TIMEOUT; the CSR and tokRow are right, every row is left as it was,
+ * and workspace and context stay usable.  Only where the rows go by bulk copies
+ * (x, rows, x_stride and D multiples of 16 bytes): else MOE_ERR_UNSUPPORTED_SHAPE. */
+int moe_debug_sort_wait_timeout(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N,
+                                int top_k, int E, int D, int32_t *expStart, int32_t *expTokI,
+                                int32_t *expTokK, int32_t *tokRow, void *rows, int limit_ms, void *ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
 /* Its gradient: d_x[t][c] = sum over the slots s of t, in slot order, of
  * d_rows[tokRow[t][s]][c] (dropped entries add nothing; a token without
  * entries gets zeros).  d_rows [n_rows][D], d_x [N][D].  An entry of tokRow

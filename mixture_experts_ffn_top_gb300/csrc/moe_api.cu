@@ -754,9 +754,9 @@ size_t moe_sort_workspace_size(int N, int top_k, int E) {
     return SORT_SCRATCH_OFFSET + align256(sort_scratch_bytes(N, E));
 }
 
-int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N, int top_k, int E,
-                    int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows,
-                    void *ws, size_t ws_bytes, cudaStream_t stream) {
+static int sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N, int top_k, int E,
+                       int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows,
+                       void *ws, size_t ws_bytes, cudaStream_t stream, unsigned long long starved_ns = 0) {
     if (!x || !topk_idx || !expStart || !expTokI || !expTokK || !tokRow || !rows || !dtype_ok(dtype) || x_stride < 0)
         return MOE_ERR_INVALID_ARG;
     if (!token_shape_ok(N, top_k, E) || D < 1 || D > MAX_ROW || x_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -770,7 +770,22 @@ int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *t
                {span(x, N, x_stride, D, b), span(topk_idx, 1, 0, Nk, 4)}))
         return MOE_ERR_INVALID_ARG;
     return launch_sort_tokens(x, x_stride, dtype, topk_idx, N, top_k, E, D, expStart, expTokI, expTokK, tokRow, rows,
-                              ws, stream);
+                              ws, stream, starved_ns);
+}
+
+int moe_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N, int top_k, int E,
+                    int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows,
+                    void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return sort_tokens(x, x_stride, dtype, topk_idx, N, top_k, E, D, expStart, expTokI, expTokK, tokRow, rows, ws,
+                       ws_bytes, stream);
+}
+
+int moe_debug_sort_wait_timeout(const void *x, int64_t x_stride, int dtype, const int32_t *topk_idx, int N, int top_k,
+                                int E, int D, int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow,
+                                void *rows, int limit_ms, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (limit_ms < 1 || limit_ms > 2000) return MOE_ERR_INVALID_ARG;
+    return sort_tokens(x, x_stride, dtype, topk_idx, N, top_k, E, D, expStart, expTokI, expTokK, tokRow, rows, ws,
+                       ws_bytes, stream, (unsigned long long)limit_ms * 1000000ull);
 }
 
 int moe_sort_tokens_grad(const void *d_rows, int64_t n_rows, int dtype, const int32_t *tokRow, int N, int top_k,

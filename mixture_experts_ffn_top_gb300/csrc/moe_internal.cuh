@@ -191,9 +191,10 @@ int launch_rmsnorm(const float *x, const float *gamma, float eps, int N, int D, 
 constexpr size_t SORT_SCRATCH_OFFSET = 256;
 int sort_ranges(int N, int *tokens);
 size_t sort_scratch_bytes(int N, int E);
+// starved_ns: failure-detection check, loads that never complete and this limit of their waits (0 normally)
 int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *idx, int N, int top_k, int E, int D,
                        int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows, void *ws,
-                       cudaStream_t s);
+                       cudaStream_t s, unsigned long long starved_ns = 0);
 // w == NULL: plain sums (the gradient of the sort)
 int launch_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t *tokRow, const float *w, int N,
                          int top_k, int D, void *out, int64_t out_stride, unsigned *status, cudaStream_t s);

@@ -117,13 +117,15 @@ enum SortCounts { COUNT_HERE, COUNT_TABLE, COUNT_SCANNED };
 // 4 us for the order: 2048 x 2048 bf16, top 8 of 64, 17.0 us (76 MB: 66% of the copy rate), 16384 tokens
 // 106.5 us (84%; rows that lie apart cost the writes some of it, a plain scatter of such rows with the order
 // given takes 104 us).  Rows read by the sorted order instead measured 125 - 155 us there (x eight times
-// from L2).
+// from L2).  wait_ns: limit of a wait for a load; starve (failure-detection check, 0 normally): bytes that every
+// load waits for beyond its own.
 template <bool BULK, SortCounts COUNTS>
 __global__ void __launch_bounds__(SORT_THREADS)
 sort_rows_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ idx, int n_entries,
                  int tokens, int top_k, int E, int row_bytes, const int *table, int32_t *__restrict__ expStart,
                  int32_t *__restrict__ expTokI, int32_t *__restrict__ expTokK, int32_t *tokRow,
-                 char *__restrict__ rows, int piece, int slots, int ring, unsigned *__restrict__ status) {
+                 char *__restrict__ rows, int piece, int slots, int ring, unsigned long long wait_ns, int starve,
+                 unsigned *__restrict__ status) {
     // the copying kernel, if there is one, may be scheduled now
     if (!BULK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(128) char smem[];
@@ -144,7 +146,7 @@ sort_rows_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *__
         const uint32_t bar = tc::smem_u32(&bars[warp * SORT_SLOTS + u % slots]);
         const int64_t t = t0 + (u / pieces) * SORT_WARPS + warp;
         const int bytes = unit_bytes(u);
-        tc::mbar_expect_tx(bar, bytes);
+        tc::mbar_expect_tx(bar, bytes + starve);
         tc::bulk_load(tc::smem_u32(smem + warp * ring + (u % slots) * piece),
                       x + t * x_stride + (int64_t)(u % pieces) * piece, bytes, bar);
     };
@@ -276,7 +278,7 @@ sort_rows_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *__
             const uint32_t bar = tc::smem_u32(&bars[warp * SORT_SLOTS + slot]);
             const int t = (u / pieces) * SORT_WARPS + warp;
             const int r = lane < top_k ? pos[t * top_k + lane] : -1;
-            const bool here = tc::mbar_wait(bar, (u / slots) & 1, &abort_s, status, SORT_WAIT_NS);
+            const bool here = tc::mbar_wait(bar, (u / slots) & 1, &abort_s, status, wait_ns);
             if (!__all_sync(0xffffffffu, here)) break;  // a copy that never came: flagged, its rows are left
             if (r >= 0)
                 bulk_store(rows + (int64_t)r * row_bytes + (int64_t)(u % pieces) * piece,
@@ -292,7 +294,7 @@ sort_rows_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *__
         for (int p = u; p < min(units, u + slots - (u > 0)); ++p) {
             const uint64_t since = tc::globaltimer();
             while (!tc::mbar_try(tc::smem_u32(&bars[warp * SORT_SLOTS + p % slots]), (p / slots) & 1) &&
-                   tc::globaltimer() - since < SORT_WAIT_NS) {
+                   tc::globaltimer() - since < wait_ns) {
             }
         }
         bulk_wait_read<0>();
@@ -613,7 +615,7 @@ size_t sort_scratch_bytes(int N, int E) { return (size_t)(sort_ranges(N, nullptr
 
 int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t *idx, int N, int top_k, int E, int D,
                        int32_t *expStart, int32_t *expTokI, int32_t *expTokK, int32_t *tokRow, void *rows, void *ws,
-                       cudaStream_t s) {
+                       cudaStream_t s, unsigned long long starved_ns) {
     int tokens = 0;
     const int ranges = sort_ranges(N, &tokens);
     const int n = N * top_k;
@@ -623,6 +625,9 @@ int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t
     const int64_t xb = x_stride * eb;
     const int width = access_bytes({x, rows}, {xb, row_bytes});
     const bool bulk = width == 16;
+    if (starved_ns && !bulk) return MOE_ERR_UNSUPPORTED_SHAPE;  // no waits to check
+    const unsigned long long wait_ns = starved_ns ? starved_ns : SORT_WAIT_NS;
+    const int starve = starved_ns ? 16 : 0;
     // shared memory: the experts' counts, and the rest (at most SORT_RING a warp) for pieces of rows, as few as
     // the ring holds at two a warp, of equal size
     const int shares = std::min(SORT_WARPS, (tokens * top_k + 31) / 32);
@@ -649,9 +654,10 @@ int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t
         if (rc) return rc;
         if (how != COUNT_HERE)
             return launch_early(kernel, dim3(ranges), dim3(SORT_THREADS), smem, s, xc, xb, idx, n, tokens, top_k, E,
-                                row_bytes, table, expStart, expTokI, expTokK, tokRow, out, piece, slots, ring, status);
+                                row_bytes, table, expStart, expTokI, expTokK, tokRow, out, piece, slots, ring, wait_ns,
+                                starve, status);
         kernel<<<ranges, SORT_THREADS, smem, s>>>(xc, xb, idx, n, tokens, top_k, E, row_bytes, table, expStart, expTokI,
-                                                  expTokK, tokRow, out, piece, slots, ring, status);
+                                                  expTokK, tokRow, out, piece, slots, ring, wait_ns, starve, status);
         return launch_status();
     };
     auto by_counts = [&](auto bc) {

@@ -69,6 +69,7 @@ _SIGS = {
     "moe_workspace_views": (_I, [_P, _I, _I, _I, _I, _I, _I] + [ctypes.POINTER(_P)] * 10),
     "moe_sort_workspace_size": (_SZ, [_I, _I, _I]),
     "moe_sort_tokens": (_I, [_P, _I64, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_debug_sort_wait_timeout": (_I, [_P, _I64, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "moe_sort_tokens_grad": (_I, [_P, _I64, _I, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
     "moe_unsort_tokens": (_I, [_P, _I64, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
     "moe_unsort_tokens_grad": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I, _P, _P, _P, _SZ, _P]),
@@ -700,6 +701,19 @@ def moe_sort_tokens(x, topk_idx, E, ws, rows=None, stream=None):
     _on(dev, stream, "moe_sort_tokens", xp, xs, DTYPES[x.dtype], ip, N, k, E, D, start.data_ptr(), tok.data_ptr(),
         slot.data_ptr(), row.data_ptr(), rp, *_ws(ws, dev))
     return rows, start, tok, slot, row
+
+
+def moe_debug_sort_wait_timeout(x, topk_idx, E, rows, limit_ms, ws, stream=None):
+    """moe_sort_tokens with copies that never complete (their waits bounded by limit_ms); the outcome is read with
+    moe_workspace_status."""
+    xp, xs = _rows_arg(x, "x")
+    (N, D), k, dev = x.shape, topk_idx.shape[1], x.get_device()
+    start, tok, slot = (torch.full((n,), -7, dtype=torch.int32, device=x.device) for n in (E + 1, N * k, N * k))
+    row = torch.full((N, k), -7, dtype=torch.int32, device=x.device)
+    _on(dev, stream, "moe_debug_sort_wait_timeout", xp, xs, DTYPES[x.dtype],
+        _arg(topk_idx, torch.int32, (N, k), dev, "topk_idx"), N, k, E, D, start.data_ptr(), tok.data_ptr(), slot.data_ptr(),
+        row.data_ptr(), _arg(rows, x.dtype, (N * k, D), dev, "rows"), int(limit_ms), *_ws(ws, dev))
+    return start, tok, slot, row
 
 
 def moe_sort_tokens_grad(d_rows, tokRow, ws, d_x=None, stream=None):

@@ -117,3 +117,11 @@ def test_binding_refuses_host_tensors():
                  lambda: ops.MoeW4Weights(torch.zeros((4, 16), dtype=torch.uint8), torch.ones((4, 1)).half())):
         with pytest.raises(ValueError):
             call()
+
+
+def test_sort_wait_check_refuses_limits(lib):
+    args = with_(SORT)
+    for ms in (0, -1, 2001):
+        assert lib.moe_debug_sort_wait_timeout(*args[:13], ms, *args[13:]) == INVALID
+    assert lib.moe_debug_sort_wait_timeout(*with_(SORT, N=0)[:13], 20, *args[13:]) == SHAPE
+    assert lib.moe_debug_sort_wait_timeout(*with_(SORT, D=63, x_stride=63)[:13], 20, *args[13:]) == SHAPE

@@ -579,3 +579,35 @@ def test_sort_of_a_routing_that_lies_in_the_workspace(ops):
     with pytest.raises(ops.MoeError) as err:
         ops.moe_sort_tokens(x, inside, wl.E, layer.ws)
     assert err.value.code == -1
+
+
+@pytest.mark.parametrize("N,D,E,k", [(3, 64, 8, 2), (700, 2048, 16, 4), (2048, 9000, 300, 3)])
+def test_sort_gives_up_copies_that_never_complete(ops, N, D, E, k):
+    """Every warp's first wait runs out, then its waits for the other copies in flight: a timeout in the status word
+    within bounds, the order as ever, no row written, and the same workspace serves the next call."""
+    import time
+
+    x, idx = values((N, D), torch.bfloat16, 1), routing(N, E, k, 0.1)
+    ws = ops.new_sort_workspace(N, k, E)
+    rows = torch.full((N * k, D), 7.5, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    since = time.time()
+    got = ops.moe_debug_sort_wait_timeout(x, idx, E, rows, 20, ws)
+    assert ops.moe_workspace_status(ws) == 4  # synchronises
+    assert time.time() - since < 10  # five waits of 20 ms a CTA, every CTA in one wave
+    assert torch.all(rows == 7.5)
+    ref = ops.moe_sort_tokens(x, idx, E, ws, rows=rows)
+    assert ops.moe_workspace_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, ref[1:]))
+    _, entries, _ = order(idx, E)
+    assert torch.equal(rows[:entries.size], x[torch.from_numpy(entries // k).cuda()])
+
+
+def test_sort_wait_check_needs_bulk_copies(ops):
+    idx = routing(6, 4, 2, 0.0)
+    rows, ws = torch.zeros((12, 33), dtype=torch.bfloat16, device="cuda"), ops.new_sort_workspace(6, 2, 4)
+    for x, out, ms, code in ((values((6, 33), torch.bfloat16, 1), rows, 20, -2),
+                             (values((6, 32), torch.bfloat16, 1), rows[:, :32].contiguous(), 0, -1)):
+        with pytest.raises(ops.MoeError) as err:
+            ops.moe_debug_sort_wait_timeout(x, idx, 4, out, ms, ws)
+        assert err.value.code == code

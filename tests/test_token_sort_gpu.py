@@ -611,3 +611,24 @@ def test_sort_wait_check_needs_bulk_copies(ops):
         with pytest.raises(ops.MoeError) as err:
             ops.moe_debug_sort_wait_timeout(x, idx, 4, out, ms, ws)
         assert err.value.code == code
+
+
+@pytest.mark.parametrize("N,D,E,k,drop,pad,shift,dtype", [
+    (40000, 24, 64, 8, 0.3, 0, 0, torch.bfloat16), (40000, 25, 64, 8, 0.1, 3, 1, torch.float16),
+    (20001, 16, 1024, 17, 0.6, 8, 0, torch.float32), (320001, 9, 3, 1, 0.2, 0, 0, torch.float32),
+    (11000, 8, 300, 32, 0.95, 0, 0, torch.float16), (38912, 33, 40, 8, 0.0, 0, 0, torch.bfloat16)])
+def test_sort_of_ranges_whose_ranks_wait_in_the_output(ops, N, D, E, k, drop, pad, shift, dtype):
+    """More than 2048 entries a range: their ranks wait in tokRow itself, for bulk copies and plain ones, with dropped
+    entries, whole tokens without any, and experts out of range among them.  (38912 x 8 is exactly 2048 a range.)"""
+    idx = routing(N, E, k, drop, N)
+    idx[N // 2: N // 2 + 300] = -1
+    x = values((N, D), dtype, 1, pad, shift)
+    check_sort(ops, x, idx, E)
+    want = idx.clone()
+    idx[::1009, 0], want[::1009, 0] = E, -1
+    ws = ops.new_sort_workspace(N, k, E)
+    got = ops.moe_sort_tokens(x, idx, E, ws)
+    assert ops.moe_workspace_status(ws) == 1
+    ref = ops.moe_sort_tokens(x, want, E, ws)
+    n = int(ref[1][-1])
+    assert torch.equal(got[0][:n], ref[0][:n]) and all(torch.equal(a, b) for a, b in zip(got[1:], ref[1:]))

@@ -632,3 +632,58 @@ def test_sort_of_ranges_whose_ranks_wait_in_the_output(ops, N, D, E, k, drop, pa
     ref = ops.moe_sort_tokens(x, want, E, ws)
     n = int(ref[1][-1])
     assert torch.equal(got[0][:n], ref[0][:n]) and all(torch.equal(a, b) for a, b in zip(got[1:], ref[1:]))
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("N,E,k", [(8, 40, 4), (9, 257, 7), (5000, 64, 8), (5003, 129, 3)])
+def test_topk_grad_of_far_apart_logits(ops, norm, N, E, k):
+    """Logits thousands and 3e38 apart, to the accuracy of near ones.  As topk_grad_reference, with L = max |l - m| taken
+    over the experts whose probability is not 0 in fp32 alone (expf is 0 below -104, exactly): those at 0 add nothing to
+    any sum, and where they stand for a probability below 2^-149 that and its gradient are off by less than 2^-146."""
+    l = torch.randn((N, E), generator=gen(N), device="cuda")
+    l[0::8] *= 1e4
+    l[1::8, 7] = 3e38
+    l[2::8] = torch.finfo(torch.float32).min
+    l[2::8, 3] = -3e38
+    l[3::8] *= 30
+    l[4::8, E // 2:] = -torch.inf
+    l[5::8, 1::2] -= 103.0  # on the edge of what expf returns
+    idx, _ = ops.moe_topk_from_logits(l, k, norm)
+    d_w = torch.randn((N, k), generator=gen(E), device="cuda")
+    ws = ops.new_sort_workspace(1, 1, 1)
+    got = ops.moe_topk_grad(l, idx, d_w, norm, ws)
+    assert ops.moe_workspace_status(ws) == 0
+    L, v = l.double(), torch.zeros((N, E), dtype=torch.float64, device="cuda")
+    v.scatter_(1, idx.long(), d_w.double())
+    chosen = torch.zeros((N, E), dtype=torch.bool, device="cuda").scatter_(1, idx.long(), True)
+    m = torch.where(chosen, L, -torch.inf) if norm else L
+    p = torch.softmax(m, dim=1)
+    below = m.amax(1, keepdim=True) - m
+    far = torch.where(below < 104, below, 0.0).amax(1, keepdim=True)
+    ref = p * (v - (p * v).sum(1, keepdim=True))
+    d, pv = (4 + far + E) * U, (p * v.abs()).sum(1, keepdim=True)
+    close(got, ref, (d + 3 * U) * ref.abs() + p * (d + E * U) * 2 * pv + 2.0 ** -146 * (v.abs() + pv + 1))
+    assert torch.all(got[1::8].abs() <= 2.0 ** -146)  # one expert has it all: nothing moves
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("N,E,k", [(16, 64, 8), (5000, 64, 8), (5003, 203, 7), (40, 700, 20)])
+def test_topk_grad_nan_and_infinity_stay_in_their_token(ops, norm, N, E, k):
+    l = torch.randn((N, E), generator=gen(N), device="cuda")
+    idx, _ = ops.moe_topk_from_logits(l, k, norm)
+    d_w = torch.randn((N, k), generator=gen(E), device="cuda")
+    ws = ops.new_sort_workspace(1, 1, 1)
+    clean = ops.moe_topk_grad(l, idx, d_w, norm, ws)
+    t = torch.arange(N, device="cuda")
+    l[t[3::9], idx[3::9, 0].long()] = float("nan")
+    l[t[5::9], idx[5::9, k - 1].long()] = float("inf")
+    d_w[7::9, 1] = float("nan")
+    got = ops.moe_topk_grad(l, idx, d_w, norm, ws)
+    bad = (t % 9 == 3) | (t % 9 == 5) | (t % 9 == 7)
+    assert torch.equal(got[~bad], clean[~bad])
+    assert torch.all(torch.isnan(got[bad].gather(1, idx[bad].long())))  # as the formula: every selected expert's
+    if norm:
+        others = torch.ones_like(got, dtype=torch.bool).scatter_(1, idx.long(), False)
+        assert torch.all(got[others] == 0)
+    else:
+        assert torch.all(torch.isnan(got[bad]))

@@ -307,8 +307,7 @@ template <int B>
 __global__ void __launch_bounds__(ROW_THREADS)
 sort_copy_kernel(const char *__restrict__ x, int64_t x_stride, const int32_t *tokRow, int N, int top_k, int row_bytes,
                  int tpt_log2, char *__restrict__ rows) {
-    using A = std::conditional_t<B == 16, uint4,
-                                 std::conditional_t<B == 8, uint2, std::conditional_t<B == 4, uint32_t, uint16_t>>>;
+    using A = std::conditional_t<B == 8, uint2, std::conditional_t<B == 4, uint32_t, uint16_t>>;
     extern __shared__ int row_s[];  // [tokens of the CTA][top_k]
     const int tpt = 1 << tpt_log2, per = ROW_THREADS >> tpt_log2;
     const int64_t t0 = (int64_t)blockIdx.x * per;
@@ -680,7 +679,6 @@ int launch_sort_tokens(const void *x, int64_t x_stride, int dtype, const int32_t
                             top_k, row_bytes, tl, out);
     };
     switch (width) {
-        case 16: return copy(std::integral_constant<int, 16>());
         case 8: return copy(std::integral_constant<int, 8>());
         case 4: return copy(std::integral_constant<int, 4>());
         default: return copy(std::integral_constant<int, 2>());

@@ -158,13 +158,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void wait_all_but(int n) {  // the n (0 .. 3) groups begun last
+__device__ __forceinline__ void wait_all_but(int n) {  // the n (0 .. 2) groups begun last
     if (n == 2)
         cp_async_wait<2>();
     else if (n == 1)
         cp_async_wait<1>();
-    else if (n == 3)
-        cp_async_wait<3>();
     else
         cp_async_wait<0>();
 }
@@ -178,7 +176,7 @@ struct W4Args {
     const int32_t *expStart;
     int n_rows, pass_rows;  // rows of an expert taken at a time
     int stage_rows;         // rows that shared memory holds
-    int slots;              // of a warp's ring: 2 to 4 pairs of records
+    int slots;              // of a warp's ring: 2 or 3 pairs of records
     int wk, wk_log2;        // warps that share a tile's chunks; the CTA's other warps take the next tiles
     int copy_log2, turn_log2;  // threads that share a row: as it is copied, as it is turned
     uint64_t ntiles_inv, pass_inv, grid_inv;  // for div_by

@@ -488,7 +488,8 @@ int moe_ffn_prefill_timed(moe_weights_t w, const float *hidden, const float *rou
  * the gradients.  Sums and weights are fp32, each result is rounded to the
  * element type once.
  *   dtype       enum moe_dtype of every tensor that is not stated otherwise
- *   D >= 1, N >= 1, 1 <= top_k <= min(E, 32), E <= 1024, N * top_k < 2^30
+ *   1 <= D <= 2^24, N >= 1, 1 <= top_k <= min(E, 32), E <= 1024, N * top_k < 2^30,
+ *   1 <= n_rows < 2^30 (MOE_ERR_UNSUPPORTED_SHAPE; MOE_ERR_INVALID_ARG for n_rows < 1)
  *   *_stride    elements from one row to the next (at most 2^30); an input's
  *               may be 0 (one row for all), an output's is at least D
  *   tokRow      [N][top_k] int32: the sorted row of each entry, or -1 for a
@@ -561,7 +562,7 @@ int moe_unsort_tokens(const void *rows, int64_t n_rows, int dtype, const int32_t
  *   d_topk_w[t][s] = sum_c d_out[t][c] * rows[tokRow[t][s]][c]  (fp32; 0 where dropped)
  * in one pass.  d_rows [n_rows][D]: rows that no entry names are left as they
  * were; two entries that name one row (moe_sort_tokens gives none) leave
- * either's value.  The dot's order is fixed for given N, D, type and
+ * either's value.  The dot's order is fixed for given N, top_k, D, type and
  * alignment. */
 int moe_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const void *rows, int64_t n_rows,
                            int dtype, const int32_t *tokRow, const float *topk_w, int N, int top_k,
@@ -595,7 +596,7 @@ int moe_topk_grad(const float *logits, const int32_t *topk_idx, const float *d_t
  *          in the high four bits of byte b
  *   scales [E][R][K/group] fp16 or bf16 (scale_dtype)
  *   zeros  [E][R][K/group] bytes, 0..15 (the low four bits count), or NULL: 8
- *   group  32, 64 or 128; K a multiple of it, at most 32768; R >= 1; E <= 1024
+ *   group  32, 64 or 128; K a multiple of it, at most 32768; 1 <= R <= 2^24; E <= 1024
  *   up_q, up_scales, up_zeros: NULL, or a second matrix of the same shape (up_zeros
  *          NULL iff zeros is): the handle then holds gate and up, and the product is
  *          y = SiLU(gate) * up, SiLU(z) = z / (1 + exp(-z)), in fp32 before the one
@@ -613,18 +614,23 @@ int moe_w4_weights_shape(moe_w4_weights_t w, int *E, int *R, int *K, int *group,
 size_t moe_w4_weights_device_bytes(moe_w4_weights_t w);
 
 /* y[j] = the handle's product of row x[j], for rows in CSR order (moe_sort_tokens).
- *   x [n_rows][K], y [n_rows][R] of `dtype`, n_rows >= 1; strides and overlaps as for moe_sort_tokens
+ *   x [n_rows][K], y [n_rows][R] of `dtype`; n_rows, strides and overlaps as for moe_sort_tokens
  *   expStart [E+1] int32 device: rows expStart[e]..expStart[e+1]-1 are expert e's;
  *            rows from expStart[E] on are left as they were.  NULL (E == 1 only):
  *            every row is expert 0's.  Offsets that do not start at 0, decrease or
  *            pass n_rows set MOE_DEV_BAD_CSR and every row is left.
  * Codes less zero points are exact, and so are fp16 rows; bf16 rows are exact down to 2^-31 of their
  * largest magnitude (smaller values lose at most 2^-39 of it); of fp32 rows at most 2^-22 of each value, or
- * 2^-50 of the row's largest, is lost.  Products are summed in fp32 per group and the groups' sums, times
- * their scales, in fp32, in an order that the weights' shape and the type fix: a row's result does not
- * depend on the rows beside it.  Sums leave fp32's range only where the definition's own do, whatever the
- * magnitudes of scales and rows.  An infinity or NaN stays in its row.  Made for few rows an expert
- * (decode): each 32 rows (fp32: 16) of an expert read its weights once more, and fewer where K is long.
+ * 2^-50 of the row's largest, is lost.  A group's products are summed by the tensor cores: 16 of them and the
+ * sum so far at a time, in fp32, but each addend may be cut 23 bits below the largest of them where fp32
+ * additions would round.  The groups' sums, times their scales, are added in fp32.  The weights' shape and the
+ * type fix the order: a row's result does not depend on the rows beside it.  Sums leave fp32's range only where
+ * the definition's own do, whatever the magnitudes of scales and rows.  An infinity or NaN stays in its row.
+ * Made for few rows an expert (decode).  An expert's weights are read once for each pass of at most
+ *   E > 1:  max(8, 2 ceil(n_rows / E)) of its rows (fp32: 4 in the place of 8), twice the mean, so that an expert
+ *           with more of them costs a pass for each as many;
+ *   E == 1: all rows (8 where R is so small that each 8 can have CTAs of their own; fp32: 4),
+ * in both cases at most 32 rows (fp32: 16), and fewer where K is long.
  * MOE_ERR_UNSUPPORTED_SHAPE past 2^31 pairs of 16 weight rows and such a pass.
  *   ws: status word (256 bytes). */
 int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype,

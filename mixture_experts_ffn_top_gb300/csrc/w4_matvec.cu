@@ -122,8 +122,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The 8 codes of a word, less the zero point, as four pairs (columns 2j, 2j + 1 of its 8): 1024 + q, or
-// 1024 + 16 q in the next four bits (a sixteenth of that is 64 + q); all of it exact.  off = 1024 + z and
+// The 8 codes of a word, less the zero point, as four pairs (columns 2j, 2j + 1 of its 8), by the conversion of
+// small integers that Kim, Henry, Fahim and Awadalla published ("Who Says Elephants Can't Run: Bringing Large Scale
+// MoE Models into Cloud Scale Production", 2022): a code under the exponent of 1024 is the fp16 number 1024 + q, or
+// 1024 + 16 q from the next four bits (a sixteenth of that is 64 + q); all of it exact.  off = 1024 + z and
 // off16 = -(64 + z), twice each.
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
     uint32_t d;

@@ -460,9 +460,10 @@ unsort_grad_kernel(const T *__restrict__ d_out, int64_t d_out_stride, const T *_
 // c = sum_s p[idx_s] d_w_s,  d_l[e] = p[e] (v[e] - c), v[e] the sum of d_w over the slots of e: -p[e] c at every
 // expert that no slot names (0 with norm, where the other logits are not even read), then the slots' own values
 // over it.  VEC: four experts an access (E % 4 == 0, aligned).  EPL experts per thread (EPL * TPT >= E).
-// Latency and launch bound at a router's sizes (2048 x 64 2.5 us), issue-bound with many tokens: the slots' rounds and
-// the butterflies are the same for a warp's 32 / TPT tokens as for one.  16384 x 256 normalised 5.5 us (the logits
-// and gradients of all experts once are 5.1 us of the copy rate; only the gradients and the slots' logits move).
+// Latency and launch bound at a router's sizes (2048 x 64 2.6 us); with many tokens the slots' rounds and the
+// butterflies, the same for a warp's 32 / TPT tokens as for one, are what the instructions go to.  16384 x 256
+// normalised 5.5 us (the logits and gradients of all experts once are 5.1 us of the copy rate; only the gradients and
+// the slots' logits move), with 26% of the issue slots busy; over all experts 53%.
 template <int EPL, bool VEC, int TPT>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
 topk_grad_kernel(const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ d_w,

@@ -637,6 +637,104 @@ int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype
                   const int32_t *expStart, int n_rows, void *y, int64_t y_stride, void *ws,
                   size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Norms of token rows with gradients (beside moe_rmsnorm), for training and for
+ * rows of any element type:
+ *   moe_layernorm:      y[t][c] = (x[t][c] - m_t) r_t gamma[c] (+ beta[c]),
+ *       m_t = mean(x[t]), r_t = 1 / sqrt(mean((x[t] - m_t)^2) + eps)
+ *   moe_layernorm_grad: with h = (x - m) r and g = gamma d_y, along each row
+ *       d_x = r (g - mean(g) - h mean(g h)),
+ *       d_gamma[c] = sum_t d_y[t][c] h[t][c],   d_beta[c] = sum_t d_y[t][c]
+ *   moe_rmsnorm_grad:   of moe_rmsnorm, h = x r, r = 1 / sqrt(mean(x^2) + eps):
+ *       d_x = r (g - h mean(g h)),   d_gamma[c] = sum_t d_y[t][c] h[t][c]
+ * x, d_y [N][D], y, d_x [N][D] of `dtype`, rows apart by their strides as for
+ * moe_sort_tokens (an input's may be 0: a gradient that is the same for all
+ * rows); gamma, beta (NULL: 0), d_gamma, d_beta (NULL: not wanted) [D] fp32.
+ * 1 <= D <= 32768, 1 <= N < 2^30 (MOE_ERR_UNSUPPORTED_SHAPE); eps > 0 and finite.
+ * The gradients form m and r from x again: nothing is kept by the forward call.
+ * Sums are fp32, in an order fixed for given N, D, type, alignment and device;
+ * the variance is summed from the deviations.  Each result is rounded to its type once.
+ * ws: moe_norm_workspace_size(N, D) bytes, as for moe_sort_tokens (the forward
+ * call needs none).  Outputs overlap no input and no other output.
+ * ------------------------------------------------------------------------- */
+int moe_layernorm(const void *x, int64_t x_stride, int dtype, const float *gamma, const float *beta, float eps, int N,
+                  int D, void *y, int64_t y_stride, cudaStream_t stream);
+size_t moe_norm_workspace_size(int N, int D);
+int moe_layernorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t x_stride, int dtype,
+                       const float *gamma, float eps, int N, int D, void *d_x, int64_t d_x_stride, float *d_gamma,
+                       float *d_beta, void *ws, size_t ws_bytes, cudaStream_t stream);
+int moe_rmsnorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t x_stride, int dtype,
+                     const float *gamma, float eps, int N, int D, void *d_x, int64_t d_x_stride, float *d_gamma,
+                     void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_matmul -- products of 16-bit rows with 16-bit matrices, one matrix or one
+ * per expert over rows in CSR order (moe_sort_tokens), the epilogue in the same
+ * pass:
+ *   y[j][r] = act(sum_k w[e][r][k] x[j][k] + bias[e][r])
+ *             (* (sum_k w_up[e][r][k] x[j][k] + bias_up[e][r]))  (+ residual[j][r])
+ *   dtype       MOE_DTYPE_F16 or MOE_DTYPE_BF16, of x, w, w_up, residual and y
+ *   x [n_rows][K], y [n_rows][R]; w, w_up (NULL: no second factor) [E][R][K]
+ *   bias, bias_up [E][R] fp32 or NULL (bias_up only with w_up)
+ *   act         enum moe_act; GELU is v Phi(v), Phi the normal distribution
+ *   residual    [n_rows][R] or NULL; it may be y itself (same stride)
+ *   expStart    [E+1] int32 device: rows expStart[e]..expStart[e+1]-1 are expert
+ *               e's; rows from expStart[E] on are left as they were.  NULL (E == 1
+ *               only): every row is expert 0's.  Offsets that do not start at 0,
+ *               decrease or pass n_rows set MOE_DEV_BAD_CSR and every row is left.
+ * K a multiple of 8, at most 2^24; x and w 16-byte aligned, x_stride a multiple of 8
+ * and at least K; y and the residual may lie anywhere (16-byte accesses are used
+ * where they fit).  1 <= E <= 1024, 1 <= R, E * R < 2^31, 1 <= n_rows < 2^30.
+ * Products are exact and summed in fp32 by the tensor cores (in an order that
+ * depends on the sizes, not on the other rows' values); the epilogue is fp32,
+ * its activations within 2^-18 of their values; one rounding to y's type.
+ * At most 32 rows run on a kernel made for few rows, which reads each touched
+ * expert's weights once; more rows on tiles of 128.  A row's NaN stays its own.
+ *   ws: status word (256 bytes). */
+enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
+
+int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const void *w_up, const float *bias,
+               const float *bias_up, int act, const void *residual, int64_t residual_stride, const int32_t *expStart,
+               int E, int n_rows, int R, int K, void *y, int64_t y_stride, void *ws, size_t ws_bytes,
+               cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_ffn_decode -- the whole layer for a decode batch of at most 32 tokens, with
+ * 16-bit expert weights as a program holds them (no handle), in one kernel:
+ *   l = routerW x[t]; (e_s, w_s) = softmax over all E and top-k of l, as moe_router_topk;
+ *   out[t] = sum_s w_s down[e_s] (SiLU(gate[e_s] x[t]) * (up[e_s] x[t]))
+ *            (+ sigmoid(shexp_gate . x[t]) shared(x[t]))  (+ residual[t])
+ *   dtype       MOE_DTYPE_F16 or MOE_DTYPE_BF16, of x, the expert weights, residual and out
+ *   x [N][D], out [N][D], residual [N][D] or NULL (it may be out itself, same stride)
+ *   routerW [E][D] fp32; gate, up [E][F][D], down [E][D][F]
+ *   sh_gate, sh_up [Fs][D], sh_down [D][Fs]: the shared expert, NULL iff Fs == 0;
+ *   shexp_gate [D] fp32, or NULL: the shared expert counts once
+ * D, F and Fs multiples of 8, D <= 32768, F, Fs <= 65536; x, the weights, routerW and
+ * shexp_gate 16-byte aligned, x_stride a multiple of 8 (or 0); 1 <= top_k <= min(E, 32),
+ * E <= 1024, 1 <= N <= 32.
+ * Sums are fp32; SiLU(gate) * up enters the second product with 16 significant bits
+ * (bf16) or 22 and more (fp16); one rounding to out's type.  The order of the sums is
+ * fixed for given sizes and device.  A NaN or infinite logit makes its own token's
+ * row NaN.
+ * The kernel takes every SM (a cooperative launch with two grid barriers, each wait
+ * limited to a second: MOE_DEV_TIMEOUT, after which out is undefined and
+ * moe_workspace_init comes before the next call).
+ *   ws: moe_decode_workspace_size bytes, 256-byte aligned, initialised once by
+ *   moe_workspace_init; two calls that may overlap must not share one. */
+size_t moe_decode_workspace_size(int N, int D, int E, int F, int top_k, int Fs);
+int moe_ffn_decode(const void *x, int64_t x_stride, int dtype, const float *routerW, const float *shexp_gate,
+                   const void *gate, const void *up, const void *down, const void *sh_gate, const void *sh_up,
+                   const void *sh_down, const void *residual, int64_t residual_stride, int N, int D, int E, int F,
+                   int Fs, int top_k, int norm_topk_prob, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                   cudaStream_t stream);
+
+/* Failure-detection check of its first grid barrier: moe_ffn_decode with the barrier waiting for one more arrival
+ * than there are CTAs, and a limit of limit_ms (1..1000).  Every CTA gives up, MOE_DEV_TIMEOUT is set, out is left as
+ * it was and the context stays usable; moe_workspace_init comes before the workspace's next call. */
+int moe_debug_decode_barrier_timeout(const void *x, int64_t x_stride, int dtype, const float *routerW, const void *gate,
+                                     const void *up, const void *down, int N, int D, int E, int F, int top_k, void *out,
+                                     int64_t out_stride, int limit_ms, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Device pointers to the intermediates moe_ffn_prefill leaves in `ws`
  * (valid after it ran on that workspace with the same shape); any output
  * pointer may be NULL.  Host pointers to receive device addresses. */

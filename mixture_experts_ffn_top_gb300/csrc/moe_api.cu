@@ -4,6 +4,7 @@
 // host memory (the caller's hidden and output rows, in place).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <initializer_list>
 #include <new>
 
@@ -925,6 +926,175 @@ int moe_w4_matvec(moe_w4_weights_t w, const void *x, int64_t x_stride, int dtype
                {span(x, n_rows, x_stride, w->K, b), span(expStart, 1, 0, w->E + 1, 4)}))
         return MOE_ERR_INVALID_ARG;
     return launch_w4_matvec(w, x, x_stride, dtype, expStart, n_rows, y, y_stride, status_word(ws), stream);
+}
+
+static bool eps_ok(float eps) { return eps > 0.0f && eps < INFINITY; }
+static bool norm_shape_ok(int N, int D) { return N >= 1 && N < (1 << 30) && D >= 1 && D <= NORM_MAX_D; }
+
+int moe_layernorm(const void *x, int64_t x_stride, int dtype, const float *gamma, const float *beta, float eps, int N,
+                  int D, void *y, int64_t y_stride, cudaStream_t stream) {
+    if (!x || !gamma || !y || !dtype_ok(dtype) || !eps_ok(eps) || x_stride < 0 || y_stride < D) return MOE_ERR_INVALID_ARG;
+    if (!norm_shape_ok(N, D) || x_stride > MAX_STRIDE || y_stride > MAX_STRIDE) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int64_t b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(x, b) || !aligned(y, b) || !aligned4({gamma, beta})) return MOE_ERR_INVALID_ARG;
+    if (!apart({span(y, N, y_stride, D, b)}, {span(x, N, x_stride, D, b), span(gamma, 1, 0, D, 4), span(beta, 1, 0, D, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_layernorm(x, x_stride, dtype, gamma, beta, eps, N, D, y, y_stride, stream);
+}
+
+size_t moe_norm_workspace_size(int N, int D) {
+    return norm_shape_ok(N, D) ? 256 + align256(norm_scratch_bytes(N, D)) : 0;
+}
+
+static int norm_grad(bool rms, const void *d_y, int64_t d_y_stride, const void *x, int64_t x_stride, int dtype,
+                     const float *gamma, float eps, int N, int D, void *d_x, int64_t d_x_stride, float *d_gamma,
+                     float *d_beta, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!d_y || !x || !gamma || !d_x || !d_gamma || !dtype_ok(dtype) || !eps_ok(eps) || d_y_stride < 0 || x_stride < 0 ||
+        d_x_stride < D)
+        return MOE_ERR_INVALID_ARG;
+    if (!norm_shape_ok(N, D) || x_stride > MAX_STRIDE || d_y_stride > MAX_STRIDE || d_x_stride > MAX_STRIDE)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    const size_t used = moe_norm_workspace_size(N, D);
+    int rc = check_ws(ws, ws_bytes, used);
+    if (rc) return rc;
+    const int64_t b = (int64_t)dtype_bytes(dtype);
+    if (!aligned(x, b) || !aligned(d_y, b) || !aligned(d_x, b) || !aligned4({gamma, d_gamma, d_beta})) return MOE_ERR_INVALID_ARG;
+    if (!apart({span(d_x, N, d_x_stride, D, b), span(d_gamma, 1, 0, D, 4), span(d_beta, 1, 0, D, 4), span(ws, 1, 0, (int64_t)used, 1)},
+               {span(d_y, N, d_y_stride, D, b), span(x, N, x_stride, D, b), span(gamma, 1, 0, D, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    return launch_norm_grad(rms, d_y, d_y_stride, x, x_stride, dtype, gamma, eps, N, D, d_x, d_x_stride, d_gamma, d_beta,
+                            ws, stream);
+}
+
+int moe_layernorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t x_stride, int dtype,
+                       const float *gamma, float eps, int N, int D, void *d_x, int64_t d_x_stride, float *d_gamma,
+                       float *d_beta, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return norm_grad(false, d_y, d_y_stride, x, x_stride, dtype, gamma, eps, N, D, d_x, d_x_stride, d_gamma, d_beta, ws,
+                     ws_bytes, stream);
+}
+
+int moe_rmsnorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t x_stride, int dtype,
+                     const float *gamma, float eps, int N, int D, void *d_x, int64_t d_x_stride, float *d_gamma,
+                     void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return norm_grad(true, d_y, d_y_stride, x, x_stride, dtype, gamma, eps, N, D, d_x, d_x_stride, d_gamma, nullptr, ws,
+                     ws_bytes, stream);
+}
+
+static bool aligned16(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (!aligned(p, 16)) return false;
+    return true;
+}
+// MOE_OK on a GB300, else the error (the kernels below use its tensor memory and clusters).
+static int device_check() {
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return major == 10 && minor == 3 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
+}
+
+int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const void *w_up, const float *bias,
+               const float *bias_up, int act, const void *residual, int64_t residual_stride, const int32_t *expStart,
+               int E, int n_rows, int R, int K, void *y, int64_t y_stride, void *ws, size_t ws_bytes,
+               cudaStream_t stream) {
+    if (!x || !w || !y || (dtype != MOE_DTYPE_F16 && dtype != MOE_DTYPE_BF16) || act < MOE_ACT_NONE || act > MOE_ACT_GELU)
+        return MOE_ERR_INVALID_ARG;
+    if ((bias_up && !w_up) || n_rows < 1 || x_stride < K || y_stride < R || (residual && residual_stride < 0))
+        return MOE_ERR_INVALID_ARG;
+    if (!expStart && E != 1) return MOE_ERR_INVALID_ARG;
+    if (E < 1 || E > MAX_E || R < 1 || (int64_t)E * R > 0x7fffffff || K < 8 || K % 8 || K > MAX_ROW || n_rows >= (1 << 30) ||
+        x_stride > MAX_STRIDE || y_stride > MAX_STRIDE || (residual && residual_stride > MAX_STRIDE))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    if (!aligned16({x, w, w_up}) || x_stride % 8 || !aligned(y, 2) || !aligned(residual, 2) || !aligned4({bias, bias_up, expStart}))
+        return MOE_ERR_INVALID_ARG;
+    const bool in_place = residual == y && residual_stride == y_stride;
+    const int64_t W = (int64_t)E * R;
+    if (!apart({span(y, n_rows, y_stride, R, 2), span(ws, 1, 0, 256, 1)},
+               {span(x, n_rows, x_stride, K, 2), span(w, W, K, K, 2), span(w_up, W, K, K, 2), span(bias, 1, 0, W, 4),
+                span(bias_up, 1, 0, W, 4), span(in_place ? nullptr : residual, n_rows, residual_stride, R, 2),
+                span(expStart, 1, 0, E + 1, 4)}))
+        return MOE_ERR_INVALID_ARG;
+    if ((rc = device_check())) return rc;
+    Matmul16Call c{};
+    c.x = x;
+    c.x_stride = x_stride;
+    c.dtype = dtype;
+    c.w = w;
+    c.w_up = w_up;
+    c.bias = bias;
+    c.bias_up = bias_up;
+    c.act = act;
+    c.residual = residual;
+    c.residual_stride = residual_stride;
+    c.expStart = expStart;
+    c.E = E;
+    c.n_rows = n_rows;
+    c.R = R;
+    c.K = K;
+    c.y = y;
+    c.y_stride = y_stride;
+    return launch_matmul16(c, status_word(ws), stream);
+}
+
+static bool decode_shape_ok(int N, int D, int E, int F, int top_k, int Fs) {
+    return N >= 1 && N <= DECODE_MAX_TOKENS && E >= 1 && E <= MAX_E && top_k >= 1 && top_k <= E && top_k <= 32 && D >= 8 &&
+           D % 8 == 0 && D <= 32768 && F >= 8 && F % 8 == 0 && F <= 65536 && Fs >= 0 && Fs % 8 == 0 && Fs <= 65536;
+}
+
+size_t moe_decode_workspace_size(int N, int D, int E, int F, int top_k, int Fs) {
+    return decode_shape_ok(N, D, E, F, top_k, Fs) ? decode16_ws_bytes(N, E, F, top_k, Fs) : 0;
+}
+
+static int ffn_decode(const Decode16Call &c, void *ws, size_t ws_bytes, cudaStream_t stream,
+                      unsigned long long limit_ns = 0) {
+    if (!c.x || !c.routerW || !c.gate || !c.up || !c.down || !c.out || (c.dtype != MOE_DTYPE_F16 && c.dtype != MOE_DTYPE_BF16))
+        return MOE_ERR_INVALID_ARG;
+    if (c.x_stride < 0 || c.out_stride < c.D || (c.residual && c.residual_stride < 0)) return MOE_ERR_INVALID_ARG;
+    if ((c.Fs > 0) != (c.sh_gate != nullptr) || (c.Fs > 0) != (c.sh_up != nullptr) || (c.Fs > 0) != (c.sh_down != nullptr) ||
+        (c.shexp_gate && c.Fs <= 0))
+        return MOE_ERR_INVALID_ARG;
+    if (!decode_shape_ok(c.N, c.D, c.E, c.F, c.top_k, c.Fs) || c.x_stride > MAX_STRIDE || c.out_stride > MAX_STRIDE ||
+        (c.residual && c.residual_stride > MAX_STRIDE))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    const size_t used = moe_decode_workspace_size(c.N, c.D, c.E, c.F, c.top_k, c.Fs);
+    int rc = check_ws(ws, ws_bytes, used);
+    if (rc) return rc;
+    if (!aligned16({c.x, c.routerW, c.shexp_gate, c.gate, c.up, c.down, c.sh_gate, c.sh_up, c.sh_down}) || c.x_stride % 8 ||
+        !aligned(c.out, 2) || !aligned(c.residual, 2))
+        return MOE_ERR_INVALID_ARG;
+    const bool in_place = c.residual == c.out && c.residual_stride == c.out_stride;
+    const int64_t EF = (int64_t)c.E * c.F;
+    if (!apart({span(c.out, c.N, c.out_stride, c.D, 2), span(ws, 1, 0, (int64_t)used, 1)},
+               {span(c.x, c.N, c.x_stride, c.D, 2), span(c.routerW, c.E, c.D, c.D, 4), span(c.shexp_gate, 1, 0, c.D, 4),
+                span(c.gate, EF, c.D, c.D, 2), span(c.up, EF, c.D, c.D, 2), span(c.down, EF, c.D, c.D, 2),
+                span(c.sh_gate, c.Fs, c.D, c.D, 2), span(c.sh_up, c.Fs, c.D, c.D, 2), span(c.sh_down, c.Fs, c.D, c.D, 2),
+                span(in_place ? nullptr : c.residual, c.N, c.residual_stride, c.D, 2)}))
+        return MOE_ERR_INVALID_ARG;
+    if ((rc = device_check())) return rc;
+    return launch_decode16(c, ws, stream, limit_ns, limit_ns ? 1 : 0);
+}
+
+int moe_ffn_decode(const void *x, int64_t x_stride, int dtype, const float *routerW, const float *shexp_gate,
+                   const void *gate, const void *up, const void *down, const void *sh_gate, const void *sh_up,
+                   const void *sh_down, const void *residual, int64_t residual_stride, int N, int D, int E, int F,
+                   int Fs, int top_k, int norm_topk_prob, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                   cudaStream_t stream) {
+    return ffn_decode({x, x_stride, dtype, routerW, shexp_gate, gate, up, down, sh_gate, sh_up, sh_down, residual,
+                       residual_stride, N, D, E, F, Fs, top_k, norm_topk_prob ? 1 : 0, out, out_stride},
+                      ws, ws_bytes, stream);
+}
+
+int moe_debug_decode_barrier_timeout(const void *x, int64_t x_stride, int dtype, const float *routerW, const void *gate,
+                                     const void *up, const void *down, int N, int D, int E, int F, int top_k, void *out,
+                                     int64_t out_stride, int limit_ms, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (limit_ms < 1 || limit_ms > 1000) return MOE_ERR_INVALID_ARG;
+    return ffn_decode({x, x_stride, dtype, routerW, nullptr, gate, up, down, nullptr, nullptr, nullptr, nullptr, 0, N, D, E,
+                       F, 0, top_k, 0, out, out_stride},
+                      ws, ws_bytes, stream, (unsigned long long)limit_ms * 1000000ull);
 }
 
 int moe_workspace_views(void *ws, int N, int D, int E, int F, int top_k, int Fs, int32_t **topk_idx, float **topk_w,

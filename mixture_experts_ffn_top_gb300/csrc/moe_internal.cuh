@@ -203,6 +203,52 @@ int launch_unsort_tokens_grad(const void *d_out, int64_t d_out_stride, const voi
                               unsigned *status, cudaStream_t s);
 int launch_topk_grad(const float *logits, const int32_t *idx, const float *d_w, int N, int E, int top_k, int norm,
                      float *d_logits, unsigned *status, cudaStream_t s);
+// norm.cu (scratch: the column sums of at most NORM_PARTS clusters, behind the status word of the workspace)
+constexpr int NORM_PARTS = 320;
+constexpr int NORM_MAX_D = 32768;
+size_t norm_scratch_bytes(int N, int D);
+int launch_layernorm(const void *x, int64_t x_stride, int dtype, const float *gamma, const float *beta, float eps, int N,
+                     int D, void *y, int64_t y_stride, cudaStream_t s);
+int launch_norm_grad(bool rms, const void *d_y, int64_t d_y_stride, const void *x, int64_t x_stride, int dtype,
+                     const float *gamma, float eps, int N, int D, void *d_x, int64_t d_x_stride, float *d_gamma,
+                     float *d_beta, void *ws, cudaStream_t s);
+// matmul16.cu
+struct Matmul16Call {
+    const void *x;
+    int64_t x_stride;
+    int dtype;
+    const void *w, *w_up;
+    const float *bias, *bias_up;
+    int act;
+    const void *residual;
+    int64_t residual_stride;
+    const int32_t *expStart;
+    int E, n_rows, R, K;
+    void *y;
+    int64_t y_stride;
+};
+int launch_matmul16(const Matmul16Call &c, unsigned *status, cudaStream_t s);
+// Tensor map of 16-bit rows [rows][cols], `stride` elements apart, read in 128-byte-swizzled boxes of 64 columns x
+// box_rows rows (false when the driver entry point or the encoding fails).
+bool encode_16bit_sw128_2d(CUtensorMap *m, const void *base, bool f16, uint64_t rows, uint64_t cols, int64_t stride,
+                           uint32_t box_rows);
+// decode16.cu
+struct Decode16Call {
+    const void *x;
+    int64_t x_stride;
+    int dtype;
+    const float *routerW, *shexp_gate;
+    const void *gate, *up, *down, *sh_gate, *sh_up, *sh_down, *residual;
+    int64_t residual_stride;
+    int N, D, E, F, Fs, top_k, norm;
+    void *out;
+    int64_t out_stride;
+};
+constexpr int DECODE_MAX_TOKENS = 32;
+size_t decode16_ws_bytes(int N, int E, int F, int top_k, int Fs);
+// barrier_ns, extra_arrivals: failure-detection check, a first barrier that cannot complete and its limit (0 normally)
+int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned long long barrier_ns = 0,
+                    int extra_arrivals = 0);
 // w4_matvec.cu
 int w4_repack(moe_w4_weights_s *w, const uint8_t *q, const void *scales, const uint8_t *zeros, const uint8_t *up_q,
               const void *up_scales, const uint8_t *up_zeros, cudaStream_t s);

@@ -21,7 +21,7 @@ _lib = None
 MOE_PATH_AUTO, MOE_PATH_MATVEC, MOE_PATH_TENSOR = 0, 1, 2
 QK = 32
 
-_P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
 # name -> (restype, argtypes)
 _SIGS = {
@@ -79,6 +79,14 @@ _SIGS = {
     "moe_w4_weights_shape": (_I, [_P] + [ctypes.POINTER(_I)] * 5),
     "moe_w4_weights_device_bytes": (_SZ, [_P]),
     "moe_w4_matvec": (_I, [_P, _P, _I64, _I, _P, _I, _P, _I64, _P, _SZ, _P]),
+    "moe_layernorm": (_I, [_P, _I64, _I, _P, _P, _F, _I, _I, _P, _I64, _P]),
+    "moe_norm_workspace_size": (_SZ, [_I, _I]),
+    "moe_layernorm_grad": (_I, [_P, _I64, _P, _I64, _I, _P, _F, _I, _I, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "moe_rmsnorm_grad": (_I, [_P, _I64, _P, _I64, _I, _P, _F, _I, _I, _P, _I64, _P, _P, _SZ, _P]),
+    "moe_matmul": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I, _P, _I64, _P, _I, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
+    "moe_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_ffn_decode": (_I, [_P, _I64, _I] + [_P] * 9 + [_I64] + [_I] * 7 + [_P, _I64, _P, _SZ, _P]),
+    "moe_debug_decode_barrier_timeout": (_I, [_P, _I64, _I] + [_P] * 4 + [_I] * 5 + [_P, _I64, _I, _P, _SZ, _P]),
     "moe_ffn_prefill_stack": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _SZ, _P]),
 }
 
@@ -878,6 +886,161 @@ def moe_w4_matvec(w: MoeW4Weights, x, expStart, ws, y=None, stream=None):
         yp, ys = _rows_arg(y, "y", x.dtype, (n, w.R), dev)
     _on(dev, stream, "moe_w4_matvec", w.handle, xp, xs, DTYPES[x.dtype], sp, n, yp, ys, *_ws(ws, dev))
     return y
+
+
+# ------------------------------- norms with gradients, 16-bit products ---
+def moe_norm_workspace_size(N, D) -> int:
+    n = int(lib().moe_norm_workspace_size(N, D))
+    if n == 0:
+        raise MoeError(-2, "moe_norm_workspace_size")
+    return n
+
+
+def new_norm_workspace(N, D, device="cuda", stream=None) -> torch.Tensor:
+    """A workspace for the norms' gradients of that shape, or fewer rows."""
+    ws = _new(moe_norm_workspace_size(N, D), torch.uint8, device, stream)
+    _on(ws.get_device(), stream, "moe_workspace_init", ws.data_ptr(), ws.numel())
+    return ws
+
+
+def moe_layernorm(x, gamma, beta, eps, y=None, stream=None):
+    """y = (x - mean) / sqrt(variance + eps) * gamma (+ beta) along the rows of x [N, D] (float32, float16 or bfloat16,
+    strided by rows); gamma, beta [D] float32, beta may be None."""
+    xp, xs = _rows_arg(x, "x")
+    (N, D), dev = x.shape, x.get_device()
+    if y is None:
+        y = _new((N, D), x.dtype, x.device, stream)
+        yp, ys = y.data_ptr(), D
+    else:
+        yp, ys = _rows_arg(y, "y", x.dtype, (N, D), dev)
+    _on(dev, stream, "moe_layernorm", xp, xs, DTYPES[x.dtype], _arg(gamma, torch.float32, (D,), dev, "gamma"),
+        None if beta is None else _arg(beta, torch.float32, (D,), dev, "beta"), eps, N, D, yp, ys)
+    return y
+
+
+def _norm_grad(name, d_y, x, gamma, eps, ws, d_x, beta, stream):
+    xp, xs = _rows_arg(x, "x")
+    (N, D), dev = x.shape, x.get_device()
+    gp, gs = _rows_arg(d_y, "d_y", x.dtype, (N, D), dev)
+    if d_x is None:
+        d_x = _new((N, D), x.dtype, x.device, stream)
+        dp, ds = d_x.data_ptr(), D
+    else:
+        dp, ds = _rows_arg(d_x, "d_x", x.dtype, (N, D), dev)
+    d_gamma = _new(D, torch.float32, x.device, stream)
+    out = [d_gamma.data_ptr()]
+    d_beta = None
+    if name == "moe_layernorm_grad":
+        d_beta = _new(D, torch.float32, x.device, stream) if beta else None
+        out.append(None if d_beta is None else d_beta.data_ptr())
+    _on(dev, stream, name, gp, gs, xp, xs, DTYPES[x.dtype], _arg(gamma, torch.float32, (D,), dev, "gamma"), eps, N, D, dp,
+        ds, *out, *_ws(ws, dev))
+    return d_x, d_gamma, d_beta
+
+
+def moe_layernorm_grad(d_y, x, gamma, eps, ws, d_x=None, beta=True, stream=None):
+    """Gradients of moe_layernorm: -> (d_x like x, d_gamma [D], d_beta [D] or None where `beta` is false), the last two
+    float32.  d_y may be one row for all (stride 0), as of a sum."""
+    return _norm_grad("moe_layernorm_grad", d_y, x, gamma, eps, ws, d_x, beta, stream)
+
+
+def moe_rmsnorm_grad(d_y, x, gamma, eps, ws, d_x=None, stream=None):
+    """Gradients of moe_rmsnorm, for rows of any element type: -> (d_x, d_gamma)."""
+    return _norm_grad("moe_rmsnorm_grad", d_y, x, gamma, eps, ws, d_x, False, stream)[:2]
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # MOE_ACT_*
+
+
+def moe_matmul(x, w, ws, expStart=None, w_up=None, bias=None, bias_up=None, act="none", residual=None, y=None,
+               stream=None):
+    """y [rows, R] = act(x w^T + bias) (* (x w_up^T + bias_up)) (+ residual) for float16 or bfloat16 rows x [rows, K].
+    w, w_up [E, R, K] (or [R, K]: one matrix), bias, bias_up [E, R] (or [R]) float32; expStart [E+1] int32 as of
+    moe_sort_tokens, or None for a single matrix.  Rows from expStart[E] on are left as they were (uninitialised when
+    `y` is not given).  residual may be y."""
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    if w.dim() == 2:
+        w, w_up, bias, bias_up = (None if t is None else t.unsqueeze(0) for t in (w, w_up, bias, bias_up))
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x must be float16 or bfloat16, got {x.dtype}")
+    if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
+        raise ValueError(f"x must be [rows, K], w [E, R, K]; got {tuple(x.shape)}, {tuple(w.shape)}")
+    dtype = x.dtype
+    xp, xs = _rows_arg(x, "x")
+    n, dev, (E, R, K) = x.shape[0], x.get_device(), w.shape
+    wp = _arg(w, dtype, w.shape, dev, "w")
+    up = None if w_up is None else _arg(w_up, dtype, w.shape, dev, "w_up")
+    bp = None if bias is None else _arg(bias, torch.float32, (E, R), dev, "bias")
+    bu = None if bias_up is None else _arg(bias_up, torch.float32, (E, R), dev, "bias_up")
+    sp = None if expStart is None else _arg(expStart, torch.int32, (E + 1,), dev, "expStart")
+    rp, rs = (None, 0) if residual is None else _rows_arg(residual, "residual", dtype, (n, R), dev)
+    if y is None:
+        y = _new((n, R), dtype, x.device, stream)
+        yp, ys = y.data_ptr(), R
+    else:
+        yp, ys = _rows_arg(y, "y", dtype, (n, R), dev)
+    _on(dev, stream, "moe_matmul", xp, xs, DTYPES[dtype], wp, up, bp, bu, ACTS[act], rp, rs, sp, E, n, R, K, yp, ys,
+        *_ws(ws, dev))
+    return y
+
+
+def moe_decode_workspace_size(N, D, E, F, top_k, Fs=0) -> int:
+    n = int(lib().moe_decode_workspace_size(N, D, E, F, top_k, Fs))
+    if n == 0:
+        raise MoeError(-2, "moe_decode_workspace_size")
+    return n
+
+
+def new_decode_workspace(N, D, E, F, top_k, Fs=0, device="cuda", stream=None) -> torch.Tensor:
+    """A workspace for moe_ffn_decode of that shape, or fewer tokens."""
+    ws = _new(moe_decode_workspace_size(N, D, E, F, top_k, Fs), torch.uint8, device, stream)
+    _on(ws.get_device(), stream, "moe_workspace_init", ws.data_ptr(), ws.numel())
+    return ws
+
+
+def moe_ffn_decode(x, routerW, gate, up, down, top_k, norm_topk_prob, ws, shared=None, shexp_gate=None, residual=None,
+                   out=None, stream=None):
+    """The whole routed-experts layer of at most 32 float16 or bfloat16 rows x [N, D] in one kernel: router (routerW
+    [E, D] float32), top-k, experts gate, up [E, F, D] and down [E, D, F] of x's type, their weighted sum.  shared: a
+    tuple (gate, up [Fs, D], down [D, Fs]) or None, counted by sigmoid(shexp_gate . x) (once where shexp_gate [D] is
+    None); residual is added last and may be out."""
+    dtype = x.dtype
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x must be float16 or bfloat16, got {dtype}")
+    if x.dim() != 2 or gate.dim() != 3:
+        raise ValueError(f"x must be [N, D], gate [E, F, D]; got {tuple(x.shape)}, {tuple(gate.shape)}")
+    xp, xs = _rows_arg(x, "x")
+    (N, D), (E, F, _), dev = x.shape, gate.shape, x.get_device()
+    sh, Fs = (None, None, None), 0
+    if shared is not None:
+        Fs = shared[0].shape[0]
+        sh = (_arg(shared[0], dtype, (Fs, D), dev, "shared gate"), _arg(shared[1], dtype, (Fs, D), dev, "shared up"),
+              _arg(shared[2], dtype, (D, Fs), dev, "shared down"))
+    rp, rs = (None, 0) if residual is None else _rows_arg(residual, "residual", dtype, (N, D), dev)
+    if out is None:
+        out = _new((N, D), dtype, x.device, stream)
+        op, os_ = out.data_ptr(), D
+    else:
+        op, os_ = _rows_arg(out, "out", dtype, (N, D), dev)
+    _on(dev, stream, "moe_ffn_decode", xp, xs, DTYPES[dtype], _arg(routerW, torch.float32, (E, D), dev, "routerW"),
+        None if shexp_gate is None else _arg(shexp_gate, torch.float32, (D,), dev, "shexp_gate"),
+        _arg(gate, dtype, (E, F, D), dev, "gate"), _arg(up, dtype, (E, F, D), dev, "up"),
+        _arg(down, dtype, (E, D, F), dev, "down"), *sh, rp, rs, N, D, E, F, Fs, top_k, 1 if norm_topk_prob else 0, op, os_,
+        *_ws(ws, dev))
+    return out
+
+
+def moe_debug_decode_barrier_timeout(x, routerW, gate, up, down, top_k, out, limit_ms, ws, stream=None):
+    """moe_ffn_decode with a first grid barrier that cannot complete (bounded by limit_ms); the outcome is read with
+    moe_workspace_status."""
+    xp, xs = _rows_arg(x, "x")
+    (N, D), (E, F, _), dev = x.shape, gate.shape, x.get_device()
+    op, os_ = _rows_arg(out, "out", x.dtype, (N, D), dev)
+    _on(dev, stream, "moe_debug_decode_barrier_timeout", xp, xs, DTYPES[x.dtype],
+        _arg(routerW, torch.float32, (E, D), dev, "routerW"), _arg(gate, x.dtype, (E, F, D), dev, "gate"),
+        _arg(up, x.dtype, (E, F, D), dev, "up"), _arg(down, x.dtype, (E, D, F), dev, "down"), N, D, E, F, top_k, op, os_,
+        int(limit_ms), *_ws(ws, dev))
 
 
 # ------------------------------------------------------------------ layer ---

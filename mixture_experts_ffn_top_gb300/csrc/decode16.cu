@@ -21,17 +21,12 @@
 #include <algorithm>
 
 #include "stream16.cuh"
-#include "topk_token.cuh"
 
 namespace moe {
 
 namespace {
 
 using namespace s16;
-
-constexpr int KC = 1024;                     // columns of a stage at most
-constexpr int H_CHUNKS = KC / (CONSUMERS * 32);  // 32-wide chunks a warp takes of a stage
-constexpr size_t X_SMEM = 48 * 1024;         // activations are staged in shared memory up to this size
 
 struct DecodeArgs {
     const void *x;
@@ -44,9 +39,10 @@ struct DecodeArgs {
     int N, D, E, F, Fs, top_k, norm;
     float *logits;    // [N][E + 1]
     unsigned *amax;   // [32] largest |h| of a token (fp16)
-    float *h;         // [entries][hs]
+    void *h;          // [entries][hs]: fp32 (fp16 weights), or per 8 values 8 rounded and 8 rests (bf16)
     int hs;
-    unsigned *status, *bar_count, *bar_gen;
+    unsigned *status;
+    unsigned long long *arrived;
     unsigned long long barrier_ns;
     int extra_arrivals;  // failure-detection check: arrivals the first barrier waits for beyond the grid (0 normally)
     int kc, pitch, stages, x_pitch;  // x_pitch 0: the activations stay in global memory
@@ -56,14 +52,15 @@ struct DecodeArgs {
 // Small arrays of a CTA, behind one another from `p` on.
 struct Lists {
     unsigned *mask;  // [E] tokens that chose an expert
-    int *pos;        // [E] its place in the list
+    int *pos;        // [E] its first entry
     int *expert;     // [touched + 1] the touched experts, then E: the shared one
     int *first;      // [touched + 1] their first entry
     int *tok;        // [entries] token
     float *w;        // [entries] weight
     int *idx;        // [N][k] the routing
     float *topw;     // [N][k]
-    __device__ Lists(char *p, int E, int N, int k, bool) {
+    short *at;       // [touched + 1][8] the entry of each of up to 8 tokens, or -1
+    __device__ Lists(char *p, int E, int N, int k) {
         const int touched = min(E, N * k) + 1, entries = N * k + N;
         mask = reinterpret_cast<unsigned *>(p);
         pos = reinterpret_cast<int *>(mask + E);
@@ -73,58 +70,113 @@ struct Lists {
         w = reinterpret_cast<float *>(tok + entries);
         idx = reinterpret_cast<int *>(w + entries);
         topw = reinterpret_cast<float *>(idx + N * k);
+        at = reinterpret_cast<short *>(topw + N * k);
     }
 };
 size_t list_bytes(int E, int N, int k) {
-    return ((size_t)2 * E + 2 * (std::min(E, N * k) + 1) + 2 * (N * k + N) + 2 * N * k) * 4;
+    const size_t touched = std::min(E, N * k) + 1;
+    return (2 * E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (N <= 8 ? touched * 16 : 0);
 }
 
-// Grid barrier (a cooperative launch) of the first `threads` threads of every CTA, which share named barrier 1: an
-// arrival counter and a generation word, both zero between calls.  False when the limit ran out.
-__device__ bool grid_barrier(unsigned *count, unsigned *gen, unsigned arrivals, unsigned *status,
+// Grid barrier of the consumer warps (a cooperative launch).  Arrivals are counted through, never reset: a call makes
+// two for each CTA, so the count is a multiple of that before every call.  False when the limit ran out.
+__device__ bool grid_barrier(unsigned long long *arrived, unsigned long long target, unsigned *status,
                              unsigned long long limit_ns, int *ok_s) {
     consumer_sync();
     if (threadIdx.x == 0) {
-        *ok_s = 1;
-        const unsigned g0 = *reinterpret_cast<volatile unsigned *>(gen);
-        __threadfence();
-        if (atomicAdd(count, 1u) == arrivals - 1) {
-            *reinterpret_cast<volatile unsigned *>(count) = 0;
-            __threadfence();
-            atomicAdd(gen, 1u);
-        } else {
+        unsigned long long n;  // releases what the CTA's threads wrote before their barrier above
+        asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(n) : "l"(arrived) : "memory");
+        ++n;
+        int ok = 1;
+        if (n < target) {
             const unsigned long long t0 = tc::globaltimer();
-            while (*reinterpret_cast<volatile unsigned *>(gen) == g0)
-                if (tc::globaltimer() - t0 > limit_ns) {
+            for (unsigned it = 1;; ++it) {
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(n) : "l"(arrived) : "memory");
+                if (n >= target) break;
+                if ((it & 31) == 0 && tc::globaltimer() - t0 > limit_ns) {
                     atomicOr(status, MOE_DEV_TIMEOUT);
-                    *ok_s = 0;
+                    ok = 0;
                     break;
                 }
+            }
         }
-        __threadfence();
+        *ok_s = ok;
     }
     consumer_sync();
     return *ok_s != 0;
 }
 
-// 8 values times `scale` as 16-bit values and the 16-bit values of what those leave (nothing of an infinity).
+// A float's place in the order of floats (no NaN; both zeros alike), and back.
+__device__ __forceinline__ unsigned order_of(float v) {
+    const unsigned u = __float_as_uint(v + 0.0f);
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(unsigned o) { return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o); }
+
+// One token by one warp: softmax over all E logits, top-k by logit (ties to the lower expert), the selected
+// probabilities (over their sum where norm).  idx, w [k] and the experts' masks in shared memory.  A NaN or infinite
+// logit leaves the choice among the others and makes the weights NaN.
+template <int EPL>
+__device__ __forceinline__ void route(const float *logits, int E, int k, int norm, int t, int lane, int *idx, float *w,
+                                      unsigned *mask) {
+    unsigned key[EPL];
+    float l[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = lane + 32 * i < E ? __ldcg(logits + lane + 32 * i) : 0.0f;
+    bool bad = false, some = false;
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        key[i] = 0;
+        if (lane + 32 * i < E) {
+            const bool fine = fabsf(l[i]) <= 3e38f;
+            some |= fine;
+            bad |= !fine && !(l[i] < 0.0f);
+            if (!fine) l[i] = l[i] > 0.0f ? 3e38f : -3e38f;
+            key[i] = order_of(l[i]);
+        }
+        top = max(top, key[i]);
+    }
+    const float m = value_of(__reduce_max_sync(0xffffffffu, top));
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) z += lane + 32 * i < E ? expf(l[i] - m) : 0.0f;
+    z = warp_sum(z);
+    bad = __any_sync(0xffffffffu, bad) || !__any_sync(0xffffffffu, some);
+    float sum = 0.0f, mine = 0.0f;
+    for (int s = 0; s < k; ++s) {
+        unsigned best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        const unsigned got = __reduce_max_sync(0xffffffffu, best);
+        const unsigned e = __reduce_min_sync(0xffffffffu, best == got ? (unsigned)(lane + 32 * at) : 0xffffffffu);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if ((unsigned)(lane + 32 * i) == e) key[i] = 0;
+        const float p = __fdiv_rn(expf(value_of(got) - m), z);
+        sum += p;
+        if (lane == s) mine = p;
+        if (lane == 0) {
+            idx[s] = (int)e;
+            atomicOr(mask + e, 1u << t);
+        }
+    }
+    if (lane < k) w[lane] = bad ? __uint_as_float(0x7fffffffu) : norm ? __fdiv_rn(mine, sum) : mine;
+}
+
+// 8 values times `scale` as 16-bit values, and as 16-bit values what those leave.
 template <typename T>
-__device__ __forceinline__ void split8(const float4 &a, const float4 &b, float scale, uint4 &hi, uint4 &lo) {
-    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void split8(const uint4 &a, const uint4 &b, float scale, uint4 &hi, uint4 &lo) {
+    const uint32_t f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float v[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) v[j] = std::is_same_v<T, __half> ? f[2 * i + j] * scale : f[2 * i + j];
+        const float v[2] = {__uint_as_float(f[2 * i]) * scale, __uint_as_float(f[2 * i + 1]) * scale};
         Pack<T, 2> p, q;
         p.set(v);
-        float r[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            r[j] = v[j] - p.get(j);
-            r[j] = fabsf(r[j]) <= fabsf(v[j]) ? r[j] : 0.0f;
-        }
+        const float r[2] = {v[0] - p.get(0), v[1] - p.get(1)};
         q.set(r);
         h[i] = p.w[0];
         l[i] = q.w[0];
@@ -141,67 +193,83 @@ __device__ __forceinline__ float h_scale(unsigned amax, bool inverse) {
     return __uint_as_float((unsigned)(127 + (inverse ? -p : p)) << 23);
 }
 
+// NTM: tiles of 8 tokens, rounded up to 1, 2 or 4.
 template <typename T, int NTM>
 __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a) {
+    constexpr bool F16 = std::is_same_v<T, __half>;
     extern __shared__ __align__(1024) char smem[];
-    __shared__ __align__(8) unsigned long long bars[2 * MAX_STAGES + 1];
+    __shared__ __align__(8) unsigned long long bars[GROUPS * 2 * MAX_STAGES + 1];
     __shared__ int abort_flag, ok_s, touched_s;
     __shared__ unsigned amax_s[MAX_ROWS];
     __shared__ float scale_s[MAX_ROWS], gate_s[MAX_ROWS];
-    __shared__ float part[CONSUMERS][8];
+    __shared__ float part[2][CONSUMERS][16];
+    __shared__ int2 group_s[MAX_E / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int N = a.N, D = a.D, E = a.E, k = a.top_k, G = gridDim.x, bid = blockIdx.x;
     const bool consumer = warp < CONSUMERS;
     const T *x = static_cast<const T *>(a.x);
-    Lists ls(smem + a.list_at, E, N, k, true);
-    const uint32_t bar = tc::smem_u32(bars), xbar = bar + 2 * MAX_STAGES * 8;
+    Lists ls(smem + a.list_at, E, N, k);
+    const uint32_t bar = tc::smem_u32(bars), xbar = bar + GROUPS * 2 * MAX_STAGES * 8;
+    unsigned long long arrivals = 0;  // of the calls before this one
     if (tid == 0) {
         abort_flag = 0;
+        ok_s = 1;
         tc::mbar_init(xbar, 1);
-        init_ring(bar, a.stages);
+        init_rings(bar, a.stages);
+        arrivals = *reinterpret_cast<volatile unsigned long long *>(a.arrived);
+        arrivals -= arrivals % (2u * (unsigned)G);
     }
     if (bid == 0 && tid < MAX_ROWS) a.amax[tid] = 0;
     if (tid < MAX_ROWS) amax_s[tid] = 0;
     for (int e = tid; e < E; e += THREADS) ls.mask[e] = 0;
     __syncthreads();
 
-    // ---- router: an expert's row (or the shared gate's) at a time
+    // ---- router: two experts' rows (or the shared gate's) and eight tokens at a time
     if (consumer) {
         const int rows = E + (a.shexp_gate != nullptr);
-        for (int e = bid; e < rows; e += G) {
-            const float *w = e < E ? a.routerW + (int64_t)e * D : a.shexp_gate;
+        int buf = 0;
+        for (int e = bid; e < rows; e += 2 * G) {
+            const int e2 = min(e + G, rows - 1);
+            const float *w0 = e < E ? a.routerW + (int64_t)e * D : a.shexp_gate;
+            const float *w1 = e2 < E ? a.routerW + (int64_t)e2 * D : a.shexp_gate;
             for (int t0 = 0; t0 < N; t0 += 8) {
-                float acc[8] = {};
-                for (int c = tid * 8; c < D; c += CONSUMERS * 256) {
-                    const float4 w0 = *reinterpret_cast<const float4 *>(w + c), w1 = *reinterpret_cast<const float4 *>(w + c + 4);
-                    const float wf[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                float acc[16] = {};
+                for (int c = tid * 4; c < D; c += CONSUMERS * 128) {
+                    const float4 u = *reinterpret_cast<const float4 *>(w0 + c), v = *reinterpret_cast<const float4 *>(w1 + c);
+                    Pack<T, 4> p[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (t0 + j < N) {
-                            Pack<T, 8> p;
-                            p.load(x + (t0 + j) * a.x_stride + c);
+                    for (int j = 0; j < 8; ++j) p[j].load(x + min(t0 + j, N - 1) * a.x_stride + c);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) acc[j] = fmaf(wf[i], p.get(i), acc[j]);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        acc[j] = fmaf(u.w, p[j].get(3), fmaf(u.z, p[j].get(2), fmaf(u.y, p[j].get(1), fmaf(u.x, p[j].get(0), acc[j]))));
+                        acc[8 + j] = fmaf(v.w, p[j].get(3), fmaf(v.z, p[j].get(2), fmaf(v.y, p[j].get(1), fmaf(v.x, p[j].get(0), acc[8 + j]))));
+                    }
                 }
+                // 16 sums over the warp: at each step a lane keeps half of its values and sends the other half
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (t0 + j < N) acc[j] = warp_sum(acc[j]);
-                if (lane == 0)
+                for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) part[warp][j] = acc[j];
+                    for (int j = 0; j < n; ++j) {
+                        const bool up = lane & o;
+                        const float send = up ? acc[j] : acc[j + n], keep = up ? acc[j + n] : acc[j];
+                        acc[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
+                if (!(lane & 1)) part[buf][warp][lane >> 1] = acc[0];
                 consumer_sync();
-                if (tid < 8 && t0 + tid < N) {
-                    float v = part[0][tid];
-                    for (int i = 1; i < CONSUMERS; ++i) v += part[i][tid];
-                    a.logits[(t0 + tid) * (E + 1) + e] = v;
+                const int t = t0 + (tid & 7), row = tid & 8 ? e + G : e;
+                if (tid < 16 && t < N && row < rows) {
+                    float v = part[buf][0][tid];
+#pragma unroll
+                    for (int i = 1; i < CONSUMERS; ++i) v += part[buf][i][tid];
+                    a.logits[t * (E + 1) + row] = v;
                 }
-                consumer_sync();
+                buf ^= 1;
             }
         }
-        grid_barrier(a.bar_count, a.bar_gen, G + a.extra_arrivals, a.status, a.barrier_ns, &ok_s);
-    } else if (a.x_pitch) {
-        // the producer has no weights to ask for yet: it brings the activations in
+        grid_barrier(a.arrived, arrivals + G + a.extra_arrivals, a.status, a.barrier_ns, &ok_s);
+    } else if (a.x_pitch && warp == CONSUMERS) {
+        // there are no weights to ask for yet: a producer brings the activations in
         if (lane == 0) tc::mbar_expect_tx(xbar, (uint32_t)(N * D * 2));
         __syncwarp();
         if (lane < N) tc::bulk_load(tc::smem_u32(smem + a.x_at) + lane * a.x_pitch, x + lane * a.x_stride, D * 2, xbar);
@@ -211,62 +279,56 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     if (!ok_s) return;  // the barrier's limit ran out
 
     // ---- every CTA routes all tokens
-    for (int t = warp; t < N; t += CONSUMERS + 1) {
-        bool bad = false, some = false;
-        auto logit = [&](int e) {  // a NaN or an infinity leaves the choice among the others and makes the weights NaN
-            const float v = __ldcg(a.logits + t * (E + 1) + e);
-            if (fabsf(v) <= 3e38f) {
-                some = true;
-                return v;
-            }
-            bad |= !(v < 0.0f);
-            return v > 0.0f ? 3e38f : -3e38f;
-        };
-        auto sg = [&]() { return __ldcg(a.logits + t * (E + 1) + E); };
-        float *scale = a.shexp_gate != nullptr ? gate_s : nullptr;
+    for (int t = warp; t < N; t += CONSUMERS + GROUPS) {
+        const float *l = a.logits + t * (E + 1);
         if (E <= 64)
-            route_token<2>(logit, sg, E, k, a.norm, t, lane, ls.idx, ls.topw, scale, nullptr);
+            route<2>(l, E, k, a.norm, t, lane, ls.idx + t * k, ls.topw + t * k, ls.mask);
+        else if (E <= 128)
+            route<4>(l, E, k, a.norm, t, lane, ls.idx + t * k, ls.topw + t * k, ls.mask);
         else if (E <= 256)
-            route_token<8>(logit, sg, E, k, a.norm, t, lane, ls.idx, ls.topw, scale, nullptr);
+            route<8>(l, E, k, a.norm, t, lane, ls.idx + t * k, ls.topw + t * k, ls.mask);
         else
-            route_token<32>(logit, sg, E, k, a.norm, t, lane, ls.idx, ls.topw, scale, nullptr);
-        __syncwarp();
-        if ((__any_sync(0xffffffffu, bad) || !__any_sync(0xffffffffu, some)) && lane < k) ls.topw[t * k + lane] = __uint_as_float(0x7fffffffu);
-        if (lane == 0 && a.shexp_gate == nullptr) gate_s[t] = 1.0f;
+            route<32>(l, E, k, a.norm, t, lane, ls.idx + t * k, ls.topw + t * k, ls.mask);
+        if (lane == 0) gate_s[t] = a.shexp_gate != nullptr ? __fdiv_rn(1.0f, 1.0f + expf(-__ldcg(l + E))) : 1.0f;
     }
     __syncthreads();
-    for (int i = tid; i < N * k; i += THREADS) atomicOr(&ls.mask[ls.idx[i]], 1u << (i / k));
-    __syncthreads();
-    if (warp == 0) {
-        int n = 0, at = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const unsigned m = e0 + lane < E ? ls.mask[e0 + lane] : 0;
-            const unsigned there = __ballot_sync(0xffffffffu, m != 0);
-            int c = __popc(m), before = c;
+    // ---- the touched experts and their entries, by expert, then token: 32 experts a warp, then the warps' totals
+    const int groups = (E + 31) / 32;
+    for (int gr = warp; gr < groups; gr += CONSUMERS + GROUPS) {
+        const int e = gr * 32 + lane;
+        const unsigned m = e < E ? ls.mask[e] : 0;
+        const unsigned there = __ballot_sync(0xffffffffu, m != 0);
+        const int c = __popc(m);
+        int before = c;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += v;
-            }
-            if (m != 0) {
-                const int p = n + __popc(there & ((1u << lane) - 1));
-                ls.expert[p] = e0 + lane;
-                ls.first[p] = at + before - c;
-                ls.pos[e0 + lane] = p;
-            }
-            n += __popc(there);
-            at += __shfl_sync(0xffffffffu, before, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
         }
-        if (lane == 0) {
-            ls.expert[n] = E;
-            ls.first[n] = N * k;
-            touched_s = n;
+        if (lane == 31) group_s[gr] = make_int2(__popc(there), before);
+        if (e < E) ls.pos[e] = __popc(there & ((1u << lane) - 1)) << 16 | (before - c);  // within the group
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += THREADS) {
+        int n = ls.pos[e] >> 16, at = ls.pos[e] & 0xffff;
+        for (int gr = 0; gr < e / 32; ++gr) n += group_s[gr].x, at += group_s[gr].y;
+        if (ls.mask[e] != 0) {
+            ls.expert[n] = e;
+            ls.first[n] = at;
         }
+        ls.pos[e] = at;
+    }
+    if (tid == 0) {
+        int n = 0;
+        for (int gr = 0; gr < groups; ++gr) n += group_s[gr].x;
+        ls.expert[n] = E;
+        ls.first[n] = N * k;
+        touched_s = n;
     }
     __syncthreads();
     for (int i = tid; i < N * k; i += THREADS) {
         const int t = i / k, e = ls.idx[i];
-        const int at = ls.first[ls.pos[e]] + __popc(ls.mask[e] & ((1u << t) - 1));
+        const int at = ls.pos[e] + __popc(ls.mask[e] & ((1u << t) - 1));
         ls.tok[at] = t;
         ls.w[at] = ls.topw[i];
     }
@@ -274,22 +336,28 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         ls.tok[N * k + t] = t;
         ls.w[N * k + t] = gate_s[t];
     }
+    if (NTM == 1)
+        for (int i = tid; i < (touched_s + 1) * 8; i += THREADS) {
+            const int l = i >> 3, t = i & 7;
+            const unsigned m = l == touched_s ? (1u << N) - 1 : ls.mask[ls.expert[l]];
+            ls.at[i] = (m >> t) & 1 ? (short)(ls.first[l] + __popc(m & ((1u << t) - 1))) : (short)-1;
+        }
     __syncthreads();
 
     // ---- the CTA's share
     const int touched = touched_s, listed = touched + (a.Fs > 0);
-    const unsigned all = N == 32 ? 0xffffffffu : (1u << N) - 1;
-    const int upe = a.F / 8;                            // tiles of 8 pairs an expert
+    const int upe = a.F / 8;  // tiles of 8 pairs an expert
     const int64_t units = (int64_t)touched * upe + a.Fs / 8;
     const int u0 = (int)(units * bid / G), u1 = (int)(units * (bid + 1) / G);
     const int row0 = (int)((int64_t)D * bid / G), row1 = (int)((int64_t)D * (bid + 1) / G);
     const int row_tiles = (row1 - row0 + 15) / 16;
-    Ring ring{smem, bar, a.stages, a.pitch, 0, 0, &abort_flag, a.status};
+    const int group = consumer ? warp / GROUP_WARPS : warp - CONSUMERS;
+    Ring ring(smem, bar, group, a.stages, a.pitch, &abort_flag, a.status);
 
-    if (!consumer) {
-        int issued = 0;
+    if (!consumer) {  // the group's producer
+        int issued = 0, turn = 0;
         bool ok = true;
-        for (int u = u0; u < u1 && ok; ++u) {
+        for (int u = u0 + group; u < u1 && ok; u += GROUPS) {
             const int i = min(u / upe, touched), e = ls.expert[i], r = (u - i * upe) * 8 + (lane & 7);
             const T *m = static_cast<const T *>(e == E ? (lane & 8 ? a.sh_up : a.sh_gate) : (lane & 8 ? a.up : a.gate));
             const T *src = m + ((int64_t)(e == E ? 0 : e) * a.F + r) * D;
@@ -304,13 +372,14 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                 const int e = ls.expert[i], K = e == E ? a.Fs : a.F;
                 const T *src = static_cast<const T *>(e == E ? a.sh_down : a.down) +
                                ((int64_t)(e == E ? 0 : e) * D + r0 + min(lane, r1 - r0 - 1)) * K;
-                for (int k0 = 0; k0 < K && ok; k0 += a.kc) {
+                for (int k0 = 0; k0 < K && ok; k0 += a.kc, turn = turn + 1 == GROUPS ? 0 : turn + 1) {
+                    if (turn != group) continue;
                     ok = ring.produce(lane, lane < r1 - r0, r1 - r0, src + k0, (uint32_t)min(a.kc, K - k0) * 2);
                     issued += ok;
                 }
             }
         }
-        if (lane == 0 && *reinterpret_cast<volatile int *>(&abort_flag)) drain(bar, a.stages, issued);
+        if (lane == 0 && *reinterpret_cast<volatile int *>(&abort_flag)) drain(ring.bar, a.stages, issued);
         return;
     }
 
@@ -319,116 +388,155 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     const T *xb = a.x_pitch ? reinterpret_cast<const T *>(smem + a.x_at) : x;
     const int64_t xs = a.x_pitch ? a.x_pitch / 2 : a.x_stride;
     float4 *red = reinterpret_cast<float4 *>(smem + a.red_at);
-    int buf = 0;
-    auto sums = [&]() { return red + buf * CONSUMERS * NTM * 32; };
-    for (int u = u0; u < u1; ++u) {
-        const int i = min(u / upe, touched), r = (u - i * upe) * 8, first = ls.first[i];
-        const int n = i == touched ? N : __popc(ls.mask[ls.expert[i]]), nt = (n + 7) / 8;
-        const T *xp[NTM];
-#pragma unroll
-        for (int j = 0; j < NTM; ++j) xp[j] = xb + ls.tok[first + min(j * 8 + g, n - 1)] * xs + t4 * 8;
-        float acc[NTM][4] = {};
-        for (int k0 = 0; k0 < D; k0 += a.kc) {
-            ring.wait_full();
-            stage_products_nt<T, NTM>(ring, min(a.kc, D - k0), k0, nt, xp, acc, warp, lane);
-            ring.release(lane);
-            ring.next();
+    auto info = [&](int64_t u) {
+        const int i = min((int)u / upe, touched);
+        return make_int2(ls.first[i], i == touched ? N : ls.first[i + 1] - ls.first[i]);
+    };
+    auto at = [&](int entry) { return xb + ls.tok[entry] * xs; };
+    auto done = [&](int64_t u, const int2 &in, const float4 *s, int nt, int thread) {
+        const int r = ((int)u - min((int)u / upe, touched) * upe) * 8;
+        // a pair of threads a value: one adds up gate, the other up
+        for (int j = thread; j < nt * 128; j += GROUP_WARPS * 32) {
+            const int is_up = j & 1, row = (j >> 1) & 7, c = j >> 4, l = row * 4 + ((c & 7) >> 1);
+            const float v = sum_of(s, nt, c >> 3, l, 2 * is_up + (c & 1));
+            const float up = __shfl_xor_sync(0xffffffffu, v, 1);
+            if (c >= in.y || is_up) continue;
+            const float h = __fdiv_rn(v, 1.0f + expf(-v)) * up * ls.w[in.x + c];
+            const int64_t to = (int64_t)(in.x + c) * a.hs + r;
+            if (F16) {
+                static_cast<float *>(a.h)[to + row] = h;
+                atomicMax(&amax_s[ls.tok[in.x + c]], __float_as_uint(h) & 0x7fffffffu);
+            } else {
+                const T hi = elem_of<T>(h);
+                T *p = static_cast<T *>(a.h) + to * 2 + row;
+                p[0] = hi;
+                p[8] = elem_of<T>(h - (float)hi);
+            }
         }
-        share_sums<NTM>(sums(), nt, acc, warp, lane);
-        consumer_sync();
-        for (int j = tid; j < nt * 64; j += CONSUMERS * 32) {
-            const int tile = j >> 6, l = (j & 63) >> 1, odd = j & 1, c = tile * 8 + 2 * (l & 3) + odd;
-            if (c >= n) continue;
-            const float gate = sum_of(sums(), nt, tile, l, odd), up = sum_of(sums(), nt, tile, l, 2 + odd);
-            const float h = __fdiv_rn(gate, 1.0f + expf(-gate)) * up * ls.w[first + c];
-            a.h[(int64_t)(first + c) * a.hs + r + (l >> 2)] = h;
-            if (std::is_same_v<T, __half>) atomicMax(&amax_s[ls.tok[first + c]], __float_as_uint(h) & 0x7fffffffu);
-        }
-        buf ^= 1;  // the next sums go elsewhere, those after them behind the next barrier
-    }
-    if (std::is_same_v<T, __half>) {
+    };
+    stream_units<T, NTM>(ring, u0, u1, D, a.kc, red, warp, lane, info, at, done);
+    if (F16) {
         consumer_sync();
         if (tid < N) atomicMax(a.amax + tid, amax_s[tid]);
     }
-    if (!grid_barrier(a.bar_count, a.bar_gen, G, a.status, a.barrier_ns, &ok_s)) *reinterpret_cast<volatile int *>(&abort_flag) = 1;
-    if (std::is_same_v<T, __half>) {
+    if (!grid_barrier(a.arrived, arrivals + 2 * G, a.status, a.barrier_ns, &ok_s)) *reinterpret_cast<volatile int *>(&abort_flag) = 1;
+    if (F16) {
         if (tid < N) scale_s[tid] = h_scale(__ldcg(a.amax + tid), false);
         consumer_sync();
     }
 
-    // ---- down
-    const int nt = (N + 7) / 8;
+    // ---- down.  Up to 8 tokens: a token's column is its own throughout, the accumulators run on over the experts.
+    // More: an expert's entries are its columns, and its sums are added to the warp's rows x tokens in shared memory
+    // (most experts have a handful of entries: one tile of columns instead of four that are all but empty).
+    constexpr bool PACKED = NTM > 1;
+    const int gw = warp % GROUP_WARPS, own_pitch = N + 1;
+    float *own = reinterpret_cast<float *>(red) + warp * 16 * own_pitch;  // PACKED: [16][own_pitch] of the warp
+    int turn = 0;  // the stages go to the groups in turn
     for (int rt = 0; rt < row_tiles; ++rt) {
         const int r0 = row0 + (row1 - row0) * rt / row_tiles, r1 = row0 + (row1 - row0) * (rt + 1) / row_tiles;
-        float acc[NTM][4] = {};
-        for (int i = 0; i < listed; ++i) {
-            const int e = ls.expert[i], K = e == E ? a.Fs : a.F;
-            const unsigned mask = e == E ? all : ls.mask[e];
-            const float *hp[NTM];
-            float scale[NTM];
-            bool on[NTM];
-#pragma unroll
-            for (int j = 0; j < NTM; ++j) {
-                const int t = j * 8 + g;
-                on[j] = (mask >> t) & 1;
-                hp[j] = a.h + (int64_t)(ls.first[i] + __popc(mask & ((1u << t) - 1))) * a.hs + t4 * 8;
-                scale[j] = std::is_same_v<T, __half> && on[j] ? scale_s[t] : 1.0f;
+        if (PACKED) {
+            consumer_sync();  // the sums before these have been read
+            for (int j = lane; j < 16 * own_pitch; j += 32) own[j] = 0.0f;
+            __syncwarp();
+        }
+        // the lane's h of a stage: 8 values in 32 bytes, CHUNKS times; asked for two stages ahead
+        struct Block {
+            uint4 a[CHUNKS], b[CHUNKS];
+            float scale;
+        };
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        auto length = [&](int i) { return i == touched ? a.Fs : a.F; };
+        auto load = [&](int i, int k0, int tile, Block &f) {
+            const int cols = min(a.kc, length(i) - k0);
+            int entry = -1;
+            if (PACKED) {
+                const int j = tile * 8 + g, n = i == touched ? N : ls.first[i + 1] - ls.first[i];
+                if (j < n) entry = ls.first[i] + j;
+            } else {
+                entry = ls.at[i * 8 + g];
             }
-            for (int k0 = 0; k0 < K; k0 += a.kc) {
-                const int cols = min(a.kc, K - k0);
-                const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float4 f[NTM == 1 ? H_CHUNKS : 1][2];
-                if (NTM == 1)  // asked for before the wait
+            f.scale = 1.0f;
+            if (F16 && entry >= 0) f.scale = scale_s[PACKED ? ls.tok[entry] : g];
+            const char *h = static_cast<const char *>(a.h) + ((int64_t)entry * a.hs + k0 + t4 * 8) * 4;
 #pragma unroll
-                    for (int q = 0; q < H_CHUNKS; ++q) {
-                        const int c = (q * CONSUMERS + warp) * 32;
-                        f[NTM == 1 ? q : 0][0] = f[NTM == 1 ? q : 0][1] = zero;
-                        if (on[0] && c + t4 * 8 < cols) {
-                            f[NTM == 1 ? q : 0][0] = __ldcg(reinterpret_cast<const float4 *>(hp[0] + k0 + c));
-                            f[NTM == 1 ? q : 0][1] = __ldcg(reinterpret_cast<const float4 *>(hp[0] + k0 + c + 4));
-                        }
-                    }
-                ring.wait_full();
-                const char *w = ring.stage() + g * ring.pitch + t4 * 16;
-#pragma unroll
-                for (int q = 0; q < H_CHUNKS; ++q) {
-                    const int c = (q * CONSUMERS + warp) * 32;
-                    if (c >= cols) break;
-                    const bool in = c + t4 * 8 < cols;
-                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                    if (in) {
-                        lo = *reinterpret_cast<const uint4 *>(w + c * 2);
-                        hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NTM; ++j) {
-                        if (NTM > 1 && !((mask >> (j * 8)) & 0xffu)) continue;
-                        float4 f0 = zero, f1 = zero;
-                        if (NTM == 1) {
-                            f0 = f[NTM == 1 ? q : 0][0];
-                            f1 = f[NTM == 1 ? q : 0][1];
-                        } else if (on[j] && in) {
-                            f0 = __ldcg(reinterpret_cast<const float4 *>(hp[j] + k0 + c));
-                            f1 = __ldcg(reinterpret_cast<const float4 *>(hp[j] + k0 + c + 4));
-                        }
-                        uint4 bh, bl;
-                        split8<T>(f0, f1, scale[j], bh, bl);
-                        mma_chunk<T>(acc[j], lo, hi, bh);
-                        mma_chunk<T>(acc[j], lo, hi, bl);
-                    }
+            for (int q = 0; q < CHUNKS; ++q) {
+                const int c = (q * GROUP_WARPS + gw) * 32;
+                f.a[q] = f.b[q] = zero;
+                if (entry >= 0 && c + t4 * 8 < cols) {
+                    f.a[q] = __ldcg(reinterpret_cast<const uint4 *>(h + c * 4));
+                    f.b[q] = __ldcg(reinterpret_cast<const uint4 *>(h + c * 4 + 16));
                 }
+            }
+        };
+        auto products = [&](int cols, const Block &f, float (&hi_sum)[4], float (&lo_sum)[4]) {
+            const char *w = ring.stage() + g * ring.pitch + t4 * 16;
+#pragma unroll
+            for (int q = 0; q < CHUNKS; ++q) {
+                const int c = (q * GROUP_WARPS + gw) * 32;
+                if (c >= cols) break;
+                uint4 lo = zero, hi = zero, bh = f.a[q], bl = f.b[q];
+                if (c + t4 * 8 < cols) {
+                    lo = *reinterpret_cast<const uint4 *>(w + c * 2);
+                    hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
+                }
+                if (F16) split8<T>(f.a[q], f.b[q], f.scale, bh, bl);
+                mma_chunk<T>(hi_sum, lo, hi, bh);
+                mma_chunk<T>(lo_sum, lo, hi, bl);
+            }
+        };
+        constexpr int TILES = PACKED ? NTM : 1;
+        float acc[TILES][4] = {}, rest[TILES][4] = {};  // of h rounded, and of the rests
+        for (int i = 0; i < listed; ++i) {
+            const int K = length(i), n = PACKED ? (i == touched ? N : ls.first[i + 1] - ls.first[i]) : 0;
+            for (int k0 = 0; k0 < K; k0 += a.kc, turn = turn + 1 == GROUPS ? 0 : turn + 1) {
+                if (turn != group) continue;
+                const int cols = min(a.kc, K - k0);
+                Block f;
+                load(i, k0, 0, f);
+                ring.wait_full();
+                products(cols, f, acc[0], rest[0]);
+#pragma unroll
+                for (int j = 1; j < TILES; ++j)
+                    if (j * 8 < n) {
+                        load(i, k0, j, f);
+                        products(cols, f, acc[j], rest[j]);
+                    }
                 ring.release(lane);
                 ring.next();
+                if (PACKED) {
+#pragma unroll
+                    for (int j = 0; j < TILES; ++j)
+                        if (j * 8 < n)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int c = j * 8 + 2 * t4 + (q & 1);
+                                if (c < n) own[(g + 8 * (q >> 1)) * own_pitch + ls.tok[ls.first[i] + c]] += acc[j][q] + rest[j][q];
+                                acc[j][q] = rest[j][q] = 0.0f;
+                            }
+                    __syncwarp();
+                }
             }
         }
-        share_sums<NTM>(sums(), nt, acc, warp, lane);
+        if (!PACKED) {
+            const float one[1][4] = {{acc[0][0] + rest[0][0], acc[0][1] + rest[0][1], acc[0][2] + rest[0][2], acc[0][3] + rest[0][3]}};
+            consumer_sync();  // the sums before these have been read
+            share_sums<1>(red, 1, one, warp, lane);
+        }
         consumer_sync();
         if (!*reinterpret_cast<volatile int *>(&abort_flag))
-            for (int j = tid; j < nt * 128; j += CONSUMERS * 32) {
-                const int row = j & 15, tile = j >> 7, c = (j >> 4) & 7, t = tile * 8 + c;
-                if (r0 + row >= r1 || t >= N) continue;
-                float v = sum_of(sums(), nt, tile, (row & 7) * 4 + (c >> 1), (row >> 3) * 2 + (c & 1));
-                if (std::is_same_v<T, __half>) v *= h_scale(__ldcg(a.amax + t), true);
+            for (int j = tid; j < N * 16; j += CONSUMERS * 32) {
+                const int row = j & 15, t = j >> 4;
+                if (r0 + row >= r1) continue;
+                float v;
+                if (PACKED) {
+                    const float *p = reinterpret_cast<const float *>(red) + row * own_pitch + t;
+                    v = p[0];
+#pragma unroll
+                    for (int i = 1; i < CONSUMERS; ++i) v += p[i * 16 * own_pitch];
+                } else {
+                    v = sum_of<CONSUMERS>(red, 1, 0, (row & 7) * 4 + (t >> 1), (row >> 3) * 2 + (t & 1));
+                }
+                if (F16) v *= h_scale(__ldcg(a.amax + t), true);
                 if (a.residual != nullptr) {
                     Pack<T, 1> p;
                     p.load(static_cast<const T *>(a.residual) + t * a.residual_stride + r0 + row);
@@ -436,7 +544,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                 }
                 static_cast<T *>(a.out)[t * a.out_stride + r0 + row] = elem_of<T>(v);
             }
-        buf ^= 1;
     }
 }
 
@@ -485,23 +592,24 @@ int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned lo
     a.norm = c.norm;
     a.logits = ws_ptr<float>(ws, L.logits);
     a.amax = ws_ptr<unsigned>(ws, L.amax);
-    a.h = ws_ptr<float>(ws, L.h);
+    a.h = ws_ptr<void>(ws, L.h);
     a.hs = L.hs;
     a.status = ws_ptr<unsigned>(ws, 0);
-    a.bar_count = ws_ptr<unsigned>(ws, BUCKET_BARRIER_OFFSET);
-    a.bar_gen = ws_ptr<unsigned>(ws, BUCKET_BARRIER_OFFSET + 64);
+    a.arrived = ws_ptr<unsigned long long>(ws, DECODE_ARRIVALS_OFFSET);
     a.barrier_ns = barrier_ns ? barrier_ns : WAIT_NS;
     a.extra_arrivals = extra_arrivals;
     const int ntm = c.N <= 8 ? 1 : c.N <= 16 ? 2 : 4;
     a.kc = std::min(KC, (std::max({c.D, c.F, c.Fs}) + 31) / 32 * 32);
     a.pitch = pitch_of(a.kc);
-    const size_t xb = (size_t)c.N * pitch_of(c.D);
-    a.x_pitch = xb <= X_SMEM ? pitch_of(c.D) : 0;
-    const size_t red = (size_t)2 * CONSUMERS * ntm * 512, lists = list_bytes(c.E, c.N, c.top_k);
-    const size_t fixed = (a.x_pitch ? xb : 0) + red + lists, most = SMEM_LIMIT - 4096;
-    a.stages = (int)std::min<size_t>(MAX_STAGES, (most - fixed) / ((size_t)16 * a.pitch));
+    // the warps' sums, or with more than a tile of tokens each warp's rows x tokens
+    const size_t red = std::max((size_t)CONSUMERS * 512 * ntm, ntm == 1 ? 0 : (size_t)CONSUMERS * 64 * (c.N + 1));
+    const size_t ring = (size_t)GROUPS * 16 * a.pitch, lists = list_bytes(c.E, c.N, c.top_k), most = SMEM_LIMIT - 5120;
+    a.stages = (int)std::min<size_t>(MAX_STAGES, (most - red - lists) / ring);
     if (a.stages < 2) return MOE_ERR_UNSUPPORTED_SHAPE;
-    a.x_at = (int)((size_t)a.stages * 16 * a.pitch);
+    // the activations are staged where there is room beside the rings
+    const size_t xb = (size_t)c.N * pitch_of(c.D);
+    a.x_pitch = a.stages * ring + red + lists + xb <= most ? pitch_of(c.D) : 0;
+    a.x_at = (int)(a.stages * ring);
     a.red_at = a.x_at + (int)(a.x_pitch ? xb : 0);
     a.list_at = a.red_at + (int)red;
     const size_t smem = a.list_at + lists;

@@ -26,9 +26,6 @@ namespace few {
 
 using namespace s16;
 
-constexpr int KC = 1024;              // columns of a stage at most
-constexpr size_t X_SMEM = 48 * 1024;  // rows are staged in shared memory up to this size
-
 struct Args {
     Matmul16Call c;
     unsigned *status;
@@ -41,17 +38,17 @@ struct Args {
 template <typename T, int NTM>
 __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
     extern __shared__ __align__(1024) char smem[];
-    __shared__ __align__(8) unsigned long long bars[2 * MAX_STAGES + 1];
+    __shared__ __align__(8) unsigned long long bars[GROUPS * 2 * MAX_STAGES + 1];
     __shared__ int abort_flag, listed_s, expert_s[MAX_ROWS], first_s[MAX_ROWS + 1];
     const Matmul16Call &c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool pair = c.w_up != nullptr;
     const T *x = static_cast<const T *>(c.x);
-    const uint32_t bar = tc::smem_u32(bars), xbar = bar + 2 * MAX_STAGES * 8;
+    const uint32_t bar = tc::smem_u32(bars), xbar = bar + GROUPS * 2 * MAX_STAGES * 8;
     if (tid == 0) {
         abort_flag = 0;
         tc::mbar_init(xbar, 1);
-        init_ring(bar, a.stages);
+        init_rings(bar, a.stages);
     }
     // the experts that have rows
     if (warp == 0) {
@@ -90,18 +87,19 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
     const int64_t units = (int64_t)listed_s * a.tiles;
     const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
     if (u0 == u1) return;
-    Ring ring{smem, bar, a.stages, a.pitch, 0, 0, &abort_flag, a.status};
+    const int group = warp < CONSUMERS ? warp / GROUP_WARPS : warp - CONSUMERS;
+    Ring ring(smem, bar, group, a.stages, a.pitch, &abort_flag, a.status);
     const int rows_x = first_s[listed_s];
 
-    if (warp == CONSUMERS) {
+    if (warp >= CONSUMERS) {
         int issued = 0;
         bool ok = true;
-        if (a.x_pitch) {
+        if (a.x_pitch && group == 0) {
             if (lane == 0) tc::mbar_expect_tx(xbar, (uint32_t)(rows_x * c.K * 2));
             __syncwarp();
             if (lane < rows_x) tc::bulk_load(tc::smem_u32(smem + a.x_at) + lane * a.x_pitch, x + lane * c.x_stride, c.K * 2, xbar);
         }
-        for (int64_t u = u0; u < u1 && ok; ++u) {
+        for (int64_t u = u0 + group; u < u1 && ok; u += GROUPS) {
             const int i = (int)(u / a.tiles), r = (int)(u - (int64_t)i * a.tiles) * a.tile, n = min(a.tile, c.R - r);
             const int l = pair ? lane & 7 : lane;
             const T *m = static_cast<const T *>(pair && (lane & 8) ? c.w_up : c.w);
@@ -112,8 +110,8 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
             }
         }
         if (lane == 0 && *reinterpret_cast<volatile int *>(&abort_flag)) {
-            drain(bar, a.stages, issued);
-            if (a.x_pitch) drain(xbar, 1, 1);
+            drain(ring.bar, a.stages, issued);
+            if (a.x_pitch && group == 0) drain(xbar, 1, 1);
         }
         return;
     }
@@ -121,31 +119,19 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
     if (a.x_pitch) tc::mbar_wait(xbar, 0, &abort_flag, a.status, WAIT_NS);
     const T *xb = a.x_pitch ? reinterpret_cast<const T *>(smem + a.x_at) : x;
     const int64_t xs = a.x_pitch ? a.x_pitch / 2 : c.x_stride;
-    float4 *red = reinterpret_cast<float4 *>(smem + a.red_at);
-    int buf = 0;
-    for (int64_t u = u0; u < u1; ++u) {
+    auto info = [&](int64_t u) {
+        const int i = (int)(u / a.tiles);
+        return make_int2(first_s[i], first_s[i + 1] - first_s[i]);
+    };
+    auto at = [&](int row) { return xb + row * xs; };
+    auto done = [&](int64_t u, const int2 &in, const float4 *s, int nt, int thread) {
+        if (*reinterpret_cast<volatile int *>(&abort_flag)) return;
         const int i = (int)(u / a.tiles), r = (int)(u - (int64_t)i * a.tiles) * a.tile, here = min(a.tile, c.R - r);
-        const int first = first_s[i], n = first_s[i + 1] - first, nt = (n + 7) / 8;
         const int64_t e = expert_s[i];
-        const T *xp[NTM];
-#pragma unroll
-        for (int j = 0; j < NTM; ++j) xp[j] = xb + (first + min(j * 8 + g, n - 1)) * xs + t4 * 8;
-        float acc[NTM][4] = {};
-        for (int k0 = 0; k0 < c.K; k0 += a.kc) {
-            ring.wait_full();
-            stage_products_nt<T, NTM>(ring, min(a.kc, c.K - k0), k0, nt, xp, acc, warp, lane);
-            ring.release(lane);
-            ring.next();
-        }
-        float4 *s = red + buf * CONSUMERS * NTM * 32;
-        share_sums<NTM>(s, nt, acc, warp, lane);
-        consumer_sync();
-        buf ^= 1;  // the next sums go elsewhere, those after them behind the next barrier
-        if (*reinterpret_cast<volatile int *>(&abort_flag)) continue;
         const int rl = pair ? 3 : 4;  // a unit's rows: 8 or 16
-        for (int j = tid; j < nt << (rl + 3); j += CONSUMERS * 32) {
+        for (int j = thread; j < nt << (rl + 3); j += GROUP_WARPS * 32) {
             const int row = j & ((1 << rl) - 1), col = (j >> rl) & 7, tile = j >> (rl + 3), l = (row & 7) * 4 + (col >> 1);
-            if (row >= here || tile * 8 + col >= n) continue;
+            if (row >= here || tile * 8 + col >= in.y) continue;
             float v[1] = {sum_of(s, nt, tile, l, (row >> 3) * 2 + (col & 1))};
             if (c.bias != nullptr) v[0] += c.bias[e * c.R + r + row];
             activate(v, c.act);
@@ -154,15 +140,16 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
                 if (c.bias_up != nullptr) up += c.bias_up[e * c.R + r + row];
                 v[0] *= up;
             }
-            const int64_t at = first + tile * 8 + col;
+            const int64_t to = in.x + tile * 8 + col;
             if (c.residual != nullptr) {
                 Pack<T, 1> p;
-                p.load(static_cast<const T *>(c.residual) + at * c.residual_stride + r + row);
+                p.load(static_cast<const T *>(c.residual) + to * c.residual_stride + r + row);
                 v[0] += p.get(0);
             }
-            static_cast<T *>(c.y)[at * c.y_stride + r + row] = elem_of<T>(v[0]);
+            static_cast<T *>(c.y)[to * c.y_stride + r + row] = elem_of<T>(v[0]);
         }
-    }
+    };
+    stream_units<T, NTM>(ring, u0, u1, c.K, a.kc, reinterpret_cast<float4 *>(smem + a.red_at), warp, lane, info, at, done);
 }
 
 int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
@@ -178,11 +165,14 @@ int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
     a.tiles = (c.R + a.tile - 1) / a.tile;
     a.kc = std::min(KC, (c.K + 31) / 32 * 32);
     a.pitch = pitch_of(a.kc);
-    const size_t xb = (size_t)c.n_rows * pitch_of(c.K), red = (size_t)2 * CONSUMERS * ntm * 512, most = SMEM_LIMIT - 4096;
-    const bool staged = xb <= X_SMEM;
+    const size_t ring = (size_t)GROUPS * 16 * a.pitch, red = (size_t)CONSUMERS * ntm * 512, most = SMEM_LIMIT - 4096;
+    a.stages = (int)std::min<size_t>(MAX_STAGES, (most - red) / ring);
+    // the rows are staged where that costs a stage of each ring at most
+    const size_t xb = (size_t)c.n_rows * pitch_of(c.K);
+    const bool staged = a.stages > 2 && (a.stages - 1) * ring + red + xb <= most;
+    if (staged && a.stages * ring + red + xb > most) --a.stages;
     a.x_pitch = staged ? pitch_of(c.K) : 0;
-    a.stages = (int)std::min<size_t>(MAX_STAGES, (most - (staged ? xb : 0) - red) / ((size_t)16 * a.pitch));
-    a.x_at = a.stages * 16 * a.pitch;
+    a.x_at = (int)(a.stages * ring);
     a.red_at = a.x_at + (int)(staged ? xb : 0);
     const size_t smem = a.red_at + red;
     const int64_t units = (int64_t)std::min(c.E, c.n_rows) * a.tiles;

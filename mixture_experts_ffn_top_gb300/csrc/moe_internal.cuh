@@ -245,6 +245,7 @@ struct Decode16Call {
     int64_t out_stride;
 };
 constexpr int DECODE_MAX_TOKENS = 32;
+constexpr size_t DECODE_ARRIVALS_OFFSET = 224;  // of the workspace: 64-bit count of the grid barriers' arrivals
 size_t decode16_ws_bytes(int N, int E, int F, int top_k, int Fs);
 // barrier_ns, extra_arrivals: failure-detection check, a first barrier that cannot complete and its limit (0 normally)
 int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned long long barrier_ns = 0,

@@ -19,9 +19,11 @@
 namespace moe {
 namespace s16 {
 
-constexpr int CONSUMERS = 8;                       // warps
-constexpr int THREADS = (CONSUMERS + 1) * 32;      // and the producer, the last warp
-constexpr int MAX_STAGES = 16;
+constexpr int CONSUMERS = 16;                      // warps, in
+constexpr int GROUPS = 2;                          // groups, each with a ring and a producer warp of its own
+constexpr int GROUP_WARPS = CONSUMERS / GROUPS;
+constexpr int THREADS = (CONSUMERS + GROUPS) * 32; // the producers are the last warps
+constexpr int MAX_STAGES = 8;                      // of a ring
 constexpr int MAX_ROWS = 32;                       // activation rows: four tiles of columns
 constexpr size_t SMEM_LIMIT = 227 * 1024;
 constexpr unsigned long long WAIT_NS = 1000000000ull;  // 1 s: a healthy wait takes microseconds
@@ -49,18 +51,30 @@ __device__ __forceinline__ void mma_chunk(float (&d)[4], const uint4 &lo, const 
     mma<T>(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
+// Named barriers: 1 of all consumers, 2 on of a group.
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(GROUP_WARPS * 32) : "memory");
+}
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory"); }
 
-// The ring: stages of 16 rows `pitch` bytes apart; full barriers (the copies' bytes) and empty ones (a warp each).
-// Every wait is bounded: when one runs out, the CTA's abort flag is raised and all further waits return at once, so
-// that every thread still walks its loops and barriers to their end (and writes no result).
+// A group's ring: stages of 16 rows `pitch` bytes apart; full barriers (the copies' bytes) and empty ones (a warp
+// each).  The group sees every phase of its barriers in order, which their parity alone would not survive otherwise:
+// copies land out of order, so a ring that two groups shared in turns could show one of them a slot's phase before
+// last.  Every wait is bounded: when one runs out, the CTA's abort flag is raised and all further waits return at once,
+// so that every thread still walks its loops and barriers to their end (and writes no result).
 struct Ring {
     char *base;
     uint32_t bar;   // full barriers, then empty ones
-    int stages, pitch, slot = 0;
-    uint32_t phase = 0;
+    int stages, pitch;
     int *abort_flag;
     unsigned *status;
+    int slot = 0;
+    uint32_t phase = 0;
+
+    // `mem`: the rings behind one another, `bars`: their barriers
+    __device__ __forceinline__ Ring(char *mem, uint32_t bars, int group, int stages, int pitch, int *abort_flag, unsigned *status)
+        : base(mem + (size_t)group * stages * 16 * pitch), bar(bars + group * stages * 16), stages(stages), pitch(pitch),
+          abort_flag(abort_flag), status(status) {}
 
     __device__ __forceinline__ char *stage() const { return base + (size_t)slot * 16 * pitch; }
     __device__ __forceinline__ void next() {
@@ -98,61 +112,94 @@ __device__ __forceinline__ void drain(uint32_t full, int stages, int issued) {
         while (!tc::mbar_try(full + (i % stages) * 8, (i / stages) & 1) && tc::globaltimer() - t0 < WAIT_NS) {}
 }
 
-// Two barriers a stage in shared memory at `bar`; call with one thread, then synchronise the CTA.
-__device__ __forceinline__ void init_ring(uint32_t bar, int stages) {
-    for (int i = 0; i < stages; ++i) {
-        tc::mbar_init(bar + i * 8, 1);
-        tc::mbar_init(bar + (stages + i) * 8, CONSUMERS);
-    }
+// The rings' barriers in shared memory at `bars`; call with one thread, then synchronise the CTA.
+__device__ __forceinline__ void init_rings(uint32_t bars, int stages) {
+    for (int r = 0; r < GROUPS; ++r)
+        for (int i = 0; i < stages; ++i) {
+            tc::mbar_init(bars + (r * 2 * stages + i) * 8, 1);
+            tc::mbar_init(bars + ((r * 2 + 1) * stages + i) * 8, GROUP_WARPS);
+        }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-// Adds the products of the ring's stage, `cols` columns of it from column k0 on, to acc: NT tiles of 8 activation
-// rows, x[n] the lane's row of tile n (columns 8 t on).
-template <typename T, int NT, int NTM>
-__device__ __forceinline__ void stage_products(const Ring &r, int cols, int k0, const T *const (&x)[NTM],
-                                               float (&acc)[NTM][4], int warp, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    const char *w = r.stage() + g * r.pitch + t * 16;
-#pragma unroll 4
-    for (int c = warp * 32; c < cols; c += CONSUMERS * 32) {
-        const bool in = c + t * 8 < cols;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo, b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = lo;
-        if (in) {
-            lo = *reinterpret_cast<const uint4 *>(w + c * 2);
-            hi = *reinterpret_cast<const uint4 *>(w + 8 * r.pitch + c * 2);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4 *>(x[n] + k0 + c);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_chunk<T>(acc[n], lo, hi, b[n]);
-    }
-}
-// The same for a number of tiles known at run time.
-template <typename T, int NTM>
-__device__ __forceinline__ void stage_products_nt(const Ring &r, int cols, int k0, int nt, const T *const (&x)[NTM],
-                                                  float (&acc)[NTM][4], int warp, int lane) {
-    if (NTM == 1 || nt == 1) return stage_products<T, 1, NTM>(r, cols, k0, x, acc, warp, lane);
-    if (NTM == 2 || nt == 2) return stage_products<T, NTM < 2 ? 1 : 2, NTM>(r, cols, k0, x, acc, warp, lane);
-    stage_products<T, NTM, NTM>(r, cols, k0, x, acc, warp, lane);
-}
+constexpr int KC = 1024;                             // columns of a stage at most
+constexpr int CHUNKS = KC / (GROUP_WARPS * 32);      // 32-wide chunks a warp takes of a stage
 
-// The warps' sums of a tile meet in shared memory, red [CONSUMERS][nt][32] float4 in the accumulators' order.
+// The sums of a group's warps meet in shared memory, red [GROUP_WARPS][nt][32] float4 in the accumulators' order.
 template <int NTM>
 __device__ __forceinline__ void share_sums(float4 *red, int nt, const float (&acc)[NTM][4], int warp, int lane) {
 #pragma unroll
     for (int n = 0; n < NTM; ++n)
         if (n < nt) red[(warp * nt + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
 }
-// Component `i` (0..3) of lane `l` in tile n, added over the warps in order.
+// Component `i` (0..3) of lane `l` in tile n, added over `WARPS` warps in order.
+template <int WARPS = GROUP_WARPS>
 __device__ __forceinline__ float sum_of(const float4 *red, int nt, int n, int l, int i) {
     const float *p = reinterpret_cast<const float *>(red + n * 32 + l) + i;
     float v = p[0];
 #pragma unroll
-    for (int w = 1; w < CONSUMERS; ++w) v += p[w * nt * 128];
+    for (int w = 1; w < WARPS; ++w) v += p[w * nt * 128];
     return v;
+}
+
+// Tiles of weight rows ("units") u0 .. u1 - 1 times the activation rows each of them meets, K columns, kc a stage.
+//   info(u)    {first, n}: the unit's activation rows, n <= 8 NTM of them from place `first` on
+//   at(i)      address of the activation row in place i
+//   done(u, info, sums, nt, thread)  by all threads of a group: its warps' sums of the unit's nt tiles of 8 rows (see sum_of)
+// The units go to the groups in turn (as their producers deal them): what a stage costs a warp beside its products (the
+// wait, the addresses) is paid by half of the warps, and the latency of the activations, asked for before the wait,
+// passes while the other group works.  red: GROUP_WARPS * NTM * 32 float4 a group.
+template <typename T, int NTM, typename Info, typename At, typename Done>
+__device__ __forceinline__ void stream_units(Ring &ring, int64_t u0, int64_t u1, int K, int kc, float4 *red, int warp,
+                                             int lane, Info info, At at, Done done) {
+    const int g = lane >> 2, t = lane & 3, group = warp / GROUP_WARPS, gw = warp % GROUP_WARPS;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float4 *sums = red + group * GROUP_WARPS * NTM * 32;
+    for (int64_t u = u0 + group; u < u1; u += GROUPS) {
+        const int2 in = info(u);
+        const int nt = (in.y + 7) / 8;
+        const T *x[NTM];
+#pragma unroll
+        for (int n = 0; n < NTM; ++n) x[n] = static_cast<const T *>(at(in.x + min(n * 8 + g, in.y - 1))) + t * 8;
+        float acc[NTM][4] = {};
+        for (int k0 = 0; k0 < K; k0 += kc) {
+            const int cols = min(kc, K - k0);
+            uint4 b[CHUNKS];
+#pragma unroll
+            for (int q = 0; q < CHUNKS; ++q) {
+                const int c = (q * GROUP_WARPS + gw) * 32;
+                b[q] = zero;
+                if (c + t * 8 < cols) b[q] = *reinterpret_cast<const uint4 *>(x[0] + k0 + c);
+            }
+            ring.wait_full();
+            const char *w = ring.stage() + g * ring.pitch + t * 16;
+#pragma unroll
+            for (int q = 0; q < CHUNKS; ++q) {
+                const int c = (q * GROUP_WARPS + gw) * 32;
+                if (c >= cols) break;
+                const bool inside = c + t * 8 < cols;
+                uint4 lo = zero, hi = zero;
+                if (inside) {
+                    lo = *reinterpret_cast<const uint4 *>(w + c * 2);
+                    hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
+                }
+                mma_chunk<T>(acc[0], lo, hi, b[q]);
+#pragma unroll
+                for (int n = 1; n < NTM; ++n)
+                    if (n < nt) {
+                        uint4 bn = zero;
+                        if (inside) bn = *reinterpret_cast<const uint4 *>(x[n] + k0 + c);
+                        mma_chunk<T>(acc[n], lo, hi, bn);
+                    }
+            }
+            ring.release(lane);
+            ring.next();
+        }
+        group_sync(group);  // the sums before these have been read
+        share_sums<NTM>(sums, nt, acc, gw, lane);
+        group_sync(group);
+        done(u, in, sums, nt, gw * 32 + lane);
+    }
 }
 
 }  // namespace s16

@@ -1,31 +1,50 @@
-// act.cuh -- activations of the 16-bit products' epilogues, in fp32, a few 2^-21 of the result.
+// act.cuh -- activations of the 16-bit products' epilogues, in fp32, a few 2^-21 of the result, two values at a time.
 #pragma once
 
-#include "moe_internal.cuh"
+#include "pair.cuh"
 
 namespace moe {
 
-__device__ __forceinline__ float act_relu(float v) { return v < 0.0f ? 0.0f : v; }  // a NaN stays
+__device__ __forceinline__ float act_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float act_rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float act_relu(float v) {  // a NaN stays
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 // v / (1 + e^-v); for v below -88 the exponential is infinite and the result -0, as the definition rounds
-__device__ __forceinline__ float act_silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float act_silu(float v) { return v * act_rcp(1.0f + act_exp2(v * -1.44269504f)); }
 
-// v Phi(v), Phi the normal distribution: with z = |v| / sqrt(2) and t = 1 / (1 + 0.35 z),
-// erfc(z) e^(z^2) = t p(t), p a polynomial fitted to it over all z >= 0 (weighted least squares, 8.3e-7 relative).
-// No cancellation on the negative side, where 1 + erf would have lost the digits.
-__device__ __forceinline__ float act_gelu(float v) {
-    const float z = fabsf(v) * 0.70710678f;
-    const float t = __fdividef(1.0f, fmaf(z, 0.35f, 1.0f));
-    float p = -0.0851045461f;
-    p = fmaf(p, t, 0.201206708f);
-    p = fmaf(p, t, -0.0145455287f);
-    p = fmaf(p, t, 0.162940193f);
-    p = fmaf(p, t, 0.154674005f);
-    p = fmaf(p, t, 0.1859089f);
-    p = fmaf(p, t, 0.19745316f);
-    p = fmaf(p, t, 0.197466285f);
-    const float q = 0.5f * t * p * __expf(-z * z);
-    return v * (v < 0.0f ? q : 1.0f - q);
+// v Phi(v) = max(v, 0) - |v| Q(|v|), Phi the normal distribution, Q = 1 - Phi = erfc(z) / 2 with z = |v| / sqrt(2).
+// With t = 1 / (1 + 0.35 z), erfc(z) e^(z^2) = t p(t), p a polynomial fitted to it over all z >= 0 (weighted least
+// squares, 8.3e-7 relative; halved here).  No cancellation on the negative side, where 1 + erf would have lost the
+// digits.  An infinity meets Q = 0 as 1e5.
+__device__ __forceinline__ void act_gelu(float &a, float &b) {
+    const float x = fabsf(a), y = fabsf(b);
+    const F2 t = pair_of(act_rcp(fmaf(x, 0.24748737f, 1.0f)), act_rcp(fmaf(y, 0.24748737f, 1.0f)));
+    auto c = [](float v) { return pair_of(v, v); };
+    F2 p = c(-0.0425522731f);
+    p = fma(p, t, c(0.100603354f));
+    p = fma(p, t, c(-0.00727276437f));
+    p = fma(p, t, c(0.0814700965f));
+    p = fma(p, t, c(0.0773370025f));
+    p = fma(p, t, c(0.09295445f));
+    p = fma(p, t, c(0.09872658f));
+    p = fma(p, t, c(0.0987331425f));
+    const F2 z = pair_of(x * 0.84932180f, y * 0.84932180f);  // z^2 log2(e) = (|v| sqrt(log2(e) / 2))^2
+    const float2 s = values_of(mul(z, z));
+    const float2 q = values_of(mul(mul(t, p), pair_of(act_exp2(-s.x), act_exp2(-s.y))));
+    a = fmaf(-fminf(x, 1e5f), q.x, act_relu(a));
+    b = fmaf(-fminf(y, 1e5f), q.y, act_relu(b));
 }
 
 template <int N>
@@ -41,7 +60,10 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
             break;
         case MOE_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_gelu(v[i]);
+            for (int i = 0; i < N; i += 2) {
+                float none = 0.0f;
+                act_gelu(v[i], i + 1 < N ? v[i + 1] : none);
+            }
             break;
         default: break;
     }

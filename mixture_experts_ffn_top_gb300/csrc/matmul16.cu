@@ -2,17 +2,21 @@
 // with bias, activation (or gate and up) and residual in the epilogue:
 //   y[j] = act(W[e] x[j] + b[e]) (* (U[e] x[j] + c[e])) (+ residual[j])
 //
-// Two kernels.  Up to 32 rows (serving): every weight is read for a few rows, so its bytes bound the product;
-// few16_kernel streams them as stream16.cuh says.  More rows (prompts, training): rows16_kernel forms tiles of 128
-// rows x 256 weight rows (gate and up: 128 of each, side by side) on the tensor cores.
+// Two kernels.  Few rows (serving; up to 32, see few::serves): every weight is read for a few rows, so its bytes bound the product;
+// few16_kernel streams them as stream16.cuh says.  More rows (prompts, training): rows16_kernel forms tiles of 256
+// weight rows (gate and up: 128 of each) on the tensor cores.
 //
-// rows16_kernel is persistent, a CTA an SM, its warps in roles: a producer that brings both operands in by TMA
-// (128-byte swizzle, 64 columns a stage, four stages), an issuer of tcgen05.mma (M 128, N 256, K 16; accumulators in
-// tensor memory, two tiles of 256 columns so that the next tile's products run under this one's epilogue), and eight
-// epilogue warps (a lane holds a row's 32 columns; bias from shared memory; the 16-bit results cross shared memory so
-// that rows leave in whole sectors).  Segments start at any row: a tile reads past its segment's end and stores
-// nothing of what it finds there.
+// rows16_kernel is persistent; two CTAs of a cluster work as a pair: the weights are the 256 rows of their products
+// (tcgen05.mma cta_group::2, 128 rows a CTA), up to 256 token rows the columns, in steps of 16, so that ragged
+// segments cost what they hold.  Warps in roles: in each CTA a producer that brings its 128 weight rows and its half of the token rows
+// in by TMA (128-byte swizzle, 64 columns a stage, six stages), in the first an issuer of the products (accumulators in
+// tensor memory, two tiles of 256 columns so that the next tile's products run under this one's epilogue), in each twelve
+// epilogue warps (a lane holds a weight row's results for 32 tokens; they cross shared memory so that rows leave in
+// whole sectors).  Sharing the token rows between the CTAs is what lets shared memory keep up: alone, a CTA's products would
+// read 96 bytes a cycle while its copies write 94.  Segments start at any row: a tile reads past its segment's end and
+// stores nothing of what it finds there.
 #include <algorithm>
+#include <atomic>
 
 #include "act.cuh"
 #include "stream16.cuh"
@@ -152,28 +156,46 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
     stream_units<T, NTM>(ring, u0, u1, c.K, a.kc, reinterpret_cast<float4 *>(smem + a.red_at), warp, lane, info, at, done);
 }
 
+// Whether the rows of `c` can lie in shared memory beside the rings, and the stages of these.
+bool stage_rows(const Matmul16Call &c, int pitch, size_t red, int *stages) {
+    const size_t ring = (size_t)GROUPS * 16 * pitch, most = SMEM_LIMIT - 4096, xb = (size_t)c.n_rows * pitch_of(c.K);
+    *stages = (int)std::min<size_t>(MAX_STAGES, (most - red) / ring);
+    // where that costs a stage of each ring at most
+    const bool staged = *stages > 2 && (*stages - 1) * ring + red + xb <= most;
+    if (staged && *stages * ring + red + xb > most) --*stages;
+    return staged;
+}
+int tiles_of(int n_rows) { return n_rows <= 8 ? 1 : n_rows <= 16 ? 2 : 4; }
+size_t red_bytes(int n_rows) { return (size_t)CONSUMERS * tiles_of(n_rows) * 512; }
+int columns(int K) { return std::min(KC, (K + 31) / 32 * 32); }
+
+// The rows this kernel serves: 32 are four column tiles of its instructions, and beyond them it would read the weights
+// again.  Of one matrix 8, or all that can lie in shared memory: rows that every unit of weights fetches from L2 cost
+// as much as these.
+bool serves(const Matmul16Call &c) {
+    int stages;
+    if (c.n_rows > MAX_ROWS) return false;
+    return c.expStart != nullptr || c.n_rows <= 8 || stage_rows(c, pitch_of(columns(c.K)), red_bytes(c.n_rows), &stages);
+}
+
 int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
     Args a{};
     a.c = c;
     a.status = status;
     const int sms = std::max(1, device_sm_count());
-    const int ntm = c.n_rows <= 8 ? 1 : c.n_rows <= 16 ? 2 : 4;
+    const int ntm = tiles_of(c.n_rows);
     const bool pair = c.w_up != nullptr;
     // Units of 16 weight rows (8 pairs), fewer where that leaves SMs without one.
     const int64_t most_rows = (int64_t)std::min(c.E, c.n_rows) * c.R;
     a.tile = (int)std::min<int64_t>(pair ? 8 : 16, (most_rows + sms - 1) / sms);
     a.tiles = (c.R + a.tile - 1) / a.tile;
-    a.kc = std::min(KC, (c.K + 31) / 32 * 32);
+    a.kc = columns(c.K);
     a.pitch = pitch_of(a.kc);
-    const size_t ring = (size_t)GROUPS * 16 * a.pitch, red = (size_t)CONSUMERS * ntm * 512, most = SMEM_LIMIT - 4096;
-    a.stages = (int)std::min<size_t>(MAX_STAGES, (most - red) / ring);
-    // the rows are staged where that costs a stage of each ring at most
-    const size_t xb = (size_t)c.n_rows * pitch_of(c.K);
-    const bool staged = a.stages > 2 && (a.stages - 1) * ring + red + xb <= most;
-    if (staged && a.stages * ring + red + xb > most) --a.stages;
+    const size_t red = red_bytes(c.n_rows), most = SMEM_LIMIT - 4096;
+    const bool staged = stage_rows(c, a.pitch, red, &a.stages);
     a.x_pitch = staged ? pitch_of(c.K) : 0;
-    a.x_at = (int)(a.stages * ring);
-    a.red_at = a.x_at + (int)(staged ? xb : 0);
+    a.x_at = (int)((size_t)a.stages * GROUPS * 16 * a.pitch);
+    a.red_at = a.x_at + (staged ? c.n_rows * a.x_pitch : 0);
     const size_t smem = a.red_at + red;
     const int64_t units = (int64_t)std::min(c.E, c.n_rows) * a.tiles;
     const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
@@ -198,75 +220,133 @@ namespace rows {
 
 using namespace tc;
 
-constexpr int TM = 128, TK = 64, STAGES = 4;
-constexpr int EPI_WARPS = 8, EPI0 = 4;  // the epilogue's first warp: warp & 3 is its quarter of the lanes
+constexpr int TK = 64;         // columns of a stage: 128 bytes, the swizzle's width
+constexpr int HALF = 128;      // weight rows of a CTA, and token rows it brings at most
+constexpr int TILE = 2 * HALF; // of the pair
+constexpr int MAX_STAGES = 10;
+constexpr int STAGE_A = HALF * TK * 2;              // bytes of a stage's weight rows
+constexpr size_t RING = 6 * 2 * (size_t)STAGE_A;    // six stages with all token rows, more with fewer
+constexpr int SPAN = 2;        // stages that one wait of the issuer covers
+constexpr int RASTER = 8;       // row tiles side by side
+constexpr int EPI_WARPS = 12, EPI0 = 4;  // the epilogue's first warp: warp & 3 is its quarter of the lanes
+constexpr int EPI_SETS = EPI_WARPS / 4; // of four warps, on 32 token rows in turn
 constexpr int THREADS = (EPI0 + EPI_WARPS) * 32;
-constexpr int PATCH = 32 * 64;  // bytes a warp's 32 rows x 32 results take in shared memory
+constexpr int PATCH = 32 * 64;          // bytes of 32 rows x 32 16-bit results
+constexpr int SWAP = 32 * 32 * 4;       // bytes of 32 x 32 fp32 values of up on their way to the gate's warp
 constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+template <bool PAIR>
+struct Shape {
+    static constexpr int COLS = PAIR ? HALF : TILE;  // result columns of the pair's tile
+    // a patch a warp; gate and up: one for both warps of a pair, where up's values pass first
+    static constexpr int PATCHES = (PAIR ? EPI_WARPS / 2 * SWAP : EPI_WARPS * PATCH);
+    static constexpr size_t SMEM = 1024 + RING + PATCHES + (MAX_E + 1) * 8;
+};
 
 struct Args {
     Matmul16Call c;
     unsigned *status;
     int wtiles;  // weight tiles a matrix
-    int vec_y, vec_res;  // 16-byte accesses fit y, the residual
+    int width;   // token rows of a tile at most
+    int vec_y;   // 16-byte accesses fit y
+    int stages, stage;  // of the ring: how many (a multiple of SPAN), bytes of each
 };
-
-template <int TN>
-__host__ __device__ constexpr int stage_bytes() { return (TM + TN) * TK * 2; }
-template <int TN>
-__host__ __device__ constexpr size_t smem_bytes() {
-    return 1024 + (size_t)STAGES * stage_bytes<TN>() + EPI_WARPS * PATCH + 2 * 2 * TN * 4 + (MAX_E + 1) * 8;
-}
+struct Maps {
+    CUtensorMap w, up;
+    CUtensorMap x[4];  // boxes of 16, 32, 64 and 128 rows
+};
 
 struct Item {
     int e, row0, nrows, wt;
+    int n;  // columns of the product: nrows rounded up to 16
 };
 
-// TN: weight rows of a tile (gate and up together).
-template <typename T, int TN, bool PAIR>
-__global__ void __launch_bounds__(THREADS, 1)
-rows16_kernel(const Args a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-              const __grid_constant__ CUtensorMap map_up) {
-    constexpr int COLS = PAIR ? TN / 2 : TN;  // results of a tile's row
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t at_cta(uint32_t addr, uint32_t rank) {  // the same place in CTA `rank`
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// One lane of a converged warp.  The issuer's warp walks its loops as a whole and lets one lane issue: what it computes
+// is then known to be the same in all lanes and lies in the uniform registers that the instruction wants.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint32_t bar) {  // arrives in both CTAs
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+// (Release at the CTA's scope: what it hands back is tensor memory, read behind tcgen05's own fence; a wider release would
+// wait for the results' stores.)
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+template <typename T, bool PAIR>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+rows16_kernel(const Args a, const __grid_constant__ Maps maps) {
+    using S = Shape<PAIR>;
     extern __shared__ char smem_raw[];
     char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    char *patches = smem + STAGES * stage_bytes<TN>();
-    float *bias_s = reinterpret_cast<float *>(patches + EPI_WARPS * PATCH);  // [2][2][TN]: bias, bias_up of a tile
-    int *start_s = reinterpret_cast<int *>(bias_s + 2 * 2 * TN);             // [E + 1] offsets
-    int *item_s = start_s + MAX_E + 1;                                       // [E + 1] first row tile of an expert
-    __shared__ __align__(8) unsigned long long bars[2 * STAGES + 4];
+    const int STAGES = a.stages, STAGE = a.stage;
+    char *patches = smem + RING;
+    int *start_s = reinterpret_cast<int *>(patches + S::PATCHES);  // [E + 1] offsets
+    int *item_s = start_s + MAX_E + 1;                             // [E + 1] first row tile
+    __shared__ __align__(8) unsigned long long bars[2 * MAX_STAGES + 4];
     __shared__ uint32_t tmem_s;
     __shared__ int abort_flag, bad_s, scan_s[THREADS / 32];
     const Matmul16Call &c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t full = smem_u32(bars), empty = full + STAGES * 8, tfull = empty + STAGES * 8, tempty = tfull + 16;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, rank = (int)cta_rank();
+    const uint32_t full = smem_u32(bars), empty = full + MAX_STAGES * 8, tfull = empty + MAX_STAGES * 8, tempty = tfull + 16;
     if (tid == 0) {
         abort_flag = bad_s = 0;
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(full + i * 8, 1);
-            mbar_init(empty + i * 8, 1);
-        }
+        for (int i = 0; i < STAGES; ++i) mbar_init(empty + i * 8, 1);
+        for (int i = 0; i < STAGES / SPAN; ++i) mbar_init(full + i * 8, SPAN);
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + i * 8, 1);
-            mbar_init(tempty + i * 8, EPI_WARPS);
+            mbar_init(tempty + i * 8, 2 * EPI_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_map(&map_x);
-        prefetch_map(&map_w);
-        if (PAIR) prefetch_map(&map_up);
+        prefetch_map(&maps.w);
+        if (PAIR) prefetch_map(&maps.up);
+        prefetch_map(&maps.x[3]);
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_s)), "r"(2 * TN)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_s)), "r"(2 * TILE)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     __syncthreads();
     // ---- row tiles of every expert
-    int nE = c.expStart == nullptr ? 1 : c.E;
+    const int nE = c.expStart == nullptr ? 1 : c.E;
     if (c.expStart == nullptr) {
         if (tid == 0) {
             start_s[0] = 0, start_s[1] = c.n_rows;
-            item_s[0] = 0, item_s[1] = (c.n_rows + TM - 1) / TM;
+            item_s[0] = 0, item_s[1] = (c.n_rows + a.width - 1) / a.width;
         }
     } else {
         int base = 0;
@@ -278,7 +358,7 @@ rows16_kernel(const Args a, const __grid_constant__ CUtensorMap map_x, const __g
                 if (s < 0 || s1 < s || s1 > c.n_rows || (e == 0 && s != 0)) bad_s = 1;
                 start_s[e] = s;
                 if (e == nE - 1) start_s[nE] = s1;
-                t = (max(s1 - s, 0) + TM - 1) / TM;
+                t = (max(s1 - s, 0) + a.width - 1) / a.width;
             }
             int in = t;
 #pragma unroll
@@ -296,14 +376,21 @@ rows16_kernel(const Args a, const __grid_constant__ CUtensorMap map_x, const __g
         }
         if (tid == 0) item_s[nE] = base;
     }
+    tc_fence_before();
     __syncthreads();
+    pair_sync();  // both CTAs' barriers are initialised
     tc_fence_after();
     const uint32_t tmem = tmem_s;
     const bool bad = bad_s != 0;
     if (bad && blockIdx.x == 0 && tid == 0) atomicOr(a.status, MOE_DEV_BAD_CSR);
     const int64_t items = bad ? 0 : (int64_t)item_s[nE] * a.wtiles;
-    const int steps = (c.K + TK - 1) / TK;
-    // item: expert by expert, weight tile by weight tile, the row tiles of one beside each other (they share its weights)
+    // a wait in the thread that issues products costs it some 300 cycles of issue time, more than half of a stage's
+    // products: it waits once for SPAN stages (an odd one out is followed by one without copies), which are released one by one
+    const int spans = (c.K + SPAN * TK - 1) / (SPAN * TK);
+    const int64_t first = blockIdx.x / 2, stride = gridDim.x / 2;
+    // item: expert by expert, RASTER row tiles at a time, weight tile by weight tile, the row tiles of one beside each other
+    // (the pairs at work share weights and rows about evenly).
+    // An expert's rows are dealt evenly to its row tiles: the product's width follows them in steps of 16.
     auto item_at = [&](int64_t it) {
         int lo = 0, hi = nE;  // the expert with item_s[e] * wtiles <= it < item_s[e + 1] * wtiles
         while (hi - lo > 1) {
@@ -314,62 +401,88 @@ rows16_kernel(const Args a, const __grid_constant__ CUtensorMap map_x, const __g
                 hi = mid;
         }
         const int tiles = item_s[lo + 1] - item_s[lo], in = (int)(it - (int64_t)item_s[lo] * a.wtiles);
+        const int rows = start_s[lo + 1] - start_s[lo], per = ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+        const int g = in / (RASTER * a.wtiles), of = in - g * RASTER * a.wtiles, wide = min(RASTER, tiles - g * RASTER);
         Item x;
         x.e = lo;
-        x.wt = in / tiles;
-        x.row0 = start_s[lo] + (in - x.wt * tiles) * TM;
-        x.nrows = min(TM, start_s[lo + 1] - x.row0);
+        x.wt = of / wide;
+        const int t = g * RASTER + of - x.wt * wide;
+        x.row0 = start_s[lo] + t * per;
+        x.nrows = max(0, min(per, rows - t * per));
+        x.n = max(16, (x.nrows + 15) / 16 * 16);
         return x;
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int slot = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
-                const Item x = item_at(it);
-                const int wrow = x.e * c.R + x.wt * COLS;
-                for (int k = 0; k < steps; ++k) {
-                    ok = mbar_wait(empty + slot * 8, phase ^ 1, &abort_flag, a.status, WAIT_NS);
-                    if (!ok) break;
-                    const uint32_t at = smem_u32(smem) + slot * stage_bytes<TN>(), b = full + slot * 8;
-                    mbar_expect_tx(b, stage_bytes<TN>());
-                    tma_load_2d(at, &map_x, k * TK, x.row0, b);
-                    tma_load_2d(at + TM * TK * 2, &map_w, k * TK, wrow, b);
-                    if (PAIR) tma_load_2d(at + (TM + COLS) * TK * 2, &map_up, k * TK, wrow, b);
-                    ++issued;
-                    if (++slot == STAGES) slot = 0, phase ^= 1;
+        const uint32_t base = smem_u32(smem), lead_full = at_cta(full, 0);
+        int slot = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        auto wait_empty = [&]() {
+            ok = __all_sync(0xffffffffu, mbar_wait(empty + slot * 8, phase ^ 1, &abort_flag, a.status, WAIT_NS));
+            return ok;
+        };
+        for (int64_t it = first; it < items && ok; it += stride) {
+            const Item x = item_at(it);
+            const int mine = x.n / 2, box = mine <= 16 ? 0 : mine <= 32 ? 1 : mine <= 64 ? 2 : 3;
+            const uint32_t bytes = STAGE_A + (16u << box) * TK * 2;
+            const int wrow = x.e * c.R + x.wt * S::COLS + rank * (S::COLS / 2), xrow = x.row0 + rank * mine;
+            for (int k = 0; k < spans * SPAN; ++k) {
+                if (!wait_empty()) break;
+                const uint32_t at = base + slot * STAGE, b = lead_full + slot / SPAN * 8;
+                if (elected()) {
+                    if (k * TK < c.K) {
+                        if (rank == 0) mbar_expect_tx(full + slot / SPAN * 8, 2 * bytes);
+                        pair_load_2d(at, &maps.w, k * TK, wrow, b);
+                        if (PAIR) pair_load_2d(at + STAGE_A / 2, &maps.up, k * TK, wrow, b);
+                        pair_load_2d(at + STAGE_A, &maps.x[box], k * TK, xrow, b);
+                    } else if (rank == 0) {
+                        mbar_arrive(full + slot / SPAN * 8);
+                    }
                 }
+                __syncwarp();
+                ++issued;
+                if (++slot == STAGES) slot = 0, phase ^= 1;
             }
-            if (!ok) s16::drain(full, STAGES, issued);
         }
+        // the arrivals still on their way to this CTA's barriers
+        for (int i = 0; i < STAGES && ok && wait_empty(); ++i)
+            if (++slot == STAGES) slot = 0, phase ^= 1;
+        if (!ok && rank == 0 && lane == 0) s16::drain(full, STAGES / SPAN, (issued + SPAN - 1) / SPAN);  // of both CTAs; the other waits for this one at the end
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = (1u << 4) | (std::is_same_v<T, __half> ? 0u : (1u << 7) | (1u << 10)) |
-                                       ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
+        if (rank == 0) {
+            constexpr uint32_t idesc = (1u << 4) | (std::is_same_v<T, __half> ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(TILE >> 4) << 24);
+            const uint32_t base = smem_u32(smem);
             int slot = 0, buf = 0;
             uint32_t phase = 0, tphase = 0;
             bool ok = true, any = false;
-            for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
-                ok = mbar_wait(tempty + buf * 8, tphase ^ 1, &abort_flag, a.status, WAIT_NS);
+            for (int64_t it = first; it < items && ok; it += stride) {
+                const uint32_t desc = idesc | ((uint32_t)(item_at(it).n >> 3) << 17);
+                ok = __all_sync(0xffffffffu, mbar_wait(tempty + buf * 8, tphase ^ 1, &abort_flag, a.status, WAIT_NS));
                 if (!ok) break;
                 tc_fence_after();
-                for (int k = 0; k < steps; ++k) {
-                    ok = mbar_wait(full + slot * 8, phase, &abort_flag, a.status, WAIT_NS);
+                for (int k = 0; k < spans; ++k) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(full + slot / SPAN * 8, phase, &abort_flag, a.status, WAIT_NS));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = smem_u32(smem) + slot * stage_bytes<TN>();
+                    const uint64_t da = smem_desc_sw128(base + slot * STAGE), db = smem_desc_sw128(base + slot * STAGE + STAGE_A);
+                    const uint32_t d = tmem + buf * TILE;
+                    if (elected()) {
 #pragma unroll
-                    for (int j = 0; j < TK / 16; ++j)
-                        mma_f16(tmem + buf * TN, smem_desc_sw128(at + j * 32), smem_desc_sw128(at + TM * TK * 2 + j * 32), idesc,
-                                k > 0 || j > 0);
-                    mma_commit(empty + slot * 8);
+                        for (int q = 0; q < SPAN; ++q) {
+                            if (q == 0 || (k * SPAN + q) * TK < c.K)
+#pragma unroll
+                                for (int j = 0; j < TK / 16; ++j)  // (addresses in a descriptor count 16 bytes)
+                                    pair_mma(d, da + (uint32_t)(q * (STAGE / 16) + j * 2), db + (uint32_t)(q * (STAGE / 16) + j * 2), desc,
+                                             k > 0 || q > 0 || j > 0);
+                            pair_commit(empty + (slot + q) * 8);
+                        }
+                        if (k == spans - 1) pair_commit(tfull + buf * 8);
+                    }
+                    __syncwarp();
                     any = true;
-                    if (++slot == STAGES) slot = 0, phase ^= 1;
+                    if ((slot += SPAN) == STAGES) slot = 0, phase ^= 1;
                 }
-                if (!ok) break;
-                mma_commit(tfull + buf * 8);
                 if (++buf == 2) buf = 0, tphase ^= 1;
             }
             if (!ok && any) {
@@ -381,141 +494,143 @@ rows16_kernel(const Args a, const __grid_constant__ CUtensorMap map_x, const __g
             }
         }
     } else if (warp >= EPI0) {
-        const int ew = warp - EPI0, quarter = warp & 3, half = ew >> 2, et = tid - EPI0 * 32;
-        char *patch = patches + ew * PATCH;
+        // A lane has a weight row, its registers 32 token rows.  Gate and up: a CTA's first 64 lanes are gate rows, the
+        // others the same up rows, whose warp hands its values to the gate's.
+        const int ew = warp - EPI0, quarter = warp & 3, set = ew >> 2, side = PAIR ? quarter >> 1 : 0;
+        const int pw = PAIR ? set * 2 + (quarter & 1) : ew;  // the warp's patch, and its pair of warps
+        char *patch = patches + pw * (PAIR ? SWAP : PATCH);
+        float *swap = reinterpret_cast<float *>(patch);
         int buf = 0;
         uint32_t tphase = 0;
         T *y = static_cast<T *>(c.y);
         const T *res = static_cast<const T *>(c.residual);
-        for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const uint32_t lead_tempty = at_cta(tempty, 0);
+        const float *bias = side ? c.bias_up : c.bias;
+        for (int64_t it = first; it < items; it += stride) {
             const Item x = item_at(it);
-            const int col0 = x.wt * COLS;
-            float *bs = bias_s + buf * 2 * TN;
-            if (c.bias != nullptr || c.bias_up != nullptr) {
-                for (int i = et; i < COLS; i += EPI_WARPS * 32) {
-                    const bool in = col0 + i < c.R;
-                    const int64_t at = (int64_t)x.e * c.R + col0 + i;
-                    bs[i] = in && c.bias != nullptr ? c.bias[at] : 0.0f;
-                    if (PAIR) bs[TN + i] = in && c.bias_up != nullptr ? c.bias_up[at] : 0.0f;
-                }
-                asm volatile("bar.sync 2, %0;" ::"n"(EPI_WARPS * 32) : "memory");
-            }
+            // the warp's 32 result columns
+            const int col0 = x.wt * S::COLS + rank * (S::COLS / 2) + (PAIR ? quarter & 1 : quarter) * 32;
+            const bool in = col0 + lane < c.R;
+            const float b = bias != nullptr && in ? bias[(int64_t)x.e * c.R + col0 + lane] : 0.0f;
             const bool ok = __all_sync(0xffffffffu, mbar_wait(tfull + buf * 8, tphase, &abort_flag, a.status, WAIT_NS));
-            if (ok) {
-                tc_fence_after();
-                const int row = quarter * 32 + lane;  // of the tile
-                const bool warp_rows = quarter * 32 < x.nrows;
-                const int64_t yrow = (int64_t)(x.row0 + quarter * 32);
+            tc_fence_after();
 #pragma unroll 1
-                for (int c0 = half * (COLS / 2); c0 < (half + 1) * (COLS / 2); c0 += 32) {
-                    if (!warp_rows || col0 + c0 >= c.R) break;
-                    uint32_t r[32], ru[32];
-                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * TN + c0, r);
-                    if (PAIR) tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * TN + COLS + c0, ru);
+            for (int c0 = set * 32; c0 < x.nrows; c0 += EPI_SETS * 32) {
+                if (col0 >= c.R) break;  // the same for both warps of a pair
+                uint32_t r[32];
+                float v[32];
+                if (ok) {
+                    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * TILE + c0, r);
                     tmem_wait_ld();
                     tmem_reg_fence32(r);
-                    if (PAIR) tmem_reg_fence32(ru);
-                    float v[32];
+                }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                    if (c.bias != nullptr)
+                for (int i = 0; i < 32; ++i) v[i] = ok ? __uint_as_float(r[i]) + b : 0.0f;
+                if (PAIR) {
+                    if (side) {
+                        asm volatile("bar.sync %0, 64;" ::"r"(3 + 2 * pw) : "memory");  // the values before have been read
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += bs[c0 + i];
+                        for (int i = 0; i < 32; ++i) swap[i * 32 + lane] = v[i];
+                        asm volatile("bar.sync %0, 64;" ::"r"(4 + 2 * pw) : "memory");
+                        continue;
+                    }
                     activate(v, c.act);
-                    if (PAIR) {
-                        if (c.bias_up != nullptr)
+                    asm volatile("bar.sync %0, 64;" ::"r"(3 + 2 * pw) : "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(4 + 2 * pw) : "memory");
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= __uint_as_float(ru[i]) + bs[TN + c0 + i];
-                        else
+                    for (int i = 0; i < 32; ++i) v[i] *= swap[i * 32 + lane];
+                } else {
+                    activate(v, c.act);
+                }
+                const int rows = min(32, x.nrows - c0);
+                const int64_t row = x.row0 + c0;
+                if (res != nullptr && in && ok) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= __uint_as_float(ru[i]);
-                    }
-                    if (res != nullptr && row < x.nrows) {
-                        const T *from = res + (int64_t)(x.row0 + row) * c.residual_stride + col0 + c0;
-                        if (a.vec_res && col0 + c0 + 32 <= c.R) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                Pack<T, 8> p;
-                                p.load(from + i * 8);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) v[i * 8 + j] += p.get(j);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (col0 + c0 + i < c.R) {
-                                    Pack<T, 1> p;
-                                    p.load(from + i);
-                                    v[i] += p.get(0);
-                                }
+                    for (int i = 0; i < 32; ++i)
+                        if (i < rows) {
+                            Pack<T, 1> p;
+                            p.load(res + (row + i) * c.residual_stride + col0 + lane);
+                            v[i] += p.get(0);
                         }
-                    }
-                    // a row's 64 bytes in four pieces, their places turned by the row so that no two lanes of an access
-                    // share a bank more often than they must
-                    __syncwarp();
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) *reinterpret_cast<T *>(patch + i * 64 + lane * 2) = elem_of<T>(v[i]);
+                __syncwarp();
+                if (!ok) continue;
+                if (a.vec_y && col0 + 32 <= c.R) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        Pack<T, 8> p;
-                        const float o[8] = {v[i * 8], v[i * 8 + 1], v[i * 8 + 2], v[i * 8 + 3], v[i * 8 + 4], v[i * 8 + 5], v[i * 8 + 6], v[i * 8 + 7]};
-                        p.set(o);
-                        *reinterpret_cast<uint4 *>(patch + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = p.a;
+                        const int rr = i * 8 + (lane >> 2), q = lane & 3;
+                        const uint4 o = *reinterpret_cast<const uint4 *>(patch + rr * 64 + q * 16);
+                        if (rr < rows) *reinterpret_cast<uint4 *>(y + (row + rr) * c.y_stride + col0 + q * 8) = o;
                     }
-                    __syncwarp();
-                    if (a.vec_y && col0 + c0 + 32 <= c.R) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int rr = i * 8 + (lane >> 2), q = lane & 3;
-                            const uint4 o = *reinterpret_cast<const uint4 *>(patch + rr * 64 + ((q ^ (rr >> 1)) & 3) * 16);
-                            if (quarter * 32 + rr < x.nrows)
-                                *reinterpret_cast<uint4 *>(y + (yrow + rr) * c.y_stride + col0 + c0 + q * 8) = o;
-                        }
-                    } else if (col0 + c0 + lane < c.R) {
-                        for (int rr = 0; rr < 32 && quarter * 32 + rr < x.nrows; ++rr)
-                            y[(yrow + rr) * c.y_stride + col0 + c0 + lane] = *reinterpret_cast<const T *>(
-                                patch + rr * 64 + (((lane >> 3) ^ (rr >> 1)) & 3) * 16 + (lane & 7) * 2);
-                    }
+                } else if (in) {
+                    for (int rr = 0; rr < rows; ++rr)
+                        y[(row + rr) * c.y_stride + col0 + lane] = *reinterpret_cast<const T *>(patch + rr * 64 + lane * 2);
                 }
-                tc_fence_before();
             }
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty + buf * 8);
+            if (lane == 0) arrive_at(lead_tempty + buf * 8);
             if (++buf == 2) buf = 0, tphase ^= 1;
         }
     }
     tc_fence_before();
     __syncthreads();
+    pair_sync();  // neither CTA's barriers, shared or tensor memory are used by the other any more
     tc_fence_after();
     if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * TN) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * TILE) : "memory");
 }
 
 int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
-    const int sms = std::max(1, device_sm_count());
-    const bool pair = c.w_up != nullptr, f16 = c.dtype == MOE_DTYPE_F16;
+    const bool f16 = c.dtype == MOE_DTYPE_F16;
     Args a{};
     a.c = c;
     a.status = status;
-    auto bits = [](const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * 2)) % 16 == 0; };
-    a.vec_y = bits(c.y, c.y_stride);
-    a.vec_res = c.residual != nullptr && bits(c.residual, c.residual_stride);
-    auto go = [&](auto kernel, int tn, size_t smem, SmemOptIn *done) {
-        const int cols = pair ? tn / 2 : tn;
-        a.wtiles = (c.R + cols - 1) / cols;
-        CUtensorMap mx, mw, mu;
-        if (!encode_16bit_sw128_2d(&mx, c.x, f16, c.n_rows, c.K, c.x_stride, TM) ||
-            !encode_16bit_sw128_2d(&mw, c.w, f16, (uint64_t)c.E * c.R, c.K, c.K, cols) ||
-            !encode_16bit_sw128_2d(&mu, pair ? c.w_up : c.w, f16, (uint64_t)c.E * c.R, c.K, c.K, cols))
-            return (int)MOE_ERR_CUDA;
-        if (int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, done)) return rc;
-        const int64_t most = ((int64_t)(c.n_rows + TM - 1) / TM + (c.expStart ? c.E : 0)) * a.wtiles;
-        kernel<<<(unsigned)std::min<int64_t>(most, sms), THREADS, smem, s>>>(a, mx, mw, mu);
+    a.vec_y = (reinterpret_cast<uintptr_t>(c.y) | (uintptr_t)(c.y_stride * 2)) % 16 == 0;
+    auto go = [&](auto kernel, auto pc, SmemOptIn *done, std::atomic<int> *most_pairs) {
+        using S = Shape<decltype(pc)::value>;
+        a.wtiles = (c.R + S::COLS - 1) / S::COLS;
+        const int wbox = c.w_up != nullptr ? HALF / 2 : HALF;
+        Maps maps;
+        bool ok = encode_16bit_sw128_2d(&maps.w, c.w, f16, (uint64_t)c.E * c.R, c.K, c.K, wbox) &&
+                  encode_16bit_sw128_2d(&maps.up, c.w_up != nullptr ? c.w_up : c.w, f16, (uint64_t)c.E * c.R, c.K, c.K, wbox);
+        for (int i = 0; i < 4; ++i) ok = ok && encode_16bit_sw128_2d(&maps.x[i], c.x, f16, c.n_rows, c.K, c.x_stride, 16 << i);
+        if (!ok) return (int)MOE_ERR_CUDA;
+        if (int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), S::SMEM, done)) return rc;
+        // every pair that runs at once (not all SMs need find a partner)
+        const int dev = current_device();
+        if (dev < 0) return (int)MOE_ERR_CUDA;
+        int pairs = most_pairs[dev].load(std::memory_order_relaxed);
+        if (pairs == 0) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(2);
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = S::SMEM;
+            if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) return (int)MOE_ERR_CUDA;
+            most_pairs[dev].store(pairs, std::memory_order_relaxed);
+        }
+        // one matrix and few tiles: narrower ones, so that more SMs have one
+        a.width = TILE;
+        while (c.expStart == nullptr && a.width > 64 && (int64_t)((c.n_rows + a.width / 2 - 1) / (a.width / 2)) * a.wtiles <= pairs) a.width /= 2;
+        // token rows of a CTA's half tile, as its box brings them
+        const int half = c.expStart != nullptr ? HALF : std::min((std::min(a.width, c.n_rows) + 15) / 16 * 8, HALF);
+        int box = 16;
+        while (box < half) box *= 2;
+        a.stage = STAGE_A + box * TK * 2;
+        a.stages = std::min<int>(MAX_STAGES, (int)(RING / a.stage)) / SPAN * SPAN;
+        const int64_t most = ((int64_t)(c.n_rows + a.width - 1) / a.width + (c.expStart ? std::min(c.E, c.n_rows) : 0)) * a.wtiles;
+        kernel<<<(unsigned)(2 * std::min<int64_t>(most, pairs)), THREADS, S::SMEM, s>>>(a, maps);
         return launch_status();
     };
     auto by_type = [&](auto *tp) {
         using T = std::remove_pointer_t<decltype(tp)>;
         static SmemOptIn done[2];
-        if (pair) return go(rows16_kernel<T, 256, true>, 256, smem_bytes<256>(), &done[0]);
-        return go(rows16_kernel<T, 256, false>, 256, smem_bytes<256>(), &done[1]);
+        static std::atomic<int> pairs[2][MAX_DEVICES];
+        if (c.w_up != nullptr) return go(rows16_kernel<T, true>, std::true_type(), &done[0], pairs[0]);
+        return go(rows16_kernel<T, false>, std::false_type(), &done[1], pairs[1]);
     };
     return f16 ? by_type(static_cast<__half *>(nullptr)) : by_type(static_cast<__nv_bfloat16 *>(nullptr));
 }
@@ -525,8 +640,7 @@ int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
 }  // namespace
 
 int launch_matmul16(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
-    // 32 rows are four column tiles of the few-row kernel's instructions; beyond them it would read the weights again
-    return c.n_rows <= s16::MAX_ROWS ? few::launch(c, status, s) : rows::launch(c, status, s);
+    return few::serves(c) ? few::launch(c, status, s) : rows::launch(c, status, s);
 }
 
 }  // namespace moe

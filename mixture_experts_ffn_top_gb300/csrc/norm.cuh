@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "elem.cuh"
+#include "pair.cuh"
 
 namespace moe {
 
@@ -101,36 +102,6 @@ struct RowSum {
     }
 };
 
-// Two fp32 values in one 64-bit register: an instruction adds or multiplies both, which halves the issue slots that
-// bound these kernels beside the memory.  One value alone (V == 1) goes the same way as a float.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 pair_of(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 values_of(F2 p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
-    return r;
-}
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float mul(float a, float b) { return a * b; }
 __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }

@@ -15,8 +15,8 @@
 //      expert by expert (ascending; the shared one last), their order fixed.
 // The ring (stream16.cuh) runs on through the second barrier: the first down tiles fly while it completes.
 //
-// h enters the tensor cores as two 16-bit columns, its rounded value and the rest: 16 significant bits in bf16, at
-// least 22 in fp16, where a token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15
+// h enters the tensor cores as two 16-bit columns, its rounded value and the rest, of up to four tokens at a time:
+// 16 significant bits in bf16, at least 22 in fp16, where a token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15
 // (a fp16 h itself could overflow or vanish).
 #include <algorithm>
 
@@ -59,7 +59,8 @@ struct Lists {
     float *w;        // [entries] weight
     int *idx;        // [N][k] the routing
     float *topw;     // [N][k]
-    short *at;       // [touched + 1][8] the entry of each of up to 8 tokens, or -1
+    short *at;       // [touched + 1][4] the entry of each of up to 4 tokens, or -1
+    int *cost;       // [touched + 2] of the listed experts before (more than 8 tokens)
     __device__ Lists(char *p, int E, int N, int k) {
         const int touched = min(E, N * k) + 1, entries = N * k + N;
         mask = reinterpret_cast<unsigned *>(p);
@@ -71,11 +72,12 @@ struct Lists {
         idx = reinterpret_cast<int *>(w + entries);
         topw = reinterpret_cast<float *>(idx + N * k);
         at = reinterpret_cast<short *>(topw + N * k);
+        cost = reinterpret_cast<int *>(topw + N * k);
     }
 };
 size_t list_bytes(int E, int N, int k) {
     const size_t touched = std::min(E, N * k) + 1;
-    return (2 * E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (N <= 8 ? touched * 16 : 0);
+    return (2 * E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (touched + 1) * 8;
 }
 
 // Grid barrier of the consumer warps (a cooperative launch).  Arrivals are counted through, never reset: a call makes
@@ -193,8 +195,8 @@ __device__ __forceinline__ float h_scale(unsigned amax, bool inverse) {
     return __uint_as_float((unsigned)(127 + (inverse ? -p : p)) << 23);
 }
 
-// NTM: tiles of 8 tokens, rounded up to 1, 2 or 4.
-template <typename T, int NTM>
+// NTM: tiles of 8 tokens, rounded up to 1, 2 or 4.  PACKED: more than 4 tokens (see the down part).
+template <typename T, int NTM, bool PACKED>
 __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a) {
     constexpr bool F16 = std::is_same_v<T, __half>;
     extern __shared__ __align__(1024) char smem[];
@@ -336,19 +338,55 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         ls.tok[N * k + t] = t;
         ls.w[N * k + t] = gate_s[t];
     }
-    if (NTM == 1)
-        for (int i = tid; i < (touched_s + 1) * 8; i += THREADS) {
-            const int l = i >> 3, t = i & 7;
+    if (!PACKED)
+        for (int i = tid; i < (touched_s + 1) * 4; i += THREADS) {
+            const int l = i >> 2, t = i & 3;
             const unsigned m = l == touched_s ? (1u << N) - 1 : ls.mask[ls.expert[l]];
             ls.at[i] = (m >> t) & 1 ? (short)(ls.first[l] + __popc(m & ((1u << t) - 1))) : (short)-1;
         }
+    // An expert's tiles of weights by what they cost: the memory's share up to 16 entries, more with their products.
+    auto tile_cost = [&](int n) { return max(2, (n + 7) / 8); };
+    if (NTM > 1 && warp == 0) {
+        int before = 0;
+        for (int l0 = 0; l0 <= touched_s; l0 += 32) {
+            const int l = l0 + lane;
+            int c = 0;
+            if (l < touched_s)
+                c = tile_cost(ls.first[l + 1] - ls.first[l]) * (a.F / 8);
+            else if (l == touched_s)
+                c = tile_cost(N) * (a.Fs / 8);
+            int in = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, in, o);
+                if (lane >= o) in += v;
+            }
+            if (l <= touched_s) ls.cost[l + 1] = before + in;
+            before += __shfl_sync(0xffffffffu, in, 31);
+        }
+        if (lane == 0) ls.cost[0] = 0;
+    }
     __syncthreads();
 
     // ---- the CTA's share
     const int touched = touched_s, listed = touched + (a.Fs > 0);
     const int upe = a.F / 8;  // tiles of 8 pairs an expert
     const int64_t units = (int64_t)touched * upe + a.Fs / 8;
-    const int u0 = (int)(units * bid / G), u1 = (int)(units * (bid + 1) / G);
+    auto share = [&](int b) {  // the first tile of CTA b
+        if (NTM == 1) return (int)(units * b / G);
+        const int64_t target = (int64_t)ls.cost[touched + 1] * b / G;
+        int lo = 0, hi = touched + 1;  // the listed expert with cost[lo] <= target < cost[lo + 1], or behind the last
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ls.cost[mid] <= target)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int each = tile_cost(lo == touched ? N : ls.first[lo + 1] - ls.first[lo]);
+        return (int)min(units, (int64_t)lo * upe + (target - ls.cost[lo] + each - 1) / each);
+    };
+    const int u0 = share(bid), u1 = share(bid + 1);
     const int row0 = (int)((int64_t)D * bid / G), row1 = (int)((int64_t)D * (bid + 1) / G);
     const int row_tiles = (row1 - row0 + 15) / 16;
     const int group = consumer ? warp / GROUP_WARPS : warp - CONSUMERS;
@@ -425,101 +463,119 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         consumer_sync();
     }
 
-    // ---- down.  Up to 8 tokens: a token's column is its own throughout, the accumulators run on over the experts.
-    // More: an expert's entries are its columns, and its sums are added to the warp's rows x tokens in shared memory
-    // (most experts have a handful of entries: one tile of columns instead of four that are all but empty).
-    constexpr bool PACKED = NTM > 1;
+    // ---- down.  The columns of a product are up to 4 entries' h, rounded, and the same entries' rests.  Up to 4 tokens: a
+    // token's column is its own throughout, the accumulators run on over the experts.  More: an expert's entries are
+    // its columns, and its sums are added to the warp's rows x tokens in shared memory (most experts have a handful).
     const int gw = warp % GROUP_WARPS, own_pitch = N + 1;
     float *own = reinterpret_cast<float *>(red) + warp * 16 * own_pitch;  // PACKED: [16][own_pitch] of the warp
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto length = [&](int i) { return i == touched ? a.Fs : a.F; };
+    auto entries = [&](int i) { return i == touched ? N : ls.first[i + 1] - ls.first[i]; };
     int turn = 0;  // the stages go to the groups in turn
     for (int rt = 0; rt < row_tiles; ++rt) {
         const int r0 = row0 + (row1 - row0) * rt / row_tiles, r1 = row0 + (row1 - row0) * (rt + 1) / row_tiles;
+        consumer_sync();  // the sums before these have been read
         if (PACKED) {
-            consumer_sync();  // the sums before these have been read
             for (int j = lane; j < 16 * own_pitch; j += 32) own[j] = 0.0f;
             __syncwarp();
         }
-        // the lane's h of a stage: 8 values in 32 bytes, CHUNKS times; asked for two stages ahead
+        // a place in the group's share of the row tile's work: listed expert, column, tile of 4 entries
+        struct Place {
+            int i, k0, j, turn;
+        };
+        auto next_stage = [&](Place &p) {  // the group's next stage
+            do {
+                if ((p.k0 += a.kc) >= length(p.i)) p.k0 = 0, ++p.i;
+                p.turn = p.turn + 1 == GROUPS ? 0 : p.turn + 1;
+            } while (p.i < listed && p.turn != group);
+            p.j = 0;
+        };
+        // the lane's h of a tile, asked for a tile ahead: 8 values of the entry of its column, CHUNKS times
         struct Block {
-            uint4 a[CHUNKS], b[CHUNKS];
+            uint4 a[CHUNKS], b[F16 ? CHUNKS : 1];
             float scale;
         };
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        auto length = [&](int i) { return i == touched ? a.Fs : a.F; };
-        auto load = [&](int i, int k0, int tile, Block &f) {
-            const int cols = min(a.kc, length(i) - k0);
-            int entry = -1;
-            if (PACKED) {
-                const int j = tile * 8 + g, n = i == touched ? N : ls.first[i + 1] - ls.first[i];
-                if (j < n) entry = ls.first[i] + j;
-            } else {
-                entry = ls.at[i * 8 + g];
-            }
-            f.scale = 1.0f;
-            if (F16 && entry >= 0) f.scale = scale_s[PACKED ? ls.tok[entry] : g];
-            const char *h = static_cast<const char *>(a.h) + ((int64_t)entry * a.hs + k0 + t4 * 8) * 4;
+        auto load = [&](const Place &p, Block &f) {
+            const int cols = min(a.kc, length(p.i) - p.k0);
+            int entry = PACKED ? (p.j * 4 + (g & 3) < entries(p.i) ? ls.first[p.i] + p.j * 4 + (g & 3) : -1) : ls.at[p.i * 4 + (g & 3)];
+            if (F16) f.scale = entry >= 0 ? scale_s[ls.tok[entry]] : 1.0f;
+            const char *h = static_cast<const char *>(a.h) + ((int64_t)entry * a.hs + p.k0 + t4 * 8) * 4 + (F16 ? 0 : (g >> 2) * 16);
 #pragma unroll
             for (int q = 0; q < CHUNKS; ++q) {
                 const int c = (q * GROUP_WARPS + gw) * 32;
-                f.a[q] = f.b[q] = zero;
-                if (entry >= 0 && c + t4 * 8 < cols) {
-                    f.a[q] = __ldcg(reinterpret_cast<const uint4 *>(h + c * 4));
-                    f.b[q] = __ldcg(reinterpret_cast<const uint4 *>(h + c * 4 + 16));
-                }
+                const bool in = entry >= 0 && c + t4 * 8 < cols;
+                f.a[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4)) : zero;
+                if constexpr (F16) f.b[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4 + 16)) : zero;
             }
         };
-        auto products = [&](int cols, const Block &f, float (&hi_sum)[4], float (&lo_sum)[4]) {
+        float acc[4] = {};
+        Place at{0, 0, 0, turn}, ahead;
+        if (turn != group) next_stage(at);
+        ahead = at;
+        auto fetch = [&](Block &f) {  // and on to the tile behind it
+            if (ahead.i >= listed) return;
+            load(ahead, f);
+            if (!PACKED || ++ahead.j * 4 >= entries(ahead.i)) next_stage(ahead);
+        };
+        // one tile; false behind the last
+        auto step = [&](const Block &now, Block &then) {
+            const int K = length(at.i), cols = min(a.kc, K - at.k0), n = PACKED ? entries(at.i) : 1;
+            const bool last = (at.j + 1) * 4 >= n;
+            fetch(then);
+            if (at.j == 0) ring.wait_full();
             const char *w = ring.stage() + g * ring.pitch + t4 * 16;
 #pragma unroll
             for (int q = 0; q < CHUNKS; ++q) {
                 const int c = (q * GROUP_WARPS + gw) * 32;
                 if (c >= cols) break;
-                uint4 lo = zero, hi = zero, bh = f.a[q], bl = f.b[q];
+                uint4 lo = zero, hi = zero, b = now.a[q];
                 if (c + t4 * 8 < cols) {
                     lo = *reinterpret_cast<const uint4 *>(w + c * 2);
                     hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
                 }
-                if (F16) split8<T>(f.a[q], f.b[q], f.scale, bh, bl);
-                mma_chunk<T>(hi_sum, lo, hi, bh);
-                mma_chunk<T>(lo_sum, lo, hi, bl);
+                if constexpr (F16) {
+                    uint4 rest;
+                    split8<T>(now.a[q], now.b[q], now.scale, b, rest);
+                    if (g >= 4) b = rest;
+                }
+                mma_chunk<T>(acc, lo, hi, b);
             }
-        };
-        constexpr int TILES = PACKED ? NTM : 1;
-        float acc[TILES][4] = {}, rest[TILES][4] = {};  // of h rounded, and of the rests
-        for (int i = 0; i < listed; ++i) {
-            const int K = length(i), n = PACKED ? (i == touched ? N : ls.first[i + 1] - ls.first[i]) : 0;
-            for (int k0 = 0; k0 < K; k0 += a.kc, turn = turn + 1 == GROUPS ? 0 : turn + 1) {
-                if (turn != group) continue;
-                const int cols = min(a.kc, K - k0);
-                Block f;
-                load(i, k0, 0, f);
-                ring.wait_full();
-                products(cols, f, acc[0], rest[0]);
-#pragma unroll
-                for (int j = 1; j < TILES; ++j)
-                    if (j * 8 < n) {
-                        load(i, k0, j, f);
-                        products(cols, f, acc[j], rest[j]);
-                    }
+            if (last) {
                 ring.release(lane);
                 ring.next();
-                if (PACKED) {
+            }
+            if (PACKED) {
+                const int first = ls.first[at.i];
 #pragma unroll
-                    for (int j = 0; j < TILES; ++j)
-                        if (j * 8 < n)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int c = j * 8 + 2 * t4 + (q & 1);
-                                if (c < n) own[(g + 8 * (q >> 1)) * own_pitch + ls.tok[ls.first[i] + c]] += acc[j][q] + rest[j][q];
-                                acc[j][q] = rest[j][q] = 0.0f;
-                            }
-                    __syncwarp();
+                for (int q = 0; q < 4; ++q) {
+                    const float v = acc[q] + __shfl_xor_sync(0xffffffffu, acc[q], 2);  // the rests' column
+                    const int c = at.j * 4 + 2 * t4 + (q & 1);
+                    if (t4 < 2 && c < n) own[(g + 8 * (q >> 1)) * own_pitch + ls.tok[first + c]] += v;
+                    acc[q] = 0.0f;
                 }
+                __syncwarp();
+            }
+            if (last)
+                next_stage(at);
+            else
+                ++at.j;
+            return at.i < listed;
+        };
+        if (at.i < listed) {
+            Block b0, b1, b2;
+            fetch(b0);
+            if constexpr (F16) {  // twice the registers: a tile ahead
+                while (step(b0, b1) && step(b1, b0)) {}
+            } else {
+                fetch(b1);
+                while (step(b0, b2) && step(b1, b0) && step(b2, b1)) {}
             }
         }
+        turn = at.turn;
         if (!PACKED) {
-            const float one[1][4] = {{acc[0][0] + rest[0][0], acc[0][1] + rest[0][1], acc[0][2] + rest[0][2], acc[0][3] + rest[0][3]}};
-            consumer_sync();  // the sums before these have been read
+            float one[1][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) one[0][q] = acc[q] + __shfl_xor_sync(0xffffffffu, acc[q], 2);
             share_sums<1>(red, 1, one, warp, lane);
         }
         consumer_sync();
@@ -601,8 +657,8 @@ int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned lo
     const int ntm = c.N <= 8 ? 1 : c.N <= 16 ? 2 : 4;
     a.kc = std::min(KC, (std::max({c.D, c.F, c.Fs}) + 31) / 32 * 32);
     a.pitch = pitch_of(a.kc);
-    // the warps' sums, or with more than a tile of tokens each warp's rows x tokens
-    const size_t red = std::max((size_t)CONSUMERS * 512 * ntm, ntm == 1 ? 0 : (size_t)CONSUMERS * 64 * (c.N + 1));
+    // the warps' sums, or each warp's rows x tokens
+    const size_t red = std::max((size_t)CONSUMERS * 512 * ntm, (size_t)CONSUMERS * 64 * (c.N + 1));
     const size_t ring = (size_t)GROUPS * 16 * a.pitch, lists = list_bytes(c.E, c.N, c.top_k), most = SMEM_LIMIT - 5120;
     a.stages = (int)std::min<size_t>(MAX_STAGES, (most - red - lists) / ring);
     if (a.stages < 2) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -621,9 +677,10 @@ int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned lo
     };
     auto by_tiles = [&](auto *tp) {
         using T = std::remove_pointer_t<decltype(tp)>;
-        static SmemOptIn done[3];
-        if (ntm == 1) return go(decode16_kernel<T, 1>, &done[0]);
-        return ntm == 2 ? go(decode16_kernel<T, 2>, &done[1]) : go(decode16_kernel<T, 4>, &done[2]);
+        static SmemOptIn done[4];
+        if (c.N <= 4) return go(decode16_kernel<T, 1, false>, &done[0]);
+        if (ntm == 1) return go(decode16_kernel<T, 1, true>, &done[1]);
+        return ntm == 2 ? go(decode16_kernel<T, 2, true>, &done[2]) : go(decode16_kernel<T, 4, true>, &done[3]);
     };
     return c.dtype == MOE_DTYPE_F16 ? by_tiles(static_cast<__half *>(nullptr)) : by_tiles(static_cast<__nv_bfloat16 *>(nullptr));
 }

@@ -164,34 +164,34 @@ __device__ __forceinline__ void stream_units(Ring &ring, int64_t u0, int64_t u1,
         float acc[NTM][4] = {};
         for (int k0 = 0; k0 < K; k0 += kc) {
             const int cols = min(kc, K - k0);
-            uint4 b[CHUNKS];
+            uint4 b[NTM == 1 ? 1 : 2][CHUNKS];
+            auto fetch = [&](int n) {
 #pragma unroll
-            for (int q = 0; q < CHUNKS; ++q) {
-                const int c = (q * GROUP_WARPS + gw) * 32;
-                b[q] = zero;
-                if (c + t * 8 < cols) b[q] = *reinterpret_cast<const uint4 *>(x[0] + k0 + c);
-            }
+                for (int q = 0; q < CHUNKS; ++q) {
+                    const int c = (q * GROUP_WARPS + gw) * 32;
+                    b[n % 2][q] = zero;
+                    if (c + t * 8 < cols) b[n % 2][q] = *reinterpret_cast<const uint4 *>(x[n] + k0 + c);
+                }
+            };
+            fetch(0);
             ring.wait_full();
             const char *w = ring.stage() + g * ring.pitch + t * 16;
 #pragma unroll
-            for (int q = 0; q < CHUNKS; ++q) {
-                const int c = (q * GROUP_WARPS + gw) * 32;
-                if (c >= cols) break;
-                const bool inside = c + t * 8 < cols;
-                uint4 lo = zero, hi = zero;
-                if (inside) {
-                    lo = *reinterpret_cast<const uint4 *>(w + c * 2);
-                    hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
-                }
-                mma_chunk<T>(acc[0], lo, hi, b[q]);
+            for (int n = 0; n < NTM; ++n)
+                if (n == 0 || n < nt) {
+                    if (n + 1 < NTM && n + 1 < nt) fetch(n + 1);  // while this tile is at work
 #pragma unroll
-                for (int n = 1; n < NTM; ++n)
-                    if (n < nt) {
-                        uint4 bn = zero;
-                        if (inside) bn = *reinterpret_cast<const uint4 *>(x[n] + k0 + c);
-                        mma_chunk<T>(acc[n], lo, hi, bn);
+                    for (int q = 0; q < CHUNKS; ++q) {
+                        const int c = (q * GROUP_WARPS + gw) * 32;
+                        if (c >= cols) break;
+                        uint4 lo = zero, hi = zero;
+                        if (c + t * 8 < cols) {
+                            lo = *reinterpret_cast<const uint4 *>(w + c * 2);
+                            hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
+                        }
+                        mma_chunk<T>(acc[n], lo, hi, b[n % 2][q]);
                     }
-            }
+                }
             ring.release(lane);
             ring.next();
         }

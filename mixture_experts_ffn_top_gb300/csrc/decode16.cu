@@ -59,7 +59,7 @@ struct Lists {
     float *w;        // [entries] weight
     int *idx;        // [N][k] the routing
     float *topw;     // [N][k]
-    short *at;       // [touched + 1][4] the entry of each of up to 4 tokens, or -1
+    short *at;       // [touched + 1][8] the entry of each of up to 8 tokens, or -1
     int *cost;       // [touched + 2] of the listed experts before (more than 8 tokens)
     __device__ Lists(char *p, int E, int N, int k) {
         const int touched = min(E, N * k) + 1, entries = N * k + N;
@@ -77,7 +77,7 @@ struct Lists {
 };
 size_t list_bytes(int E, int N, int k) {
     const size_t touched = std::min(E, N * k) + 1;
-    return (2 * E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (touched + 1) * 8;
+    return (2 * E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (touched + 1) * 16;
 }
 
 // Grid barrier of the consumer warps (a cooperative launch).  Arrivals are counted through, never reset: a call makes
@@ -195,10 +195,10 @@ __device__ __forceinline__ float h_scale(unsigned amax, bool inverse) {
     return __uint_as_float((unsigned)(127 + (inverse ? -p : p)) << 23);
 }
 
-// NTM: tiles of 8 tokens, rounded up to 1, 2 or 4.  PACKED: more than 4 tokens (see the down part).
-template <typename T, int NTM, bool PACKED>
+// NTM: tiles of 8 tokens, rounded up to 1, 2 or 4.
+template <typename T, int NTM>
 __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a) {
-    constexpr bool F16 = std::is_same_v<T, __half>;
+    constexpr bool F16 = std::is_same_v<T, __half>, PACKED = NTM > 1;  // (see the down part)
     extern __shared__ __align__(1024) char smem[];
     __shared__ __align__(8) unsigned long long bars[GROUPS * 2 * MAX_STAGES + 1];
     __shared__ int abort_flag, ok_s, touched_s;
@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         ls.w[N * k + t] = gate_s[t];
     }
     if (!PACKED)
-        for (int i = tid; i < (touched_s + 1) * 4; i += THREADS) {
-            const int l = i >> 2, t = i & 3;
+        for (int i = tid; i < (touched_s + 1) * 8; i += THREADS) {
+            const int l = i >> 3, t = i & 7;
             const unsigned m = l == touched_s ? (1u << N) - 1 : ls.mask[ls.expert[l]];
             ls.at[i] = (m >> t) & 1 ? (short)(ls.first[l] + __popc(m & ((1u << t) - 1))) : (short)-1;
         }
@@ -463,14 +463,51 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         consumer_sync();
     }
 
-    // ---- down.  The columns of a product are up to 4 entries' h, rounded, and the same entries' rests.  Up to 4 tokens: a
-    // token's column is its own throughout, the accumulators run on over the experts.  More: an expert's entries are
-    // its columns, and its sums are added to the warp's rows x tokens in shared memory (most experts have a handful).
+    // ---- down.  Up to 8 tokens: a token's column is its own throughout, rounded h and rests one after the other, the
+    // accumulators run on over the experts.  More (PACKED): the columns are up to 4 of an expert's entries, rounded, and the
+    // same entries' rests, and the sums are added to the warp's rows x tokens in shared memory (most experts have a
+    // handful: one tile instead of eight that are all but empty).
     const int gw = warp % GROUP_WARPS, own_pitch = N + 1;
     float *own = reinterpret_cast<float *>(red) + warp * 16 * own_pitch;  // PACKED: [16][own_pitch] of the warp
     const uint4 zero = make_uint4(0, 0, 0, 0);
     auto length = [&](int i) { return i == touched ? a.Fs : a.F; };
-    auto entries = [&](int i) { return i == touched ? N : ls.first[i + 1] - ls.first[i]; };
+    auto count = [&](int i) { return i == touched ? N : ls.first[i + 1] - ls.first[i]; };
+    // the lane's h of a tile: 8 values of its column's entry (-1: none), CHUNKS times: fp32, or rounded and rests (a packed
+    // tile's lane needs one of them)
+    constexpr bool BOTH = F16 || !PACKED;
+    struct Block {
+        uint4 a[CHUNKS], b[BOTH ? CHUNKS : 1];
+        float scale;
+    };
+    auto load = [&](int entry, int k0, int cols, Block &f) {
+        if (F16) f.scale = entry >= 0 ? scale_s[ls.tok[entry]] : 1.0f;
+        const char *h = static_cast<const char *>(a.h) + ((int64_t)entry * a.hs + k0 + t4 * 8) * 4 + (BOTH ? 0 : (g >> 2) * 16);
+#pragma unroll
+        for (int q = 0; q < CHUNKS; ++q) {
+            const int c = (q * GROUP_WARPS + gw) * 32;
+            const bool in = entry >= 0 && c + t4 * 8 < cols;
+            f.a[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4)) : zero;
+            if constexpr (BOTH) f.b[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4 + 16)) : zero;
+        }
+    };
+    auto products = [&](int cols, const Block &f, float (&acc)[4], float (&rest_acc)[4]) {
+        const char *w = ring.stage() + g * ring.pitch + t4 * 16;
+#pragma unroll
+        for (int q = 0; q < CHUNKS; ++q) {
+            const int c = (q * GROUP_WARPS + gw) * 32;
+            if (c >= cols) break;
+            uint4 lo = zero, hi = zero, b = f.a[q];
+            if (c + t4 * 8 < cols) {
+                lo = *reinterpret_cast<const uint4 *>(w + c * 2);
+                hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
+            }
+            uint4 rest = f.b[BOTH ? q : 0];
+            if constexpr (F16) split8<T>(f.a[q], f.b[q], f.scale, b, rest);
+            if (F16 && PACKED && g >= 4) b = rest;
+            mma_chunk<T>(acc, lo, hi, b);
+            if (!PACKED) mma_chunk<T>(rest_acc, lo, hi, rest);
+        }
+    };
     int turn = 0;  // the stages go to the groups in turn
     for (int rt = 0; rt < row_tiles; ++rt) {
         const int r0 = row0 + (row1 - row0) * rt / row_tiles, r1 = row0 + (row1 - row0) * (rt + 1) / row_tiles;
@@ -479,7 +516,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             for (int j = lane; j < 16 * own_pitch; j += 32) own[j] = 0.0f;
             __syncwarp();
         }
-        // a place in the group's share of the row tile's work: listed expert, column, tile of 4 entries
         struct Place {
             int i, k0, j, turn;
         };
@@ -490,62 +526,44 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             } while (p.i < listed && p.turn != group);
             p.j = 0;
         };
-        // the lane's h of a tile, asked for a tile ahead: 8 values of the entry of its column, CHUNKS times
-        struct Block {
-            uint4 a[CHUNKS], b[F16 ? CHUNKS : 1];
-            float scale;
-        };
-        auto load = [&](const Place &p, Block &f) {
-            const int cols = min(a.kc, length(p.i) - p.k0);
-            int entry = PACKED ? (p.j * 4 + (g & 3) < entries(p.i) ? ls.first[p.i] + p.j * 4 + (g & 3) : -1) : ls.at[p.i * 4 + (g & 3)];
-            if (F16) f.scale = entry >= 0 ? scale_s[ls.tok[entry]] : 1.0f;
-            const char *h = static_cast<const char *>(a.h) + ((int64_t)entry * a.hs + p.k0 + t4 * 8) * 4 + (F16 ? 0 : (g >> 2) * 16);
-#pragma unroll
-            for (int q = 0; q < CHUNKS; ++q) {
-                const int c = (q * GROUP_WARPS + gw) * 32;
-                const bool in = entry >= 0 && c + t4 * 8 < cols;
-                f.a[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4)) : zero;
-                if constexpr (F16) f.b[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4 + 16)) : zero;
-            }
-        };
-        float acc[4] = {};
-        Place at{0, 0, 0, turn}, ahead;
+        Place at{0, 0, 0, turn};
         if (turn != group) next_stage(at);
-        ahead = at;
-        auto fetch = [&](Block &f) {  // and on to the tile behind it
-            if (ahead.i >= listed) return;
-            load(ahead, f);
-            if (!PACKED || ++ahead.j * 4 >= entries(ahead.i)) next_stage(ahead);
-        };
-        // one tile; false behind the last
-        auto step = [&](const Block &now, Block &then) {
-            const int K = length(at.i), cols = min(a.kc, K - at.k0), n = PACKED ? entries(at.i) : 1;
-            const bool last = (at.j + 1) * 4 >= n;
-            fetch(then);
-            if (at.j == 0) ring.wait_full();
-            const char *w = ring.stage() + g * ring.pitch + t4 * 16;
-#pragma unroll
-            for (int q = 0; q < CHUNKS; ++q) {
-                const int c = (q * GROUP_WARPS + gw) * 32;
-                if (c >= cols) break;
-                uint4 lo = zero, hi = zero, b = now.a[q];
-                if (c + t4 * 8 < cols) {
-                    lo = *reinterpret_cast<const uint4 *>(w + c * 2);
-                    hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
-                }
-                if constexpr (F16) {
-                    uint4 rest;
-                    split8<T>(now.a[q], now.b[q], now.scale, b, rest);
-                    if (g >= 4) b = rest;
-                }
-                mma_chunk<T>(acc, lo, hi, b);
-            }
-            if (last) {
+        if constexpr (!PACKED) {
+            float acc[4] = {}, rests[4] = {};
+            Block f;
+            auto fetch = [&](const Place &p) { load(ls.at[p.i * 8 + g], p.k0, min(a.kc, length(p.i) - p.k0), f); };
+            if (at.i < listed) fetch(at);
+            while (at.i < listed) {
+                const int cols = min(a.kc, length(at.i) - at.k0);
+                next_stage(at);
+                ring.wait_full();
+                products(cols, f, acc, rests);
+                if (at.i < listed) fetch(at);  // the next stage's, while the other group works
                 ring.release(lane);
                 ring.next();
             }
-            if (PACKED) {
-                const int first = ls.first[at.i];
+            const float one[1][4] = {{acc[0] + rests[0], acc[1] + rests[1], acc[2] + rests[2], acc[3] + rests[3]}};
+            share_sums<1>(red, 1, one, warp, lane);
+        } else {
+            float acc[4] = {};
+            Place ahead = at;
+            auto fetch = [&](Block &f) {  // and on to the tile behind it
+                if (ahead.i >= listed) return;
+                const int n = count(ahead.i), e = ahead.j * 4 + (g & 3);
+                load(e < n ? ls.first[ahead.i] + e : -1, ahead.k0, min(a.kc, length(ahead.i) - ahead.k0), f);
+                if (++ahead.j * 4 >= n) next_stage(ahead);
+            };
+            // one tile; false behind the last
+            auto step = [&](const Block &now, Block &then) {
+                const int K = length(at.i), n = count(at.i), first = ls.first[at.i];
+                const bool last = (at.j + 1) * 4 >= n;
+                fetch(then);
+                if (at.j == 0) ring.wait_full();
+                products(min(a.kc, K - at.k0), now, acc, acc);
+                if (last) {
+                    ring.release(lane);
+                    ring.next();
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float v = acc[q] + __shfl_xor_sync(0xffffffffu, acc[q], 2);  // the rests' column
@@ -554,43 +572,37 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                     acc[q] = 0.0f;
                 }
                 __syncwarp();
-            }
-            if (last)
-                next_stage(at);
-            else
-                ++at.j;
-            return at.i < listed;
-        };
-        if (at.i < listed) {
-            Block b0, b1, b2;
-            fetch(b0);
-            if constexpr (F16) {  // twice the registers: a tile ahead
-                while (step(b0, b1) && step(b1, b0)) {}
-            } else {
-                fetch(b1);
-                while (step(b0, b2) && step(b1, b0) && step(b2, b1)) {}
+                if (last)
+                    next_stage(at);
+                else
+                    ++at.j;
+                return at.i < listed;
+            };
+            if (at.i < listed) {
+                Block b0, b1, b2;
+                fetch(b0);
+                if constexpr (F16) {  // twice the registers: a tile ahead
+                    while (step(b0, b1) && step(b1, b0)) {}
+                } else {
+                    fetch(b1);
+                    while (step(b0, b2) && step(b1, b0) && step(b2, b1)) {}
+                }
             }
         }
         turn = at.turn;
-        if (!PACKED) {
-            float one[1][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) one[0][q] = acc[q] + __shfl_xor_sync(0xffffffffu, acc[q], 2);
-            share_sums<1>(red, 1, one, warp, lane);
-        }
         consumer_sync();
         if (!*reinterpret_cast<volatile int *>(&abort_flag))
             for (int j = tid; j < N * 16; j += CONSUMERS * 32) {
-                const int row = j & 15, t = j >> 4;
+                const int row = j & 15, t = j >> 4, of = row;
                 if (r0 + row >= r1) continue;
                 float v;
                 if (PACKED) {
-                    const float *p = reinterpret_cast<const float *>(red) + row * own_pitch + t;
+                    const float *p = reinterpret_cast<const float *>(red) + of * own_pitch + t;
                     v = p[0];
 #pragma unroll
                     for (int i = 1; i < CONSUMERS; ++i) v += p[i * 16 * own_pitch];
                 } else {
-                    v = sum_of<CONSUMERS>(red, 1, 0, (row & 7) * 4 + (t >> 1), (row >> 3) * 2 + (t & 1));
+                    v = sum_of<CONSUMERS>(red, 1, 0, (of & 7) * 4 + (t >> 1), (of >> 3) * 2 + (t & 1));
                 }
                 if (F16) v *= h_scale(__ldcg(a.amax + t), true);
                 if (a.residual != nullptr) {
@@ -677,10 +689,9 @@ int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned lo
     };
     auto by_tiles = [&](auto *tp) {
         using T = std::remove_pointer_t<decltype(tp)>;
-        static SmemOptIn done[4];
-        if (c.N <= 4) return go(decode16_kernel<T, 1, false>, &done[0]);
-        if (ntm == 1) return go(decode16_kernel<T, 1, true>, &done[1]);
-        return ntm == 2 ? go(decode16_kernel<T, 2, true>, &done[2]) : go(decode16_kernel<T, 4, true>, &done[3]);
+        static SmemOptIn done[3];
+        if (ntm == 1) return go(decode16_kernel<T, 1>, &done[0]);
+        return ntm == 2 ? go(decode16_kernel<T, 2>, &done[1]) : go(decode16_kernel<T, 4>, &done[2]);
     };
     return c.dtype == MOE_DTYPE_F16 ? by_tiles(static_cast<__half *>(nullptr)) : by_tiles(static_cast<__nv_bfloat16 *>(nullptr));
 }

@@ -393,26 +393,28 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     Ring ring(smem, bar, group, a.stages, a.pitch, &abort_flag, a.status);
 
     if (!consumer) {  // the group's producer
+        const Layout lay(D);
         int issued = 0, turn = 0;
         bool ok = true;
         for (int u = u0 + group; u < u1 && ok; u += GROUPS) {
-            const int i = min(u / upe, touched), e = ls.expert[i], r = (u - i * upe) * 8 + (lane & 7);
-            const T *m = static_cast<const T *>(e == E ? (lane & 8 ? a.sh_up : a.sh_gate) : (lane & 8 ? a.up : a.gate));
-            const T *src = m + ((int64_t)(e == E ? 0 : e) * a.F + r) * D;
+            const int i = min(u / upe, touched), e = ls.expert[i], r = (u - i * upe) * 8;
+            const int64_t from = ((int64_t)(e == E ? 0 : e) * a.F + r) * D;
+            const T *gate = static_cast<const T *>(e == E ? a.sh_gate : a.gate) + from;
+            const T *up = static_cast<const T *>(e == E ? a.sh_up : a.up) + from;
             for (int k0 = 0; k0 < D && ok; k0 += a.kc) {
-                ok = ring.produce(lane, lane < 16, 16, src + k0, (uint32_t)min(a.kc, D - k0) * 2);
+                ok = ring.produce(lane, lay, D, min(a.kc, D - k0), gate + k0, 8, up + k0, 8);
                 issued += ok;
             }
         }
         for (int rt = 0; rt < row_tiles && ok; ++rt) {
             const int r0 = row0 + (row1 - row0) * rt / row_tiles, r1 = row0 + (row1 - row0) * (rt + 1) / row_tiles;
             for (int i = 0; i < listed && ok; ++i) {
-                const int e = ls.expert[i], K = e == E ? a.Fs : a.F;
-                const T *src = static_cast<const T *>(e == E ? a.sh_down : a.down) +
-                               ((int64_t)(e == E ? 0 : e) * D + r0 + min(lane, r1 - r0 - 1)) * K;
+                const int e = ls.expert[i], K = e == E ? a.Fs : a.F, n = r1 - r0;
+                const T *src = static_cast<const T *>(e == E ? a.sh_down : a.down) + ((int64_t)(e == E ? 0 : e) * D + r0) * K;
+                const Layout lay(K);
                 for (int k0 = 0; k0 < K && ok; k0 += a.kc, turn = turn + 1 == GROUPS ? 0 : turn + 1) {
                     if (turn != group) continue;
-                    ok = ring.produce(lane, lane < r1 - r0, r1 - r0, src + k0, (uint32_t)min(a.kc, K - k0) * 2);
+                    ok = ring.produce(lane, lay, K, min(a.kc, K - k0), src + k0, min(n, 8), src + (int64_t)8 * K + k0, n - min(n, 8));
                     issued += ok;
                 }
             }
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         const int r = ((int)u - min((int)u / upe, touched) * upe) * 8;
         // a pair of threads a value: one adds up gate, the other up
         for (int j = thread; j < nt * 128; j += GROUP_WARPS * 32) {
-            const int is_up = j & 1, row = (j >> 1) & 7, c = j >> 4, l = row * 4 + ((c & 7) >> 1);
+            const int is_up = j & 1, row = (j >> 1) & 7, c = j >> 4, l = lane_of_row(row) * 4 + ((c & 7) >> 1);
             const float v = sum_of(s, nt, c >> 3, l, 2 * is_up + (c & 1));
             const float up = __shfl_xor_sync(0xffffffffu, v, 1);
             if (c >= in.y || is_up) continue;
@@ -490,8 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             if constexpr (BOTH) f.b[q] = in ? __ldcg(reinterpret_cast<const uint4 *>(h + c * 4 + 16)) : zero;
         }
     };
-    auto products = [&](int cols, const Block &f, float (&acc)[4], float (&rest_acc)[4]) {
-        const char *w = ring.stage() + g * ring.pitch + t4 * 16;
+    auto products = [&](const Layout &lay, int cols, const Block &f, float (&acc)[4], float (&rest_acc)[4]) {
+        const char *w = ring.stage() + lay.lane_at(g) + t4 * 16;
 #pragma unroll
         for (int q = 0; q < CHUNKS; ++q) {
             const int c = (q * GROUP_WARPS + gw) * 32;
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             uint4 lo = zero, hi = zero, b = f.a[q];
             if (c + t4 * 8 < cols) {
                 lo = *reinterpret_cast<const uint4 *>(w + c * 2);
-                hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
+                hi = *reinterpret_cast<const uint4 *>(w + 2 * lay.four + c * 2);
             }
             uint4 rest = f.b[BOTH ? q : 0];
             if constexpr (F16) split8<T>(f.a[q], f.b[q], f.scale, b, rest);
@@ -534,10 +536,10 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             auto fetch = [&](const Place &p) { load(ls.at[p.i * 8 + g], p.k0, min(a.kc, length(p.i) - p.k0), f); };
             if (at.i < listed) fetch(at);
             while (at.i < listed) {
-                const int cols = min(a.kc, length(at.i) - at.k0);
+                const int K = length(at.i), cols = min(a.kc, K - at.k0);
                 next_stage(at);
                 ring.wait_full();
-                products(cols, f, acc, rests);
+                products(Layout(K), cols, f, acc, rests);
                 if (at.i < listed) fetch(at);  // the next stage's, while the other group works
                 ring.release(lane);
                 ring.next();
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                 const bool last = (at.j + 1) * 4 >= n;
                 fetch(then);
                 if (at.j == 0) ring.wait_full();
-                products(min(a.kc, K - at.k0), now, acc, acc);
+                products(Layout(K), min(a.kc, K - at.k0), now, acc, acc);
                 if (last) {
                     ring.release(lane);
                     ring.next();
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         consumer_sync();
         if (!*reinterpret_cast<volatile int *>(&abort_flag))
             for (int j = tid; j < N * 16; j += CONSUMERS * 32) {
-                const int row = j & 15, t = j >> 4, of = row;
+                const int row = j & 15, t = j >> 4, of = lane_of_row(row & 7) + (row & 8);  // the products' row
                 if (r0 + row >= r1) continue;
                 float v;
                 if (PACKED) {

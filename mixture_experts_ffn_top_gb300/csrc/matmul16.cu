@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
     const int rows_x = first_s[listed_s];
 
     if (warp >= CONSUMERS) {
+        const Layout lay(c.K);
         int issued = 0;
         bool ok = true;
         if (a.x_pitch && group == 0) {
@@ -105,11 +106,11 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
         }
         for (int64_t u = u0 + group; u < u1 && ok; u += GROUPS) {
             const int i = (int)(u / a.tiles), r = (int)(u - (int64_t)i * a.tiles) * a.tile, n = min(a.tile, c.R - r);
-            const int l = pair ? lane & 7 : lane;
-            const T *m = static_cast<const T *>(pair && (lane & 8) ? c.w_up : c.w);
-            const T *src = m + ((int64_t)expert_s[i] * c.R + r + min(l, n - 1)) * c.K;
+            const int64_t row = (int64_t)expert_s[i] * c.R + r;
+            const T *w = static_cast<const T *>(c.w) + row * c.K, *second = pair ? static_cast<const T *>(c.w_up) + row * c.K : w + (int64_t)8 * c.K;
+            const int n0 = min(n, 8), n1 = pair ? n : n - n0;
             for (int k0 = 0; k0 < c.K && ok; k0 += a.kc) {
-                ok = ring.produce(lane, lane < 16 && l < n, pair ? 2 * n : n, src + k0, (uint32_t)min(a.kc, c.K - k0) * 2);
+                ok = ring.produce(lane, lay, c.K, min(a.kc, c.K - k0), w + k0, n0, second + k0, n1);
                 issued += ok;
             }
         }
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
         const int64_t e = expert_s[i];
         const int rl = pair ? 3 : 4;  // a unit's rows: 8 or 16
         for (int j = thread; j < nt << (rl + 3); j += GROUP_WARPS * 32) {
-            const int row = j & ((1 << rl) - 1), col = (j >> rl) & 7, tile = j >> (rl + 3), l = (row & 7) * 4 + (col >> 1);
+            const int row = j & ((1 << rl) - 1), col = (j >> rl) & 7, tile = j >> (rl + 3), l = lane_of_row(row & 7) * 4 + (col >> 1);
             if (row >= here || tile * 8 + col >= in.y) continue;
             float v[1] = {sum_of(s, nt, tile, l, (row >> 3) * 2 + (col & 1))};
             if (c.bias != nullptr) v[0] += c.bias[e * c.R + r + row];

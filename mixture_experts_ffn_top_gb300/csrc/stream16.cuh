@@ -10,7 +10,7 @@
 // A dot product does not care for the order of its columns, as long as both operands share it: lane (g, t) takes the 8
 // consecutive columns 8 t .. 8 t + 7 of a 32-wide chunk, one 16-byte access of weight row g, of row g + 8 and of
 // activation row g, and feeds them to two instructions.  Rows lie 64 bytes past a multiple of 128 apart: no bank
-// conflicts.
+// conflicts (see Layout for the weights').
 #pragma once
 
 #include "elem.cuh"
@@ -30,6 +30,27 @@ constexpr unsigned long long WAIT_NS = 1000000000ull;  // 1 s: a healthy wait ta
 
 // Row pitch in bytes of `cols` 16-bit columns.
 __host__ __device__ constexpr int pitch_of(int cols) { return (cols * 2 + 127) / 128 * 128 + 64; }
+
+// How up to 16 weight rows lie in a stage.  The copy engine takes some 45 ns a copy whatever its size, as much as 2 KB
+// take at the memory's rate: of rows up to half of that four that follow one another in memory come as one copy, longer
+// ones in pieces of KC columns, a copy each.  Row s lies at (s & 3) rows and (s >> 2) fours, and lane g reads rows
+// (g >> 1) + 4 (g & 1) and 8 more: the two rows of an access phase belong to fours an odd multiple of 64 bytes apart,
+// so that no two lanes meet in a bank.
+constexpr int KC = 1024;    // columns of a stage at most
+constexpr int FOURS = 512;  // columns of rows that come four at a time
+struct Layout {
+    int row, four;  // bytes
+    bool whole;
+    __device__ __forceinline__ explicit Layout(int K) {
+        whole = K <= FOURS;
+        row = whole ? K * 2 : (min(K, KC) + 31) / 32 * 64 + 16;
+        four = 4 * row;
+        if (four % 128 == 0) four += 64;  // (16 rows stay below 16 pitch_of(K))
+    }
+    __device__ __forceinline__ int lane_at(int g) const { return (g & 1) * four + (g >> 1) * row; }
+};
+// The lane that reads row r (0 .. 7).
+__device__ __forceinline__ int lane_of_row(int r) { return (r & 3) * 2 + (r >> 2); }
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -90,15 +111,20 @@ struct Ring {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar + (stages + slot) * 8);
     }
-    // Producer warp: the `rows` lanes with `mine` copy `bytes` from their src into the rows of their numbers.  False
-    // after a timeout.
-    __device__ __forceinline__ bool produce(int lane, bool mine, int rows, const void *src, uint32_t bytes) {
+    // Producer warp: `cols` columns of 16 rows or fewer, n0 from src0 on and, as rows 8 on, n1 from src1 on (rows K
+    // columns long).  False after a timeout.
+    template <typename T>
+    __device__ __forceinline__ bool produce(int lane, const Layout &y, int K, int cols, const T *src0, int n0, const T *src1, int n1) {
         const bool ok = __all_sync(0xffffffffu, wait_empty());
         if (!ok) return false;
         const uint32_t full = bar + slot * 8;
-        if (lane == 0) tc::mbar_expect_tx(full, bytes * rows);
+        if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)((n0 + n1) * cols * 2));
         __syncwarp();
-        if (mine) tc::bulk_load(tc::smem_u32(stage()) + lane * pitch, src, bytes, full);
+        const int s = y.whole ? lane * 4 : lane, r = s & 7;  // first row of the lane's copy
+        const int left = (s < 8 ? n0 : s < 16 ? n1 : 0) - r, rows = y.whole ? min(4, left) : min(1, left);
+        if (rows > 0)
+            tc::bulk_load(tc::smem_u32(stage()) + (s >> 2) * y.four + (s & 3) * y.row, (s < 8 ? src0 : src1) + (int64_t)r * K,
+                          (uint32_t)(rows * cols * 2), full);
         next();
         return true;
     }
@@ -122,7 +148,6 @@ __device__ __forceinline__ void init_rings(uint32_t bars, int stages) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-constexpr int KC = 1024;                             // columns of a stage at most
 constexpr int CHUNKS = KC / (GROUP_WARPS * 32);      // 32-wide chunks a warp takes of a stage
 
 // The sums of a group's warps meet in shared memory, red [GROUP_WARPS][nt][32] float4 in the accumulators' order.
@@ -154,6 +179,7 @@ __device__ __forceinline__ void stream_units(Ring &ring, int64_t u0, int64_t u1,
                                              int lane, Info info, At at, Done done) {
     const int g = lane >> 2, t = lane & 3, group = warp / GROUP_WARPS, gw = warp % GROUP_WARPS;
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    const Layout lay(K);
     float4 *sums = red + group * GROUP_WARPS * NTM * 32;
     for (int64_t u = u0 + group; u < u1; u += GROUPS) {
         const int2 in = info(u);
@@ -175,7 +201,7 @@ __device__ __forceinline__ void stream_units(Ring &ring, int64_t u0, int64_t u1,
             };
             fetch(0);
             ring.wait_full();
-            const char *w = ring.stage() + g * ring.pitch + t * 16;
+            const char *w = ring.stage() + lay.lane_at(g) + t * 16;
 #pragma unroll
             for (int n = 0; n < NTM; ++n)
                 if (n == 0 || n < nt) {
@@ -187,7 +213,7 @@ __device__ __forceinline__ void stream_units(Ring &ring, int64_t u0, int64_t u1,
                         uint4 lo = zero, hi = zero;
                         if (c + t * 8 < cols) {
                             lo = *reinterpret_cast<const uint4 *>(w + c * 2);
-                            hi = *reinterpret_cast<const uint4 *>(w + 8 * ring.pitch + c * 2);
+                            hi = *reinterpret_cast<const uint4 *>(w + 2 * lay.four + c * 2);
                         }
                         mma_chunk<T>(acc[n], lo, hi, b[n % 2][q]);
                     }

@@ -119,6 +119,7 @@ CASES = [  # N, D, E, F, k, Fs, gated, norm, residual, skew
     (32, 2048, 128, 768, 8, 0, False, True, False, 1.8), (32, 128, 4, 64, 4, 64, True, False, True, 0),
     (3, 4096, 10, 96, 2, 40, False, False, False, 0), (32, 72, 1024, 8, 32, 0, False, True, False, 0),
     (7, 1024, 300, 40, 5, 0, False, False, False, 0), (31, 5000, 5, 2056, 2, 0, False, False, False, 0), (1, 8, 3, 8, 3, 8, True, True, True, 0),
+    (8, 776, 24, 600, 4, 520, True, True, False, 0), (13, 640, 12, 1000, 3, 0, False, False, True, 0), (30, 904, 40, 520, 6, 72, False, True, False, 1.5),
     (4, 9000, 6, 16, 2, 0, False, False, False, 0), (8, 16, 33, 3000, 1, 0, False, True, False, 0),
 ]
 

@@ -112,7 +112,7 @@ SIZES = [  # E, rows, R, K
     (1, 17, 130, 72), (1, 31, 513, 256), (1, 32, 300, 4096), (1, 5, 5, 16384), (1, 20, 4000, 24), (1, 32, 40, 9000),
     (1, 33, 1, 8), (1, 33, 257, 64), (1, 100, 300, 72), (1, 128, 256, 128), (1, 129, 130, 200), (1, 1000, 520, 1032),
     (1, 257, 2047, 264), (1, 4096, 96, 2048), (1, 640, 31, 64),
-    (2, 1, 40, 64), (5, 7, 30, 416), (64, 32, 96, 1024), (1024, 30, 8, 32), (3, 32, 520, 640), (16, 2, 512, 1024),
+    (1, 8, 20000, 776), (1, 12, 9000, 520), (1, 4, 12000, 1016), (1, 6, 15000, 504), (2, 1, 40, 64), (5, 7, 30, 416), (64, 32, 96, 1024), (1024, 30, 8, 32), (3, 32, 520, 640), (16, 2, 512, 1024),
     (2, 40, 64, 256), (7, 300, 50, 128), (64, 500, 96, 512), (1024, 100, 8, 32), (1024, 5000, 24, 64), (3, 1000, 520, 640),
     (128, 4000, 130, 96), (300, 64, 20, 192),
 ]

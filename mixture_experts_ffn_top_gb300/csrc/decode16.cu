@@ -8,7 +8,7 @@
 // runs through, with two grid barriers:
 //   1. router: an expert's row at a time over the CTA's threads; barrier; every CTA routes all tokens for itself
 //      (top-k of a few tokens costs less than a third barrier) and lists the touched experts;
-//   2. gate and up: tiles of 8 gate and the same 8 up rows, the tiles of all touched experts dealt evenly;
+//   2. gate and up: tiles of 8 gate and the same 8 up rows, the tiles of all touched experts dealt in turn;
 //      h = w_s SiLU(gate) up, in fp32, to the workspace; barrier;
 //   3. down: each CTA owns some output rows and walks all touched experts over them.  The routing weight is in h, so
 //      one accumulator takes the products of every expert and no partial rows are combined afterwards: sums go
@@ -60,7 +60,6 @@ struct Lists {
     int *idx;        // [N][k] the routing
     float *topw;     // [N][k]
     short *at;       // [touched + 1][8] the entry of each of up to 8 tokens, or -1
-    int *cost;       // [touched + 2] of the listed experts before (more than 8 tokens)
     __device__ Lists(char *p, int E, int N, int k) {
         const int touched = min(E, N * k) + 1, entries = N * k + N;
         mask = reinterpret_cast<unsigned *>(p);
@@ -72,7 +71,6 @@ struct Lists {
         idx = reinterpret_cast<int *>(w + entries);
         topw = reinterpret_cast<float *>(idx + N * k);
         at = reinterpret_cast<short *>(topw + N * k);
-        cost = reinterpret_cast<int *>(topw + N * k);
     }
 };
 size_t list_bytes(int E, int N, int k) {
@@ -209,6 +207,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int N = a.N, D = a.D, E = a.E, k = a.top_k, G = gridDim.x, bid = blockIdx.x;
     const bool consumer = warp < CONSUMERS;
+    const int row0 = (int)((unsigned)D * bid / (unsigned)G), row1 = (int)((unsigned)D * (bid + 1) / (unsigned)G);
+    const int row_tiles = (row1 - row0 + 15) / 16;
     const T *x = static_cast<const T *>(a.x);
     Lists ls(smem + a.list_at, E, N, k);
     const uint32_t bar = tc::smem_u32(bars), xbar = bar + GROUPS * 2 * MAX_STAGES * 8;
@@ -344,51 +344,12 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             const unsigned m = l == touched_s ? (1u << N) - 1 : ls.mask[ls.expert[l]];
             ls.at[i] = (m >> t) & 1 ? (short)(ls.first[l] + __popc(m & ((1u << t) - 1))) : (short)-1;
         }
-    // An expert's tiles of weights by what they cost: the memory's share up to 16 entries, more with their products.
-    auto tile_cost = [&](int n) { return max(2, (n + 7) / 8); };
-    if (NTM > 1 && warp == 0) {
-        int before = 0;
-        for (int l0 = 0; l0 <= touched_s; l0 += 32) {
-            const int l = l0 + lane;
-            int c = 0;
-            if (l < touched_s)
-                c = tile_cost(ls.first[l + 1] - ls.first[l]) * (a.F / 8);
-            else if (l == touched_s)
-                c = tile_cost(N) * (a.Fs / 8);
-            int in = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, in, o);
-                if (lane >= o) in += v;
-            }
-            if (l <= touched_s) ls.cost[l + 1] = before + in;
-            before += __shfl_sync(0xffffffffu, in, 31);
-        }
-        if (lane == 0) ls.cost[0] = 0;
-    }
     __syncthreads();
 
     // ---- the CTA's share
     const int touched = touched_s, listed = touched + (a.Fs > 0);
     const int upe = a.F / 8;  // tiles of 8 pairs an expert
-    const int64_t units = (int64_t)touched * upe + a.Fs / 8;
-    auto share = [&](int b) {  // the first tile of CTA b
-        if (NTM == 1) return (int)(units * b / G);
-        const int64_t target = (int64_t)ls.cost[touched + 1] * b / G;
-        int lo = 0, hi = touched + 1;  // the listed expert with cost[lo] <= target < cost[lo + 1], or behind the last
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (ls.cost[mid] <= target)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int each = tile_cost(lo == touched ? N : ls.first[lo + 1] - ls.first[lo]);
-        return (int)min(units, (int64_t)lo * upe + (target - ls.cost[lo] + each - 1) / each);
-    };
-    const int u0 = share(bid), u1 = share(bid + 1);
-    const int row0 = (int)((int64_t)D * bid / G), row1 = (int)((int64_t)D * (bid + 1) / G);
-    const int row_tiles = (row1 - row0 + 15) / 16;
+    const int units = touched * upe + a.Fs / 8;
     const int group = consumer ? warp / GROUP_WARPS : warp - CONSUMERS;
     Ring ring(smem, bar, group, a.stages, a.pitch, &abort_flag, a.status);
 
@@ -396,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         const Layout lay(D);
         int issued = 0, turn = 0;
         bool ok = true;
-        for (int u = u0 + group; u < u1 && ok; u += GROUPS) {
+        for (int u = first_unit(group); u < units && ok; u += unit_stride()) {
             const int i = min(u / upe, touched), e = ls.expert[i], r = (u - i * upe) * 8;
             const int64_t from = ((int64_t)(e == E ? 0 : e) * a.F + r) * D;
             const T *gate = static_cast<const T *>(e == E ? a.sh_gate : a.gate) + from;
@@ -428,13 +389,13 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     const T *xb = a.x_pitch ? reinterpret_cast<const T *>(smem + a.x_at) : x;
     const int64_t xs = a.x_pitch ? a.x_pitch / 2 : a.x_stride;
     float4 *red = reinterpret_cast<float4 *>(smem + a.red_at);
-    auto info = [&](int64_t u) {
-        const int i = min((int)u / upe, touched);
+    auto info = [&](int u) {
+        const int i = min(u / upe, touched);
         return make_int2(ls.first[i], i == touched ? N : ls.first[i + 1] - ls.first[i]);
     };
     auto at = [&](int entry) { return xb + ls.tok[entry] * xs; };
-    auto done = [&](int64_t u, const int2 &in, const float4 *s, int nt, int thread) {
-        const int r = ((int)u - min((int)u / upe, touched) * upe) * 8;
+    auto done = [&](int u, const int2 &in, const float4 *s, int nt, int thread) {
+        const int r = (u - min(u / upe, touched) * upe) * 8;
         // a pair of threads a value: one adds up gate, the other up
         for (int j = thread; j < nt * 128; j += GROUP_WARPS * 32) {
             const int is_up = j & 1, row = (j >> 1) & 7, c = j >> 4, l = lane_of_row(row) * 4 + ((c & 7) >> 1);
@@ -454,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             }
         }
     };
-    stream_units<T, NTM>(ring, u0, u1, D, a.kc, red, warp, lane, info, at, done);
+    stream_units<T, NTM>(ring, units, D, a.kc, red, warp, lane, info, at, done);
     if (F16) {
         consumer_sync();
         if (tid < N) atomicMax(a.amax + tid, amax_s[tid]);

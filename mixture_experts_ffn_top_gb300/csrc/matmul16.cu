@@ -88,9 +88,8 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
         }
     }
     __syncthreads();
-    const int64_t units = (int64_t)listed_s * a.tiles;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    if (u0 == u1) return;
+    const int units = listed_s * a.tiles;
+    if ((int)blockIdx.x >= units) return;
     const int group = warp < CONSUMERS ? warp / GROUP_WARPS : warp - CONSUMERS;
     Ring ring(smem, bar, group, a.stages, a.pitch, &abort_flag, a.status);
     const int rows_x = first_s[listed_s];
@@ -104,8 +103,8 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
             __syncwarp();
             if (lane < rows_x) tc::bulk_load(tc::smem_u32(smem + a.x_at) + lane * a.x_pitch, x + lane * c.x_stride, c.K * 2, xbar);
         }
-        for (int64_t u = u0 + group; u < u1 && ok; u += GROUPS) {
-            const int i = (int)(u / a.tiles), r = (int)(u - (int64_t)i * a.tiles) * a.tile, n = min(a.tile, c.R - r);
+        for (int u = first_unit(group); u < units && ok; u += unit_stride()) {
+            const int i = u / a.tiles, r = (u - i * a.tiles) * a.tile, n = min(a.tile, c.R - r);
             const int64_t row = (int64_t)expert_s[i] * c.R + r;
             const T *w = static_cast<const T *>(c.w) + row * c.K, *second = pair ? static_cast<const T *>(c.w_up) + row * c.K : w + (int64_t)8 * c.K;
             const int n0 = min(n, 8), n1 = pair ? n : n - n0;
@@ -124,14 +123,14 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
     if (a.x_pitch) tc::mbar_wait(xbar, 0, &abort_flag, a.status, WAIT_NS);
     const T *xb = a.x_pitch ? reinterpret_cast<const T *>(smem + a.x_at) : x;
     const int64_t xs = a.x_pitch ? a.x_pitch / 2 : c.x_stride;
-    auto info = [&](int64_t u) {
-        const int i = (int)(u / a.tiles);
+    auto info = [&](int u) {
+        const int i = u / a.tiles;
         return make_int2(first_s[i], first_s[i + 1] - first_s[i]);
     };
     auto at = [&](int row) { return xb + row * xs; };
-    auto done = [&](int64_t u, const int2 &in, const float4 *s, int nt, int thread) {
+    auto done = [&](int u, const int2 &in, const float4 *s, int nt, int thread) {
         if (*reinterpret_cast<volatile int *>(&abort_flag)) return;
-        const int i = (int)(u / a.tiles), r = (int)(u - (int64_t)i * a.tiles) * a.tile, here = min(a.tile, c.R - r);
+        const int i = u / a.tiles, r = (u - i * a.tiles) * a.tile, here = min(a.tile, c.R - r);
         const int64_t e = expert_s[i];
         const int rl = pair ? 3 : 4;  // a unit's rows: 8 or 16
         for (int j = thread; j < nt << (rl + 3); j += GROUP_WARPS * 32) {
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1) few16_kernel(const Args a) {
             static_cast<T *>(c.y)[to * c.y_stride + r + row] = elem_of<T>(v[0]);
         }
     };
-    stream_units<T, NTM>(ring, u0, u1, c.K, a.kc, reinterpret_cast<float4 *>(smem + a.red_at), warp, lane, info, at, done);
+    stream_units<T, NTM>(ring, units, c.K, a.kc, reinterpret_cast<float4 *>(smem + a.red_at), warp, lane, info, at, done);
 }
 
 // Whether the rows of `c` can lie in shared memory beside the rings, and the stages of these.
@@ -199,6 +198,7 @@ int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
     a.red_at = a.x_at + (staged ? c.n_rows * a.x_pitch : 0);
     const size_t smem = a.red_at + red;
     const int64_t units = (int64_t)std::min(c.E, c.n_rows) * a.tiles;
+    if (units > 0x40000000) return MOE_ERR_UNSUPPORTED_SHAPE;
     const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
     auto go = [&](auto kernel, SmemOptIn *done) {
         if (int rc = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), most, done)) return rc;

@@ -150,6 +150,11 @@ __device__ __forceinline__ void init_rings(uint32_t bars, int stages) {
 
 constexpr int CHUNKS = KC / (GROUP_WARPS * 32);      // 32-wide chunks a warp takes of a stage
 
+// The units of a group: what is at work at a time lies side by side in memory, and every CTA gets its share of each
+// expert's, so that experts that cost more cost all of them the same.
+__device__ __forceinline__ int first_unit(int group) { return blockIdx.x + group * gridDim.x; }
+__device__ __forceinline__ int unit_stride() { return GROUPS * gridDim.x; }
+
 // The sums of a group's warps meet in shared memory, red [GROUP_WARPS][nt][32] float4 in the accumulators' order.
 template <int NTM>
 __device__ __forceinline__ void share_sums(float4 *red, int nt, const float (&acc)[NTM][4], int warp, int lane) {
@@ -167,7 +172,8 @@ __device__ __forceinline__ float sum_of(const float4 *red, int nt, int n, int l,
     return v;
 }
 
-// Tiles of weight rows ("units") u0 .. u1 - 1 times the activation rows each of them meets, K columns, kc a stage.
+// Tiles of weight rows ("units") below `units`, a group's share of them, times the activation rows each of them meets, K columns,
+// kc a stage.
 //   info(u)    {first, n}: the unit's activation rows, n <= 8 NTM of them from place `first` on
 //   at(i)      address of the activation row in place i
 //   done(u, info, sums, nt, thread)  by all threads of a group: its warps' sums of the unit's nt tiles of 8 rows (see sum_of)
@@ -175,13 +181,13 @@ __device__ __forceinline__ float sum_of(const float4 *red, int nt, int n, int l,
 // wait, the addresses) is paid by half of the warps, and the latency of the activations, asked for before the wait,
 // passes while the other group works.  red: GROUP_WARPS * NTM * 32 float4 a group.
 template <typename T, int NTM, typename Info, typename At, typename Done>
-__device__ __forceinline__ void stream_units(Ring &ring, int64_t u0, int64_t u1, int K, int kc, float4 *red, int warp,
+__device__ __forceinline__ void stream_units(Ring &ring, int units, int K, int kc, float4 *red, int warp,
                                              int lane, Info info, At at, Done done) {
     const int g = lane >> 2, t = lane & 3, group = warp / GROUP_WARPS, gw = warp % GROUP_WARPS;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const Layout lay(K);
     float4 *sums = red + group * GROUP_WARPS * NTM * 32;
-    for (int64_t u = u0 + group; u < u1; u += GROUPS) {
+    for (int u = first_unit(group); u < units; u += unit_stride()) {
         const int2 in = info(u);
         const int nt = (in.y + 7) / 8;
         const T *x[NTM];

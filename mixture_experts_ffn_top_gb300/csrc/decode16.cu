@@ -52,7 +52,6 @@ struct DecodeArgs {
 // Small arrays of a CTA, behind one another from `p` on.
 struct Lists {
     unsigned *mask;  // [E] tokens that chose an expert
-    int *pos;        // [E] its first entry
     int *expert;     // [touched + 1] the touched experts, then E: the shared one
     int *first;      // [touched + 1] their first entry
     int *tok;        // [entries] token
@@ -60,22 +59,23 @@ struct Lists {
     int *idx;        // [N][k] the routing
     float *topw;     // [N][k]
     short *at;       // [touched + 1][8] the entry of each of up to 8 tokens, or -1
+    int *pos;        // [E] an expert's first entry (more than 8 tokens)
     __device__ Lists(char *p, int E, int N, int k) {
         const int touched = min(E, N * k) + 1, entries = N * k + N;
         mask = reinterpret_cast<unsigned *>(p);
-        pos = reinterpret_cast<int *>(mask + E);
-        expert = pos + E;
+        expert = reinterpret_cast<int *>(mask + E);
         first = expert + touched;
         tok = first + touched;
         w = reinterpret_cast<float *>(tok + entries);
         idx = reinterpret_cast<int *>(w + entries);
         topw = reinterpret_cast<float *>(idx + N * k);
         at = reinterpret_cast<short *>(topw + N * k);
+        pos = reinterpret_cast<int *>(topw + N * k);
     }
 };
 size_t list_bytes(int E, int N, int k) {
     const size_t touched = std::min(E, N * k) + 1;
-    return (2 * E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (touched + 1) * 16;
+    return (E + 2 * touched + 2 * (N * k + N) + 2 * N * k) * 4 + (N <= 8 ? touched * 16 : (size_t)E * 4);
 }
 
 // Grid barrier of the consumer warps (a cooperative launch).  Arrivals are counted through, never reset: a call makes
@@ -203,7 +203,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     __shared__ unsigned amax_s[MAX_ROWS];
     __shared__ float scale_s[MAX_ROWS], gate_s[MAX_ROWS];
     __shared__ float part[2][CONSUMERS][16];
-    __shared__ int2 group_s[MAX_E / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int N = a.N, D = a.D, E = a.E, k = a.top_k, G = gridDim.x, bid = blockIdx.x;
     const bool consumer = warp < CONSUMERS;
@@ -226,49 +225,67 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     for (int e = tid; e < E; e += THREADS) ls.mask[e] = 0;
     __syncthreads();
 
-    // ---- router: two experts' rows (or the shared gate's) and eight tokens at a time
+    // ---- router: one or two experts' rows (or the shared gate's) and 8 or 16 tokens at a time
     if (consumer) {
         const int rows = E + (a.shexp_gate != nullptr);
-        int buf = 0;
-        for (int e = bid; e < rows; e += 2 * G) {
-            const int e2 = min(e + G, rows - 1);
-            const float *w0 = e < E ? a.routerW + (int64_t)e * D : a.shexp_gate;
-            const float *w1 = e2 < E ? a.routerW + (int64_t)e2 * D : a.shexp_gate;
-            for (int t0 = 0; t0 < N; t0 += 8) {
-                float acc[16] = {};
-                for (int c = tid * 4; c < D; c += CONSUMERS * 128) {
-                    const float4 u = *reinterpret_cast<const float4 *>(w0 + c), v = *reinterpret_cast<const float4 *>(w1 + c);
-                    Pack<T, 4> p[8];
+        auto router = [&](auto rc, auto tc_) {
+            constexpr int ROWS = decltype(rc)::value, TOKENS = decltype(tc_)::value, V = ROWS * TOKENS;
+            int buf = 0;
+            for (int e = bid; e < rows; e += ROWS * G) {
+                const float *w[ROWS];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j].load(x + min(t0 + j, N - 1) * a.x_stride + c);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        acc[j] = fmaf(u.w, p[j].get(3), fmaf(u.z, p[j].get(2), fmaf(u.y, p[j].get(1), fmaf(u.x, p[j].get(0), acc[j]))));
-                        acc[8 + j] = fmaf(v.w, p[j].get(3), fmaf(v.z, p[j].get(2), fmaf(v.y, p[j].get(1), fmaf(v.x, p[j].get(0), acc[8 + j]))));
-                    }
+                for (int i = 0; i < ROWS; ++i) {
+                    const int ei = min(e + i * G, rows - 1);
+                    w[i] = ei < E ? a.routerW + (int64_t)ei * D : a.shexp_gate;
                 }
-                // 16 sums over the warp: at each step a lane keeps half of its values and sends the other half
+                for (int t0 = 0; t0 < N; t0 += TOKENS) {
+                    float acc[V] = {};
+                    for (int c = tid * 4; c < D; c += CONSUMERS * 128) {
+                        float4 u[ROWS];
+                        Pack<T, 4> p[TOKENS];
 #pragma unroll
-                for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1)
+                        for (int i = 0; i < ROWS; ++i) u[i] = *reinterpret_cast<const float4 *>(w[i] + c);
 #pragma unroll
-                    for (int j = 0; j < n; ++j) {
-                        const bool up = lane & o;
-                        const float send = up ? acc[j] : acc[j + n], keep = up ? acc[j + n] : acc[j];
-                        acc[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        for (int j = 0; j < TOKENS; ++j) p[j].load(x + min(t0 + j, N - 1) * a.x_stride + c);
+#pragma unroll
+                        for (int j = 0; j < TOKENS; ++j)
+#pragma unroll
+                            for (int i = 0; i < ROWS; ++i) {
+                                float &v = acc[i * TOKENS + j];
+                                v = fmaf(u[i].w, p[j].get(3), fmaf(u[i].z, p[j].get(2), fmaf(u[i].y, p[j].get(1), fmaf(u[i].x, p[j].get(0), v))));
+                            }
                     }
-                acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
-                if (!(lane & 1)) part[buf][warp][lane >> 1] = acc[0];
-                consumer_sync();
-                const int t = t0 + (tid & 7), row = tid & 8 ? e + G : e;
-                if (tid < 16 && t < N && row < rows) {
-                    float v = part[buf][0][tid];
+                    // V sums over the warp: at each step a lane keeps half of its values and sends the other half
 #pragma unroll
-                    for (int i = 1; i < CONSUMERS; ++i) v += part[buf][i][tid];
-                    a.logits[t * (E + 1) + row] = v;
+                    for (int o = 16, n = V / 2; n > 0; o >>= 1, n >>= 1)
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            const bool up = lane & o;
+                            const float send = up ? acc[j] : acc[j + n], keep = up ? acc[j + n] : acc[j];
+                            acc[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+#pragma unroll
+                    for (int o = 16 / V; o > 0; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+                    if (lane % (32 / V) == 0) part[buf][warp][lane / (32 / V)] = acc[0];
+                    consumer_sync();
+                    const int t = t0 + tid % TOKENS, row = e + tid / TOKENS * G;
+                    if (tid < V && t < N && row < rows) {
+                        float v = part[buf][0][tid];
+#pragma unroll
+                        for (int i = 1; i < CONSUMERS; ++i) v += part[buf][i][tid];
+                        a.logits[t * (E + 1) + row] = v;
+                    }
+                    buf ^= 1;
                 }
-                buf ^= 1;
             }
-        }
+        };
+        using std::integral_constant;
+        if (rows > G)
+            router(integral_constant<int, 2>(), integral_constant<int, 8>());
+        else if (NTM == 1)
+            router(integral_constant<int, 1>(), integral_constant<int, 8>());
+        else
+            router(integral_constant<int, 1>(), integral_constant<int, 16>());
         grid_barrier(a.arrived, arrivals + G + a.extra_arrivals, a.status, a.barrier_ns, &ok_s);
     } else if (a.x_pitch && warp == CONSUMERS) {
         // there are no weights to ask for yet: a producer brings the activations in
@@ -294,57 +311,70 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         if (lane == 0) gate_s[t] = a.shexp_gate != nullptr ? __fdiv_rn(1.0f, 1.0f + expf(-__ldcg(l + E))) : 1.0f;
     }
     __syncthreads();
-    // ---- the touched experts and their entries, by expert, then token: 32 experts a warp, then the warps' totals
+    // ---- the touched experts and their entries, by expert, then token.  A thread lists its expert; how many there are
+    // before it every warp counts for itself.
     const int groups = (E + 31) / 32;
+    int listed_before = 0, entries_before = 0, next_group = 0;
     for (int gr = warp; gr < groups; gr += CONSUMERS + GROUPS) {
+        for (; next_group < gr; ++next_group) {
+            const int e = next_group * 32 + lane;
+            const unsigned m = e < E ? ls.mask[e] : 0;
+            listed_before += __popc(__ballot_sync(0xffffffffu, m != 0));
+            entries_before += __reduce_add_sync(0xffffffffu, __popc(m));
+        }
         const int e = gr * 32 + lane;
-        const unsigned m = e < E ? ls.mask[e] : 0;
-        const unsigned there = __ballot_sync(0xffffffffu, m != 0);
-        const int c = __popc(m);
-        int before = c;
+        unsigned m = e < E ? ls.mask[e] : 0;
+        const int n = listed_before + __popc(__ballot_sync(0xffffffffu, m != 0) & ((1u << lane) - 1)), c = __popc(m);
+        int in = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += v;
+            const int v = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += v;
         }
-        if (lane == 31) group_s[gr] = make_int2(__popc(there), before);
-        if (e < E) ls.pos[e] = __popc(there & ((1u << lane) - 1)) << 16 | (before - c);  // within the group
-    }
-    __syncthreads();
-    for (int e = tid; e < E; e += THREADS) {
-        int n = ls.pos[e] >> 16, at = ls.pos[e] & 0xffff;
-        for (int gr = 0; gr < e / 32; ++gr) n += group_s[gr].x, at += group_s[gr].y;
-        if (ls.mask[e] != 0) {
+        if (m != 0) {
+            int at = entries_before + in - c;
             ls.expert[n] = e;
             ls.first[n] = at;
+            if (PACKED) {
+                ls.pos[e] = at;
+            } else {
+                for (int t = 0; t < 8; ++t) ls.at[n * 8 + t] = -1;
+                for (; m != 0; m &= m - 1, ++at) {
+                    const int t = __ffs(m) - 1;
+                    int s = 0;
+                    while (ls.idx[t * k + s] != e) ++s;  // an expert in a token's mask is among its choices
+                    ls.tok[at] = t;
+                    ls.w[at] = ls.topw[t * k + s];
+                    ls.at[n * 8 + t] = (short)at;
+                }
+            }
         }
-        ls.pos[e] = at;
     }
-    if (tid == 0) {
-        int n = 0;
-        for (int gr = 0; gr < groups; ++gr) n += group_s[gr].x;
-        ls.expert[n] = E;
-        ls.first[n] = N * k;
-        touched_s = n;
+    if (warp == CONSUMERS + GROUPS - 1) {  // the shared expert, behind them
+        for (; next_group < groups; ++next_group) {
+            const int e = next_group * 32 + lane;
+            listed_before += __popc(__ballot_sync(0xffffffffu, e < E && ls.mask[e] != 0));
+        }
+        if (lane == 0) {
+            ls.expert[listed_before] = E;
+            ls.first[listed_before] = N * k;
+            touched_s = listed_before;
+        }
+        if (lane < N) {
+            ls.tok[N * k + lane] = lane;
+            ls.w[N * k + lane] = gate_s[lane];
+        }
+        if (!PACKED && lane < 8) ls.at[listed_before * 8 + lane] = lane < N ? (short)(N * k + lane) : (short)-1;
     }
     __syncthreads();
-    for (int i = tid; i < N * k; i += THREADS) {
-        const int t = i / k, e = ls.idx[i];
-        const int at = ls.pos[e] + __popc(ls.mask[e] & ((1u << t) - 1));
-        ls.tok[at] = t;
-        ls.w[at] = ls.topw[i];
-    }
-    for (int t = tid; t < N; t += THREADS) {
-        ls.tok[N * k + t] = t;
-        ls.w[N * k + t] = gate_s[t];
-    }
-    if (!PACKED)
-        for (int i = tid; i < (touched_s + 1) * 8; i += THREADS) {
-            const int l = i >> 3, t = i & 7;
-            const unsigned m = l == touched_s ? (1u << N) - 1 : ls.mask[ls.expert[l]];
-            ls.at[i] = (m >> t) & 1 ? (short)(ls.first[l] + __popc(m & ((1u << t) - 1))) : (short)-1;
+    if (PACKED) {
+        for (int i = tid; i < N * k; i += THREADS) {
+            const int t = i / k, e = ls.idx[i], at = ls.pos[e] + __popc(ls.mask[e] & ((1u << t) - 1));
+            ls.tok[at] = t;
+            ls.w[at] = ls.topw[i];
         }
-    __syncthreads();
+        __syncthreads();
+    }
 
     // ---- the CTA's share
     const int touched = touched_s, listed = touched + (a.Fs > 0);

@@ -985,14 +985,21 @@ static bool aligned16(std::initializer_list<const void *> ps) {
         if (!aligned(p, 16)) return false;
     return true;
 }
-// MOE_OK on a GB300, else the error (the kernels below use its tensor memory and clusters).
+// MOE_OK on a GB300, else the error (the kernels below use its tensor memory and clusters); asked once per device.
 static int device_check() {
-    int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return major == 10 && minor == 3 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
+    static std::atomic<int> known[MAX_DEVICES];  // 0: not asked yet, 1: a GB300, 2: another device
+    const int dev = current_device();
+    if (dev < 0) return MOE_ERR_CUDA;
+    int is = known[dev].load(std::memory_order_relaxed);
+    if (is == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        is = major == 10 && minor == 3 ? 1 : 2;
+        known[dev].store(is, std::memory_order_relaxed);
+    }
+    return is == 1 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
 }
 
 int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const void *w_up, const float *bias,

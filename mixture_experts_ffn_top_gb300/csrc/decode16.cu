@@ -522,20 +522,24 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         Place at{0, 0, 0, turn};
         if (turn != group) next_stage(at);
         if constexpr (!PACKED) {
-            float acc[4] = {}, rests[4] = {};
+            float one[1][4] = {};
             Block f;
             auto fetch = [&](const Place &p) { load(ls.at[p.i * 8 + g], p.k0, min(a.kc, length(p.i) - p.k0), f); };
             if (at.i < listed) fetch(at);
             while (at.i < listed) {
                 const int K = length(at.i), cols = min(a.kc, K - at.k0);
+                // a column without an entry stays out: 0 times a weight that is not finite
+                const short2 there = *reinterpret_cast<const short2 *>(ls.at + at.i * 8 + 2 * t4);
                 next_stage(at);
                 ring.wait_full();
+                float acc[4] = {}, rests[4] = {};
                 products(Layout(K), cols, f, acc, rests);
                 if (at.i < listed) fetch(at);  // the next stage's, while the other group works
                 ring.release(lane);
                 ring.next();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) one[0][q] += (q & 1 ? there.y : there.x) >= 0 ? acc[q] + rests[q] : 0.0f;
             }
-            const float one[1][4] = {{acc[0] + rests[0], acc[1] + rests[1], acc[2] + rests[2], acc[3] + rests[3]}};
             share_sums<1>(red, 1, one, warp, lane);
         } else {
             float acc[4] = {};

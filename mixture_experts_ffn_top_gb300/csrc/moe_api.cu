@@ -1011,7 +1011,7 @@ int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const 
     if ((bias_up && !w_up) || n_rows < 1 || x_stride < K || y_stride < R || (residual && residual_stride < 0))
         return MOE_ERR_INVALID_ARG;
     if (!expStart && E != 1) return MOE_ERR_INVALID_ARG;
-    if (E < 1 || E > MAX_E || R < 1 || (int64_t)E * R > 0x7fffffff || K < 8 || K % 8 || K > MAX_ROW || n_rows >= (1 << 30) ||
+    if (E < 1 || E > MAX_E || R < 1 || (int64_t)E * R > 0x7fffff00 || K < 8 || K % 8 || K > MAX_ROW || n_rows >= (1 << 30) ||
         x_stride > MAX_STRIDE || y_stride > MAX_STRIDE || (residual && residual_stride > MAX_STRIDE))
         return MOE_ERR_UNSUPPORTED_SHAPE;
     int rc = check_ws(ws, ws_bytes, 256);

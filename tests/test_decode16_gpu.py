@@ -121,6 +121,7 @@ CASES = [  # N, D, E, F, k, Fs, gated, norm, residual, skew
     (7, 1024, 300, 40, 5, 0, False, False, False, 0), (31, 5000, 5, 2056, 2, 0, False, False, False, 0), (1, 8, 3, 8, 3, 8, True, True, True, 0),
     (8, 776, 24, 600, 4, 520, True, True, False, 0), (13, 640, 12, 1000, 3, 0, False, False, True, 0), (30, 904, 40, 520, 6, 72, False, True, False, 1.5),
     (4, 9000, 6, 16, 2, 0, False, False, False, 0), (8, 16, 33, 3000, 1, 0, False, True, False, 0),
+    (32, 32768, 2, 16, 1, 0, False, False, False, 0), (6, 32, 2, 65536, 1, 0, False, False, True, 0), (32, 2056, 9, 24, 9, 8, False, False, False, 0),
 ]
 
 
@@ -181,6 +182,21 @@ def reference_of(clean, like):
     return ref, HALF[like.dtype] * ref.abs()
 
 
+@pytest.mark.parametrize("N", [8, 9])
+def test_weights_that_are_not_finite_reach_their_experts_tokens_only(ops, N):
+    s = layer(N, 64, 6, 16, BF16, seed=14)
+    ws = ops.new_decode_workspace(N, 64, 6, 16, 2)
+    clean = call(ops, s, 2, False, ws)
+    idx = torch.topk(s["x"].double() @ s["routerW"].double().t(), 2, dim=1).indices
+    e = int(idx[0, 0])
+    hit = (idx == e).any(dim=1)
+    assert not hit.all()
+    s["down"][e, :, 3] = float("inf")
+    s["gate"][e, 2] = float("nan")
+    out = call(ops, s, 2, False, ws)
+    assert torch.equal(out[~hit], clean[~hit]) and not torch.isfinite(out[hit]).any()
+
+
 def test_masked_experts(ops):
     """Experts whose logit is -inf are never chosen; a token with fewer finite logits than slots gives NaN nowhere else."""
     s = layer(5, 64, 12, 16, BF16, seed=5)
@@ -234,6 +250,25 @@ def test_batches_share_a_workspace_and_graphs(ops):
     y = call(ops, parts[2], 4, True, other, stream=st)
     st.synchronize()
     assert torch.equal(y, first[2])
+
+
+def test_two_calls_at_once(ops):
+    """On two streams with a workspace each, among other kernels on a third: the same bits as alone."""
+    a, b = layer(8, 1024, 16, 256, BF16, seed=15), layer(20, 512, 32, 96, F16, seed=16)
+    wa, wb = ops.new_decode_workspace(8, 1024, 16, 256, 4), ops.new_decode_workspace(20, 512, 32, 96, 4)
+    want = call(ops, a, 4, True, wa), call(ops, b, 4, True, wb)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[torch.empty_like(want[i]) for _ in range(10)] for i in range(2)]
+    busy = torch.zeros(1 << 22, device="cuda")
+    torch.cuda.synchronize()
+    for n in range(10):
+        call(ops, a, 4, True, wa, out=outs[0][n], stream=streams[0])
+        call(ops, b, 4, True, wb, out=outs[1][n], stream=streams[1])
+        with torch.cuda.stream(streams[2]):
+            busy.add_(1)
+    torch.cuda.synchronize()
+    for i, ws in enumerate((wa, wb)):
+        assert ops.moe_workspace_status(ws) == 0 and all(torch.equal(o, want[i]) for o in outs[i])
 
 
 def test_barrier_timeout(ops):

@@ -65,7 +65,7 @@ def test_matmul(lib):
                 dict(ys=31), dict(res=0x7000000, rs=-1), dict(x=0x1000008), dict(w=0x2000002), dict(up=0x6000008), dict(xs=68),
                 dict(y=0x4000001), dict(bias=0x6000002), dict(ws=0x5000080)):
         assert f(*with_(MATMUL, **bad)) == INVALID, bad
-    for bad in (dict(E=0), dict(E=1025), dict(R=0), dict(K=0), dict(K=60), dict(n=1 << 30), dict(E=1024, R=1 << 21, ys=1 << 21),
+    for bad in (dict(E=0), dict(E=1025), dict(R=0), dict(K=0), dict(K=60), dict(n=1 << 30), dict(E=1024, R=1 << 21, ys=1 << 21), dict(E=1, R=0x7fffff01, ys=1 << 31),
                 dict(xs=(1 << 30) + 8)):
         assert f(*with_(MATMUL, **bad)) == SHAPE, bad
     assert f(*with_(MATMUL, ws_bytes=255)) == SMALL

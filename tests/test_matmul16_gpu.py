@@ -222,6 +222,21 @@ def test_captured_and_on_another_stream(ops, ws):
         assert torch.equal(y, y2) and torch.equal(y, y3)
 
 
+def test_calls_at_once(ops, ws):
+    """Few rows and many, on two streams at once: the same bits as alone."""
+    w = randn((5, 700, 520), BF16, 2, 0.04)
+    xs = [randn((n, 520), BF16, 1) for n in (24, 1500)]
+    starts = [torch.tensor(offsets(5, x.shape[0], 1), dtype=torch.int32, device="cuda") for x in xs]
+    want = [ops.moe_matmul(x, w, ws, expStart=s) for x, s in zip(xs, starts)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [(i, torch.empty_like(want[i])) for _ in range(8) for i in (0, 1, 1)]
+    torch.cuda.synchronize()
+    for j, (i, y) in enumerate(outs):
+        ops.moe_matmul(xs[i], w, ws, expStart=starts[i], y=y, stream=streams[j % 3])
+    torch.cuda.synchronize()
+    assert ops.moe_workspace_status(ws) == 0 and all(torch.equal(y, want[i]) for i, y in outs)
+
+
 def test_large_offsets(ops, ws):
     """Results past 2^31 elements from the first."""
     n, R = 70000, 32768

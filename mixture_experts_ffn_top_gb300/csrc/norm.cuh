@@ -422,14 +422,30 @@ struct TileArgs {
     int rows, parts, part_units;  // rows of a tile, parts of a row and units of each
     int pitch;                    // bytes from one row to the next in shared memory
     int split_log2;               // threads on a row's units: 1 << split_log2
-    int load_bytes, store_vec;    // accesses of 16, 4 or 2 bytes; whether 4 results go out at once
+    int load_bytes;               // accesses of 16 or 4 bytes
     int chunks, step_rows, step_chunks;  // accesses a row; from one access of a thread to its next
+    uintptr_t lo[2], hi[2];       // SHIFT: where x and d_y begin and end
 };
 
-template <typename T>
-__device__ __forceinline__ void load_unit(const char *row, int u, F2 &a, F2 &b) {
+// Unit u of a row; SHIFT: of `left` columns from it on, the row `at` (even, below 16) bytes behind its place: whole words
+// are read and shifted by two bytes where need be, columns behind the end are zeros.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void load_unit(const char *row, int u, F2 &a, F2 &b, int at = 0, int left = 4) {
     Pack<T, 4> p;
-    p.load(reinterpret_cast<const T *>(row) + u * 4);
+    if constexpr (SHIFT) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(row + (at & 8)) + u;
+        const uint2 l = q[0], h = q[1];
+        const bool word = at & 4;
+        const uint32_t w0 = word ? l.y : l.x, w1 = word ? h.x : l.y, w2 = word ? h.y : h.x, how = at & 2 ? 0x5432 : 0x3210;
+        p.w[0] = __byte_perm(w0, w1, how);
+        p.w[1] = __byte_perm(w1, w2, how);
+        if (left < 4) {
+            p.w[0] &= left < 2 ? 0xffffu : 0xffffffffu;
+            p.w[1] &= left < 3 ? 0u : 0xffffu;
+        }
+    } else {
+        p.load(reinterpret_cast<const T *>(row) + u * 4);
+    }
     a = pair_of(p.get(0), p.get(1));
     b = pair_of(p.get(2), p.get(3));
 }
@@ -439,8 +455,12 @@ __device__ __forceinline__ void load_pairs(const float4 *p, F2 &a, F2 &b) {
     b = pair_of(v.z, v.w);
 }
 
-// NU: units a thread finishes.  FULL: every lane has all its units, and every thread (no conditions inside).
-template <typename T, bool RMS, int NU, int THREADS, bool FULL>
+// NU: units a thread finishes.  FULL: every lane has all its units, and every thread (no conditions inside).  SHIFT (16-bit
+// rows that do not start on 16 bytes each): a row comes in whole 16-byte pieces, as far from one in shared memory as in
+// global memory, what they hold beside it ignored (pieces that pass the ends of x or d_y come by elements), is
+// shifted into place as it is read, and its results leave as pairs that neighbouring lanes complete.  8192 x 2047 bf16:
+// by elements 155 us.
+template <typename T, bool RMS, int NU, int THREADS, bool FULL, bool SHIFT>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const TileArgs t) {
     const NormArgs &a = t.n;
     extern __shared__ __align__(16) char smem[];
@@ -454,24 +474,40 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
 
     const int load_r = tid / t.chunks, load_c = tid - load_r * t.chunks;
+    auto piece = [&](const T *row, int c, char *dst, int which) {
+        const uintptr_t from = (reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15) + c * 16, end = reinterpret_cast<uintptr_t>(row + D);
+        if (from >= end) return;
+        if (from >= t.lo[which] && from + 16 <= t.hi[which]) {
+            copy_async<16>(dst, reinterpret_cast<const void *>(from));
+        } else {
+            for (int i = 0; i < 16; i += 2)
+                if (from + i >= reinterpret_cast<uintptr_t>(row) && from + i < end)
+                    *reinterpret_cast<uint16_t *>(dst + i) = *reinterpret_cast<const uint16_t *>(from + i);
+        }
+    };
+    // how far (in bytes) a row lies behind a multiple of 16
+    const unsigned x_at = reinterpret_cast<uintptr_t>(x) & 15, x_by = (unsigned)(a.x_stride * 2) & 15;
+    const unsigned d_at = reinterpret_cast<uintptr_t>(dy) & 15, d_by = (unsigned)(a.dy_stride * 2) & 15;
     auto load = [&](int tile, int slot) {
         if (tile < tiles) {
             const int r0 = tile * R, n = min(R, a.N - r0);
             char *to = smem + slot * stage;
             for (int r = load_r, c = load_c; r < n;) {
-                const int at = c * t.load_bytes;
-                const char *px = reinterpret_cast<const char *>(x + (int64_t)(r0 + r) * a.x_stride) + at;
-                const char *pd = reinterpret_cast<const char *>(dy + (int64_t)(r0 + r) * a.dy_stride) + at;
-                char *dst = to + r * t.pitch + at;
-                if (t.load_bytes == 16) {
-                    copy_async<16>(dst, px);
-                    copy_async<16>(dst + array, pd);
-                } else if (t.load_bytes == 4) {
-                    copy_async<4>(dst, px);
-                    copy_async<4>(dst + array, pd);
+                const T *row_x = x + (int64_t)(r0 + r) * a.x_stride, *row_d = dy + (int64_t)(r0 + r) * a.dy_stride;
+                char *dst = to + r * t.pitch + c * t.load_bytes;
+                if constexpr (SHIFT) {
+                    piece(row_x, c, dst, 0);
+                    piece(row_d, c, dst + array, 1);
                 } else {
-                    *reinterpret_cast<uint16_t *>(dst) = *reinterpret_cast<const uint16_t *>(px);
-                    *reinterpret_cast<uint16_t *>(dst + array) = *reinterpret_cast<const uint16_t *>(pd);
+                    const char *px = reinterpret_cast<const char *>(row_x) + c * t.load_bytes;
+                    const char *pd = reinterpret_cast<const char *>(row_d) + c * t.load_bytes;
+                    if (t.load_bytes == 16) {
+                        copy_async<16>(dst, px);
+                        copy_async<16>(dst + array, pd);
+                    } else {
+                        copy_async<4>(dst, px);
+                        copy_async<4>(dst + array, pd);
+                    }
                 }
                 r += t.step_rows;
                 c += t.step_chunks;
@@ -480,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
         }
         copies_commit();
     };
-    if (D % 4 != 0)  // the columns behind a row's end count as zeros
+    if (!SHIFT && D % 4 != 0)  // the columns behind a row's end count as zeros
         for (int i = tid; i < TILE_STAGES * 2 * R; i += threads)
             for (int c = D; c < units * 4; ++c) reinterpret_cast<T *>(smem + i * t.pitch)[c] = elem_of<T>(0.0f);
     const int step = gridDim.x;
@@ -508,6 +544,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
     }
     for (int c = tid; c < units * 4; c += threads) gs[c] = c < D ? a.gamma[c] : 0.0f;
     const float inv = 1.0f / (float)D;
+    const bool pairs = split >= 32;  // a warp's lanes are neighbours of one row
+    const uint32_t mask = pairs ? 0xffffffffu : ((1u << split) - 1) << (lane & ~(split - 1));  // the lanes of its row
     int slot = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += step) {
         copies_wait<1>();
@@ -520,11 +558,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
             const int row = t.parts == 1 ? job : job / t.parts, part = job - row * t.parts;
             const int first = part * t.part_units, mine = min(t.part_units, units - first);  // units
             const char *xr = xs + row * t.pitch, *dr = ds + row * t.pitch;
+            const int xa = (x_at + (tile * R + row) * x_by) & 15, da = (d_at + (tile * R + row) * d_by) & 15;
             F2 v[LANE_UNITS][2], s0 = pair_of(0.0f, 0.0f), s1 = s0;
 #pragma unroll
             for (int i = 0; i < LANE_UNITS; ++i)
                 if (FULL || lane + 32 * i < mine) {
-                    load_unit<T>(xr, first + lane + 32 * i, v[i][0], v[i][1]);
+                    load_unit<T, SHIFT>(xr, first + lane + 32 * i, v[i][0], v[i][1], xa, D - (first + lane + 32 * i) * 4);
                     if constexpr (!RMS) s0 = add(s0, v[i][0]), s1 = add(s1, v[i][1]);
                 }
             float m = 0.0f;
@@ -544,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
                         d1 = pair_of(f.x, 0.0f);
                     }
                     F2 y0, y1, w0, w1;
-                    load_unit<T>(dr, u, y0, y1);
+                    load_unit<T, SHIFT>(dr, u, y0, y1, da, D - u * 4);
                     load_pairs(reinterpret_cast<const float4 *>(gs) + u, w0, w1);
                     y0 = mul(y0, w0), y1 = mul(y1, w1);
                     q0 = fma(d0, d0, q0), q1 = fma(d1, d1, q1);
@@ -589,13 +628,15 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
             load_pairs(&stat_s[row][0], minus_m, rr);
             load_pairs(&stat_s[row][1], minus_mg, minus_mgh);
             T *to = out + (int64_t)row * a.out_stride;
+            const int xa = (x_at + (tile * R + row) * x_by) & 15, da = (d_at + (tile * R + row) * d_by) & 15;
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
                 const int u = u0 + j * split;
-                if (!FULL && u >= units) break;
+                if (SHIFT ? __all_sync(mask, u >= units) : !FULL && u >= units) break;
+                const int at = SHIFT ? min(u, units - 1) : u;
                 F2 v[2], d[2];
-                load_unit<T>(xs + row * t.pitch, u, v[0], v[1]);
-                load_unit<T>(ds + row * t.pitch, u, d[0], d[1]);
+                load_unit<T, SHIFT>(xs + row * t.pitch, at, v[0], v[1], xa);
+                load_unit<T, SHIFT>(ds + row * t.pitch, at, d[0], d[1], da);  // (what stands behind the end is not stored)
                 float o[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -606,9 +647,31 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const
                     const float2 f = values_of(mul(rr, fma(h, minus_mgh, RMS ? mul(d[i], gm[e]) : fma(d[i], gm[e], minus_mg))));
                     o[2 * i] = f.x, o[2 * i + 1] = f.y;
                 }
-                if (FULL || t.store_vec) {
-                    Pack<T, 4> p;
-                    p.set(o);
+                Pack<T, 4> p;
+                p.set(o);
+                if constexpr (SHIFT) {
+                    const uint32_t next = __shfl_down_sync(mask, p.w[0], 1);
+                    // half a word off: the lane before stores the first result, this one the next lane's with its last
+                    const bool off = reinterpret_cast<uintptr_t>(to) & 2, joined = off && pairs && lane > 0;
+                    if (u * 4 + 4 <= D && (!off || pairs)) {
+                        T *q = to + u * 4;
+                        if (off) {
+                            if (!joined) q[0] = elem_of<T>(o[0]);
+                            *reinterpret_cast<uint32_t *>(q + 1) = __byte_perm(p.w[0], p.w[1], 0x5432);
+                            if (lane < 31 && u + 1 < units)
+                                *reinterpret_cast<uint32_t *>(q + 3) = __byte_perm(p.w[1], next, 0x5432);
+                            else
+                                q[3] = elem_of<T>(o[3]);
+                        } else {
+                            reinterpret_cast<uint32_t *>(q)[0] = p.w[0];
+                            reinterpret_cast<uint32_t *>(q)[1] = p.w[1];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (u * 4 + i < D && !(i == 0 && joined)) to[u * 4 + i] = elem_of<T>(o[i]);
+                    }
+                } else if (FULL || t.load_bytes == 16) {
                     p.store(to + u * 4);
                 } else {
 #pragma unroll
@@ -760,12 +823,19 @@ int launch_norm_tiles(const NormArgs &n, int load_bytes, void *scratch, cudaStre
     TileArgs t{};
     t.n = n;
     t.load_bytes = load_bytes;
-    t.store_vec = load_bytes == 16;
     const int units = (n.D + 3) / 4;
+    const bool shift = sizeof(T) == 2 && load_bytes < 16;
+    t.chunks = shift ? (n.D * 2 + 14 + 15) / 16 : n.D * (int)sizeof(T) / load_bytes;
     t.pitch = (units * 4 * (int)sizeof(T) + 15) / 16 * 16;
+    if (shift) {
+        t.load_bytes = 16;
+        t.pitch = std::max((units * 8 + 16 + 15) / 16 * 16, t.chunks * 16);
+        t.lo[0] = reinterpret_cast<uintptr_t>(n.x), t.hi[0] = t.lo[0] + ((n.N - 1) * n.x_stride + n.D) * 2;
+        t.lo[1] = reinterpret_cast<uintptr_t>(n.dy), t.hi[1] = t.lo[1] + ((n.N - 1) * n.dy_stride + n.D) * 2;
+    }
     // two CTAs of 256 threads an SM with rows up to 2048 columns, else one of 512
     const int threads = units <= 512 ? 256 : 512, nu = units <= 256 ? 1 : units <= 1024 ? 2 : 4;
-    const int budget = (threads == 512 ? 160 : 96) * 1024 / TILE_STAGES;
+    const int budget = (threads == 512 ? 160 : 97) * 1024 / TILE_STAGES;
     t.rows = 1;
     while (2 * t.rows <= TILE_ROWS && 4 * t.rows * t.pitch <= budget) t.rows *= 2;
     t.parts = 1;
@@ -773,7 +843,6 @@ int launch_norm_tiles(const NormArgs &n, int load_bytes, void *scratch, cudaStre
     t.part_units = (units + t.parts - 1) / t.parts;
     t.split_log2 = 0;
     while ((1 << t.split_log2) < std::min(units, threads)) ++t.split_log2;
-    t.chunks = n.D * (int)sizeof(T) / load_bytes;
     t.step_rows = threads / t.chunks;
     t.step_chunks = threads % t.chunks;
     const bool full = load_bytes == 16 && n.D % 4 == 0 && units == nu << t.split_log2 && t.part_units == 32 * LANE_UNITS &&
@@ -789,8 +858,11 @@ int launch_norm_tiles(const NormArgs &n, int load_bytes, void *scratch, cudaStre
     };
     auto by_full = [&](auto nc, auto tc) {
         constexpr int NU = decltype(nc)::value, THREADS = decltype(tc)::value;
-        static SmemOptIn done[2];
-        return full ? go(norm_tile_kernel<T, RMS, NU, THREADS, true>, &done[0]) : go(norm_tile_kernel<T, RMS, NU, THREADS, false>, &done[1]);
+        static SmemOptIn done[3];
+        if constexpr (sizeof(T) == 2)
+            if (shift) return go(norm_tile_kernel<T, RMS, NU, THREADS, false, true>, &done[2]);
+        return full ? go(norm_tile_kernel<T, RMS, NU, THREADS, true, false>, &done[0])
+                    : go(norm_tile_kernel<T, RMS, NU, THREADS, false, false>, &done[1]);
     };
     using std::integral_constant;
     const int rc = nu == 1          ? by_full(integral_constant<int, 1>(), integral_constant<int, 256>())

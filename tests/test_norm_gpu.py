@@ -119,6 +119,45 @@ def test_gradients(ops, N, D, pad, at, dtype, rms):
     assert torch.all(out[:, D:] == 5)
 
 
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("D", [1, 2, 3, 5, 9, 63, 126, 127, 129, 130, 255, 1000, 1027, 2046, 2048, 2050, 4099, 4381, 8191])
+def test_gradients_of_rows_at_any_place(ops, D, dtype, rms):
+    """x, d_y and d_x each at places of their own, rows an odd number of elements apart; nothing between d_x's rows is
+    touched.  Bounds as in test_gradients."""
+    N = 67 if D > 1000 else 1500
+    gamma = torch.randn(D, generator=gen(6), device="cuda")
+    ws = ops.new_norm_workspace(N, D)
+    for pads, ats in (((5, 3, 1), (1, 2, 3)), ((0, 7, 2), (0, 5, 6)), ((9, 8, 7), (7, 4, 2))):
+        x, dy = rows(N, D, dtype, 4, pads[0], ats[0]), rows(N, D, dtype, 5, pads[1], ats[1], off=0.05)
+        buf = torch.full((N * (D + pads[2]) + ats[2] + 9,), 5.0, dtype=dtype, device="cuda")
+        wide = buf[ats[2]:ats[2] + N * (D + pads[2])].view(N, D + pads[2])
+        if rms:
+            d_x, d_gamma = ops.moe_rmsnorm_grad(dy, x, gamma, EPS, ws, d_x=wide[:, :D])
+        else:
+            d_x, d_gamma, d_beta = ops.moe_layernorm_grad(dy, x, gamma, EPS, ws, d_x=wide[:, :D])
+        h, r, dm, rel, e_h = statistics(x, rms, EPS)
+        d, gm = dy.double(), gamma.double()
+        g = d * gm
+        gd = (g * h / r).abs().sum(dim=1, keepdim=True)
+        mgh, mg = (g * h).mean(dim=1, keepdim=True), torch.zeros_like(r) if rms else g.mean(dim=1, keepdim=True)
+        e_mgh = r / D * (47 * U * gd + g.abs().sum(dim=1, keepdim=True) * dm) + mgh.abs() * (rel + 2 * U)
+        inner = g - mg - h * mgh
+        tol = r * (46 * U * g.abs().mean(dim=1, keepdim=True) + h.abs() * e_mgh + mgh.abs() * e_h +
+                   4 * U * (g.abs() + mg.abs() + (h * mgh).abs())) + (r * inner).abs() * (rel + 2 * U)
+        close(d_x, r * inner, tol, dtype)
+        n_c = N / 152 + 64
+        close(d_gamma, (d * h).sum(0), (d.abs() * e_h).sum(0) + n_c * U * (d * h).abs().sum(0))
+        if not rms:
+            close(d_beta, d.sum(0), n_c * U * d.abs().sum(0))
+        assert torch.all(wide[:, D:] == 5) and torch.all(buf[:ats[2]] == 5) and torch.all(buf[-9:] == 5)
+    one = rows(1, D, dtype, 18, 0, 3)  # a row for all, between values that are not finite
+    around = torch.full((D + 32,), float("nan"), dtype=dtype, device="cuda")
+    around[5:5 + D] = one[0]
+    a = ops.moe_rmsnorm_grad(around[5:5 + D].unsqueeze(0).expand(N, D), x, gamma, EPS, ws, d_x=wide[:, :D])[0].clone()
+    assert torch.equal(a, ops.moe_rmsnorm_grad(rows(N, D, dtype, 5, 3, 1).copy_(one.expand(N, D)), x, gamma, EPS, ws, d_x=wide[:, :D])[0])
+
+
 def test_rows_far_off_centre(ops):
     """A mean of a thousand deviations, and one element a thousand times the others: the deviations keep their digits."""
     x = rows(64, 2048, F32, 7, off=1000.0)

@@ -518,6 +518,17 @@ rows16_kernel(const Args a, const __grid_constant__ Maps maps) {
 #pragma unroll 1
             for (int c0 = set * 32; c0 < x.nrows; c0 += EPI_SETS * 32) {
                 if (col0 >= c.R) break;  // the same for both warps of a pair
+                const int rows = min(32, x.nrows - c0);
+                const int64_t row = x.row0 + c0;
+                const bool add = res != nullptr && ok && !side;
+                T rv[32];  // the residual, on its way while the results are formed (or, with two of these, while one waits)
+                auto ask = [&]() {
+                    if (!add) return;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (in && i < rows) rv[i] = res[(row + i) * c.residual_stride + col0 + lane];
+                };
+                if (!PAIR) ask();
                 uint32_t r[32];
                 float v[32];
                 if (ok) {
@@ -536,6 +547,7 @@ rows16_kernel(const Args a, const __grid_constant__ Maps maps) {
                         continue;
                     }
                     activate(v, c.act);
+                    ask();
                     asm volatile("bar.sync %0, 64;" ::"r"(3 + 2 * pw) : "memory");
                     asm volatile("bar.sync %0, 64;" ::"r"(4 + 2 * pw) : "memory");
 #pragma unroll
@@ -543,23 +555,17 @@ rows16_kernel(const Args a, const __grid_constant__ Maps maps) {
                 } else {
                     activate(v, c.act);
                 }
-                const int rows = min(32, x.nrows - c0);
-                const int64_t row = x.row0 + c0;
-                if (res != nullptr && in && ok) {
+                if (add) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (i < rows) {
-                            Pack<T, 1> p;
-                            p.load(res + (row + i) * c.residual_stride + col0 + lane);
-                            v[i] += p.get(0);
-                        }
+                        if (in && i < rows) v[i] += (float)rv[i];
                 }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) *reinterpret_cast<T *>(patch + i * 64 + lane * 2) = elem_of<T>(v[i]);
-                __syncwarp();
                 if (!ok) continue;
                 if (a.vec_y && col0 + 32 <= c.R) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) *reinterpret_cast<T *>(patch + i * 64 + lane * 2) = elem_of<T>(v[i]);
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int rr = i * 8 + (lane >> 2), q = lane & 3;
@@ -567,8 +573,9 @@ rows16_kernel(const Args a, const __grid_constant__ Maps maps) {
                         if (rr < rows) *reinterpret_cast<uint4 *>(y + (row + rr) * c.y_stride + col0 + q * 8) = o;
                     }
                 } else if (in) {
-                    for (int rr = 0; rr < rows; ++rr)
-                        y[(row + rr) * c.y_stride + col0 + lane] = *reinterpret_cast<const T *>(patch + rr * 64 + lane * 2);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < rows) y[(row + i) * c.y_stride + col0 + lane] = elem_of<T>(v[i]);
                 }
             }
             tc_fence_before();

@@ -684,13 +684,16 @@ int moe_rmsnorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t
  *               decrease or pass n_rows set MOE_DEV_BAD_CSR and every row is left.
  * K a multiple of 8, at most 2^24; x and w 16-byte aligned, x_stride a multiple of 8
  * and at least K; y and the residual may lie anywhere (16-byte accesses are used
- * where they fit).  1 <= E <= 1024, 1 <= R, E * R < 2^31, 1 <= n_rows < 2^30.
+ * where they fit).  1 <= E <= 1024, 1 <= R, E * R <= 2^31 - 256, 1 <= n_rows < 2^30
+ * (MOE_ERR_UNSUPPORTED_SHAPE, as for few rows with more than 2^30 pieces of work).
  * Products are exact and summed in fp32 by the tensor cores (in an order that
  * depends on the sizes, not on the other rows' values); the epilogue is fp32,
  * its activations within 2^-18 of their values; one rounding to y's type.
- * At most 32 rows run on a kernel made for few rows, which reads each touched
- * expert's weights once; more rows on tiles of 128.  A row's NaN stays its own.
- *   ws: status word (256 bytes). */
+ * Few rows (at most 32 over experts; of one matrix 8, or up to 32 that fit beside the
+ * weights in shared memory) run on a kernel that reads each touched expert's weights
+ * once; more rows on tensor-core tiles of 256 weight rows x up to 256 rows.  What a
+ * row holds reaches its own result only, what an expert's weights hold its own rows.
+ *   ws: status word (256 bytes); calls on several streams may share it. */
 enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
 
 int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const void *w_up, const float *bias,
@@ -714,13 +717,16 @@ int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const 
  * E <= 1024, 1 <= N <= 32.
  * Sums are fp32; SiLU(gate) * up enters the second product with 16 significant bits
  * (bf16) or 22 and more (fp16); one rounding to out's type.  The order of the sums is
- * fixed for given sizes and device.  A NaN or infinite logit makes its own token's
- * row NaN.
+ * fixed for given sizes and device.  An expert whose logit is -inf is not chosen while
+ * others are left; a NaN or +inf logit, or SiLU(gate) * up that is not finite, makes its
+ * own token's row NaN.  Weights that are not finite reach their experts' tokens only.
  * The kernel takes every SM (a cooperative launch with two grid barriers, each wait
  * limited to a second: MOE_DEV_TIMEOUT, after which out is undefined and
  * moe_workspace_init comes before the next call).
- *   ws: moe_decode_workspace_size bytes, 256-byte aligned, initialised once by
- *   moe_workspace_init; two calls that may overlap must not share one. */
+ *   ws: moe_decode_workspace_size bytes (of N tokens, or more), 256-byte aligned,
+ *   initialised once by moe_workspace_init (its status block holds the barriers' 64-bit
+ *   arrival count, which runs on from call to call); calls that may overlap, captured
+ *   ones among them, must not share one.  A workspace stays on its device. */
 size_t moe_decode_workspace_size(int N, int D, int E, int F, int top_k, int Fs);
 int moe_ffn_decode(const void *x, int64_t x_stride, int dtype, const float *routerW, const float *shexp_gate,
                    const void *gate, const void *up, const void *down, const void *sh_gate, const void *sh_up,

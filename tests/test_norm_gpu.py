@@ -119,6 +119,24 @@ def test_gradients(ops, N, D, pad, at, dtype, rms):
     assert torch.all(out[:, D:] == 5)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("D", [1, 2, 3, 7, 62, 127, 129, 255, 1000, 1027, 2046, 2048, 4381, 8191])
+def test_layernorm_of_rows_at_any_place(ops, D, dtype):
+    """x and y each at places of their own, many rows; nothing between y's rows is touched.  Bounds as in test_layernorm."""
+    N = 1300
+    gamma, beta = torch.randn(D, generator=gen(2), device="cuda"), torch.randn(D, generator=gen(3), device="cuda")
+    for pads, ats, b in (((5, 1), (1, 3), beta), ((0, 2), (0, 6), None), ((9, 8), (7, 2), beta)):
+        x = rows(N, D, dtype, 4, pads[0], ats[0])
+        buf = torch.full((N * (D + pads[1]) + ats[1] + 9,), 5.0, dtype=dtype, device="cuda")
+        wide = buf[ats[1]:ats[1] + N * (D + pads[1])].view(N, D + pads[1])
+        y = ops.moe_layernorm(x, gamma, b, EPS, y=wide[:, :D])
+        h, r, dm, rel, e_h = statistics(x, False, EPS)
+        ref = h * gamma.double() + (0 if b is None else b.double())
+        tol = gamma.double().abs() * e_h + 2 * U * ((h * gamma.double()).abs() + (0 if b is None else b.double().abs()))
+        close(y, ref, tol, dtype)
+        assert torch.all(wide[:, D:] == 5) and torch.all(buf[:ats[1]] == 5) and torch.all(buf[-9:] == 5)
+
+
 @pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
 @pytest.mark.parametrize("D", [1, 2, 3, 5, 9, 63, 126, 127, 129, 130, 255, 1000, 1027, 2046, 2048, 2050, 4099, 4381, 8191])

@@ -229,21 +229,24 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     for (int e = tid; e < E; e += THREADS) ls.mask[e] = 0;
     __syncthreads();
 
-    // ---- router: one or two experts' rows (or the shared gate's) and 8 or 16 tokens at a time: two rows where a CTA has
-    // two, so that both share the tokens' loads; 16 tokens where there are more than 8 (one token 40 to 36 us)
+    // ---- router: an expert's row (or the shared gate's) and 8 tokens at a time, 16 where 8 would take more rounds; two rows
+    // where a CTA has two, so that both share the tokens' loads (one token 40 to 36 us).  Few rows: a CTA takes some of
+    // the tokens instead of all (32 tokens, 32 rows of 4096 and as many experts of 512: 115 to 109 us).
     if (consumer) {
         const int rows = E + (a.shexp_gate != nullptr);
         auto router = [&](auto rc, auto tc_) {
             constexpr int ROWS = decltype(rc)::value, TOKENS = decltype(tc_)::value, V = ROWS * TOKENS;
             int buf = 0;
-            for (int e = bid; e < rows; e += ROWS * G) {
+            const int token_groups = ROWS == 1 ? (N + TOKENS - 1) / TOKENS : 1;
+            for (int u = bid; u < rows * token_groups; u += ROWS * G) {
+                const int e = ROWS == 1 ? u % rows : u, first = u / rows * TOKENS, last = ROWS == 1 ? first + 1 : N;
                 const float *w[ROWS];
 #pragma unroll
                 for (int i = 0; i < ROWS; ++i) {
                     const int ei = min(e + i * G, rows - 1);
                     w[i] = ei < E ? a.routerW + (int64_t)ei * D : a.shexp_gate;
                 }
-                for (int t0 = 0; t0 < N; t0 += TOKENS) {
+                for (int t0 = first; t0 < last; t0 += TOKENS) {
                     float acc[V] = {};
                     for (int c = tid * 4; c < D; c += CONSUMERS * 128) {
                         float4 u[ROWS];
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         using std::integral_constant;
         if (rows > G)
             router(integral_constant<int, 2>(), integral_constant<int, 8>());
-        else if (NTM == 1)
+        else if (NTM == 1 || rows * ((N + 7) / 8) <= G)
             router(integral_constant<int, 1>(), integral_constant<int, 8>());
         else
             router(integral_constant<int, 1>(), integral_constant<int, 16>());

@@ -14,14 +14,14 @@
 //      one accumulator takes the products of every expert and no partial rows are combined afterwards: sums go
 //      expert by expert (ascending; the shared one last), their order fixed.
 // The rings (stream16.cuh) run on through the second barrier: the first down tiles fly while it completes.
-// bf16, 64 experts of 1024 x 2048, top 8: one token 30 us (floor 14.9), eight tokens 95 us (82% of the copy rate); 32 tokens
-// over 128 experts of 768 some of which are ahead 99 us (94%).  Of eight tokens' time the router takes 3.3 us, the first barrier
-// 1.3, routing and lists 4.1, gate and up 55, the second barrier 4 to 5, down 30: what is left above the bytes are the 9 us
-// in which no weights fly and the barrier's wait for the slowest CTA.
+// bf16, 64 experts of 1024 x 2048, top 8: one token 30 us (floor 14.9), eight tokens 95 us (82% of the copy rate); 32
+// tokens over 128 experts of 768 some of which are ahead 99 us (94%).  Of eight tokens' time the router takes 3.3 us,
+// the first barrier 1.3, routing and lists 4.1, gate and up 55, the second barrier 4 to 5, down 30: what is left above
+// the bytes are the 9 us in which no weights fly and the barrier's wait for the slowest CTA.
 //
-// h enters the tensor cores as two 16-bit columns, its rounded value and the rest: 16 significant bits in bf16, at least 22
-// in fp16, where a token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15 (a fp16 h itself
-// could overflow or vanish).
+// h enters the tensor cores as two 16-bit columns, its rounded value and the rest: 16 significant bits in bf16, at
+// least 22 in fp16, where a token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15 (a
+// fp16 h itself could overflow or vanish).
 #include <algorithm>
 
 #include "stream16.cuh"
@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     for (int e = tid; e < E; e += THREADS) ls.mask[e] = 0;
     __syncthreads();
 
-    // ---- router: an expert's row (or the shared gate's) and 8 tokens at a time, 16 where 8 would take more rounds; two rows
-    // where a CTA has two, so that both share the tokens' loads (one token 40 to 36 us).  Few rows: a CTA takes some of
-    // the tokens instead of all (32 tokens, 32 rows of 4096 and as many experts of 512: 115 to 109 us).
+    // ---- router: an expert's row (or the shared gate's) and 8 tokens at a time, 16 where 8 would take more rounds;
+    // two rows where a CTA has two, so that both share the tokens' loads (one token 40 to 36 us).  Few rows: a CTA
+    // takes some of the tokens instead of all (32 tokens, 32 rows of 4096 and as many experts of 512: 115 to 109 us).
     if (consumer) {
         const int rows = E + (a.shexp_gate != nullptr);
         auto router = [&](auto rc, auto tc_) {
@@ -465,16 +465,16 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     }
 
     // ---- down.  Up to 8 tokens: a token's column is its own throughout, rounded h and rests one after the other, the
-    // accumulators run on over the experts.  More (PACKED): the columns are up to 4 of an expert's entries, rounded, and the
-    // same entries' rests, and the sums are added to the warp's rows x tokens in shared memory (most experts have a
-    // handful: one tile instead of eight that are all but empty).
+    // accumulators run on over the experts.  More (PACKED): the columns are up to 4 of an expert's entries, rounded,
+    // and the same entries' rests, and the sums are added to the warp's rows x tokens in shared memory (most experts
+    // have a handful: one tile instead of eight that are all but empty).
     const int gw = warp % GROUP_WARPS, own_pitch = N + 1;
     float *own = reinterpret_cast<float *>(red) + warp * 16 * own_pitch;  // PACKED: [16][own_pitch] of the warp
     const uint4 zero = make_uint4(0, 0, 0, 0);
     auto length = [&](int i) { return i == touched ? a.Fs : a.F; };
     auto count = [&](int i) { return i == touched ? N : ls.first[i + 1] - ls.first[i]; };
-    // the lane's h of a tile: 8 values of its column's entry (-1: none), CHUNKS times: fp32, or rounded and rests (a packed
-    // tile's lane needs one of them)
+    // the lane's h of a tile: 8 values of its column's entry (-1: none), CHUNKS times: fp32, or rounded and rests (a
+    // packed tile's lane needs one of them)
     constexpr bool BOTH = F16 || !PACKED;
     struct Block {
         uint4 a[CHUNKS], b[BOTH ? CHUNKS : 1];

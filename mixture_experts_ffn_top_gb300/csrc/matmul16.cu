@@ -3,21 +3,22 @@
 //   y[j] = act(W[e] x[j] + b[e]) (* (U[e] x[j] + c[e])) (+ residual[j])
 //
 // Two kernels.  Few rows (serving, see few::serves): every weight is read for a few rows, so its bytes bound the
-// product; few16_kernel streams them as stream16.cuh says (8 x 32768 x 4096: 45 us, 6.0 TB/s, 89% of a copy).  More rows
-// (prompts, training): rows16_kernel forms tiles of 256 weight rows (gate and up: 128 of each) on the tensor cores.
+// product; few16_kernel streams them as stream16.cuh says (8 x 32768 x 4096: 45 us, 6.0 TB/s, 89% of a copy).  More
+// rows (prompts, training): rows16_kernel forms tiles of 256 weight rows (gate and up: 128 of each) on the tensor
+// cores.
 //
 // rows16_kernel is persistent; two CTAs of a cluster work as a pair: the weights are the 256 rows of their products
 // (tcgen05.mma cta_group::2, 128 rows a CTA), up to 256 token rows the columns, in steps of 16, so that ragged segments
-// cost what they hold.  Warps in roles: in each CTA a producer that brings its 128 weight rows and its half of the token
-// rows in by TMA (128-byte swizzle, 64 columns a stage, six stages), in the first an issuer of the products (accumulators
-// in tensor memory, two tiles of 256 columns so that the next tile's products run under this one's epilogue), in each
-// twelve epilogue warps (a lane holds a weight row's results for 32 tokens; where 16-byte accesses fit they cross shared
-// memory so that rows leave in whole sectors).  Sharing the token rows between the CTAs is what lets shared memory keep
-// up: alone, a CTA's products would read 96 bytes a cycle while its copies write 94.  Segments start at any row: a tile
-// reads past its segment's end and stores nothing of what it finds there.
+// cost what they hold.  Warps in roles: in each CTA a producer that brings its 128 weight rows and its half of the
+// token rows in by TMA (128-byte swizzle, 64 columns a stage, six stages), in the first an issuer of the products
+// (accumulators in tensor memory, two tiles of 256 columns so that the next tile's products run under this one's
+// epilogue), in each twelve epilogue warps (a lane holds a weight row's results for 32 tokens; where 16-byte accesses
+// fit they cross shared memory so that rows leave in whole sectors).  Sharing the token rows between the CTAs is what
+// lets shared memory keep up: alone, a CTA's products would read 96 bytes a cycle while its copies write 94.  Segments
+// start at any row: a tile reads past its segment's end and stores nothing of what it finds there.
 // bf16, 8192 x 8192 x 2048: 147 us, 1.87 PFLOP/s (with bias and GELU 154), the tensor pipe active in 90% of the cycles;
-// gate and up of 64 experts of 1024 x 2048 over 16384 rows 118 us, 5.4 TB/s and 55% of the pipe: a wave of tiles asks for
-// its weights all at once, and half of the experts have a few rows more than a tile holds.
+// gate and up of 64 experts of 1024 x 2048 over 16384 rows 118 us, 5.4 TB/s and 55% of the pipe: a wave of tiles asks
+// for its weights all at once, and half of the experts have a few rows more than a tile holds.
 #include <algorithm>
 #include <atomic>
 
@@ -173,9 +174,10 @@ size_t red_bytes(int n_rows) { return (size_t)CONSUMERS * tiles_of(n_rows) * 512
 int columns(int K) { return std::min(KC, (K + 31) / 32 * 32); }
 
 // The rows this kernel serves: 32 are four column tiles of its instructions, and beyond them it would read the weights
-// again.  Of one matrix 8, or all that can lie in shared memory: rows that every unit of weights fetches from L2 cost as
-// much as these.  In us, here and on tiles: 16 x 2048 x 2048 11.4 and 15.5, 32 of them 15.5 and 15.5, 16 x 16384 x 2048
-// 21.7 and 19.6; not in shared memory 32 x 16384 x 2048 38 and 20, 16 x 8192 x 8192 38 and 34, 32 of them 65 and 34.
+// again.  Of one matrix 8, or all that can lie in shared memory: rows that every unit of weights fetches from L2 cost
+// as much as these.  In us, here and on tiles: 16 x 2048 x 2048 11.4 and 15.5, 32 of them 15.5 and 15.5, 16 x 16384 x
+// 2048 21.7 and 19.6; not in shared memory 32 x 16384 x 2048 38 and 20, 16 x 8192 x 8192 38 and 34, 32 of them 65 and
+// 34.
 bool serves(const Matmul16Call &c) {
     int stages;
     if (c.n_rows > MAX_ROWS) return false;
@@ -306,8 +308,8 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {  // arrives in both 
                  "h"((uint16_t)3)
                  : "memory");
 }
-// (Release at the CTA's scope: what it hands back is tensor memory, read behind tcgen05's own fence; a wider release would
-// wait for the results' stores.)
+// (Release at the CTA's scope: what it hands back is tensor memory, read behind tcgen05's own fence; a wider release
+// would wait for the results' stores.)
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -390,11 +392,12 @@ rows16_kernel(const Args a, const __grid_constant__ Maps maps) {
     if (bad && blockIdx.x == 0 && tid == 0) atomicOr(a.status, MOE_DEV_BAD_CSR);
     const int64_t items = bad ? 0 : (int64_t)item_s[nE] * a.wtiles;
     // a wait in the thread that issues products costs it some 300 cycles of issue time, more than half of a stage's
-    // products: it waits once for SPAN stages (an odd one out is followed by one without copies), which are released one by one
+    // products: it waits once for SPAN stages (an odd one out is followed by one without copies), which are released
+    // one by one
     const int spans = (c.K + SPAN * TK - 1) / (SPAN * TK);
     const int64_t first = blockIdx.x / 2, stride = gridDim.x / 2;
-    // item: expert by expert, RASTER row tiles at a time, weight tile by weight tile, the row tiles of one beside each other
-    // (the pairs at work share weights and rows about evenly).
+    // item: expert by expert, RASTER row tiles at a time, weight tile by weight tile, the row tiles of one beside each
+    // other (the pairs at work share weights and rows about evenly).
     // An expert's rows are dealt evenly to its row tiles: the product's width follows them in steps of 16.
     auto item_at = [&](int64_t it) {
         int lo = 0, hi = nE;  // the expert with item_s[e] * wtiles <= it < item_s[e + 1] * wtiles
@@ -624,8 +627,8 @@ int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
             if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) return (int)MOE_ERR_CUDA;
             most_pairs[dev].store(pairs, std::memory_order_relaxed);
         }
-        // one matrix and few tiles: narrower ones, so that more SMs have one (256 to 1024 rows x 2048 x 2048 17 us, with whole
-        // tiles 22; nothing changes from 2048 x 4096 x 2048 on)
+        // one matrix and few tiles: narrower ones, so that more SMs have one (256 to 1024 rows x 2048 x 2048 17 us,
+        // with whole tiles 22; nothing changes from 2048 x 4096 x 2048 on)
         a.width = TILE;
         while (c.expStart == nullptr && a.width > 64 && (int64_t)((c.n_rows + a.width / 2 - 1) / (a.width / 2)) * a.wtiles <= pairs) a.width /= 2;
         // token rows of a CTA's half tile, as its box brings them

@@ -427,8 +427,8 @@ struct TileArgs {
     uintptr_t lo[2], hi[2];       // SHIFT: where x and d_y begin and end
 };
 
-// Unit u of a row; SHIFT: of `left` columns from it on, the row `at` (even, below 16) bytes behind its place: whole words
-// are read and shifted by two bytes where need be, columns behind the end are zeros.
+// Unit u of a row; SHIFT: of `left` columns from it on, the row `at` (even, below 16) bytes behind its place: whole
+// words are read and shifted by two bytes where need be, columns behind the end are zeros.
 template <typename T, bool SHIFT>
 __device__ __forceinline__ void load_unit(const char *row, int u, F2 &a, F2 &b, int at = 0, int left = 4) {
     Pack<T, 4> p;
@@ -455,11 +455,11 @@ __device__ __forceinline__ void load_pairs(const float4 *p, F2 &a, F2 &b) {
     b = pair_of(v.z, v.w);
 }
 
-// NU: units a thread finishes.  FULL: every lane has all its units, and every thread (no conditions inside).  SHIFT (16-bit
-// rows an odd number of elements apart, or at odd places): a row comes in whole 16-byte pieces, as far from one in shared memory as in
-// global memory, what they hold beside it ignored (pieces that pass the ends of x or d_y come by elements), is
-// shifted into place as it is read, and its results leave as pairs that neighbouring lanes complete.  8192 x 2047 bf16
-// 51 us, by elements 148 (rows on 4 bytes, copied and stored 4 bytes at a time, need no shifting).
+// NU: units a thread finishes.  FULL: every lane has all its units, and every thread (no conditions inside).  SHIFT
+// (16-bit rows an odd number of elements apart, or at odd places): a row comes in whole 16-byte pieces, as far from one
+// in shared memory as in global memory, what they hold beside it ignored (pieces that pass the ends of x or d_y come by
+// elements), is shifted into place as it is read, and its results leave as pairs that neighbouring lanes complete. 
+// 8192 x 2047 bf16 51 us, by elements 148 (rows on 4 bytes, copied and stored 4 bytes at a time, need no shifting).
 template <typename T, bool RMS, int NU, int THREADS, bool FULL, bool SHIFT>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) norm_tile_kernel(const TileArgs t) {
     const NormArgs &a = t.n;

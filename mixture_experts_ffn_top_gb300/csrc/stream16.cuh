@@ -3,12 +3,12 @@
 //
 // Such products read every weight once, so the bytes bound them.  A CTA's two groups of eight warps have a ring and a
 // producer warp each, which asks for tiles of up to 16 weight rows x KC columns by bulk copies as far ahead as the ring
-// reaches (some 200 KB an SM in both, more than the memory system needs in flight).  The group's warps share a tile's columns
-// and multiply with mma.sync m16n8k16, weights as the 16 rows, up to 8 activation rows as the columns, accumulators in
-// registers in fp32.  (tcgen05.mma would hold 128 rows against columns that are not there, and its operands' layout
-// would cost the copies their freedom: a tenth of the tensor pipe's time is all that these products take.)
-// Two groups: what a stage costs a warp beside its products (the wait, the addresses) is paid by half of the warps, and
-// a group's latency passes while the other works.
+// reaches (some 200 KB an SM in both, more than the memory system needs in flight).  The group's warps share a tile's
+// columns and multiply with mma.sync m16n8k16, weights as the 16 rows, up to 8 activation rows as the columns,
+// accumulators in registers in fp32.  (tcgen05.mma would hold 128 rows against columns that are not there, and its
+// operands' layout would cost the copies their freedom: a tenth of the tensor pipe's time is all that these products
+// take.) Two groups: what a stage costs a warp beside its products (the wait, the addresses) is paid by half of the
+// warps, and a group's latency passes while the other works.
 //
 // A dot product does not care for the order of its columns, as long as both operands share it: lane (g, t) takes the 8
 // consecutive columns 8 t .. 8 t + 7 of a 32-wide chunk, one 16-byte access of weight row g, of row g + 8 and of
@@ -35,10 +35,10 @@ constexpr unsigned long long WAIT_NS = 1000000000ull;  // 1 s: a healthy wait ta
 __host__ __device__ constexpr int pitch_of(int cols) { return (cols * 2 + 127) / 128 * 128 + 64; }
 
 // How up to 16 weight rows lie in a stage.  The copy engine takes some 45 ns a copy whatever its size, as much as 2 KB
-// take at the memory's rate.  Rows of up to half of that come four to a copy (they follow one another in memory): a layer
-// of 5 tokens with experts of 512 columns takes 58 us, row by row 62.  Longer rows come a copy each, in pieces of KC
-// columns: four at a time, a layer of 32 tokens with experts of 768 columns took 213 us against 207 (a slot is held until
-// the last row of four has landed).  Row s lies at (s & 3) rows and (s >> 2) fours, and lane g reads rows
+// take at the memory's rate.  Rows of up to half of that come four to a copy (they follow one another in memory): a
+// layer of 5 tokens with experts of 512 columns takes 58 us, row by row 62.  Longer rows come a copy each, in pieces of
+// KC columns: four at a time, a layer of 32 tokens with experts of 768 columns took 213 us against 207 (a slot is held
+// until the last row of four has landed).  Row s lies at (s & 3) rows and (s >> 2) fours, and lane g reads rows
 // (g >> 1) + 4 (g & 1) and 8 more: the two rows of an access phase belong to fours an odd multiple of 64 bytes apart,
 // so that no two lanes meet in a bank.
 constexpr int KC = 1024;    // columns of a stage at most
@@ -177,12 +177,13 @@ __device__ __forceinline__ float sum_of(const float4 *red, int nt, int n, int l,
     return v;
 }
 
-// A group's share of the units (tiles of weight rows, as its producer deals them) times the activation rows that each of
-// them meets, K columns, kc a stage.
+// A group's share of the units (tiles of weight rows, as its producer deals them) times the activation rows that each
+// of them meets, K columns, kc a stage.
 //   info(u)    {first, n}: the unit's activation rows, n <= 8 NTM of them from place `first` on
 //   at(i)      address of the activation row in place i
 //   done(u, info, sums, nt, thread)  by all threads of a group: its warps' sums of the unit's nt tiles of 8 rows (see sum_of)
-// The activations of a stage are asked for before the wait for its weights.  red: GROUP_WARPS * NTM * 32 float4 a group.
+// The activations of a stage are asked for before the wait for its weights.  red: GROUP_WARPS * NTM * 32 float4 a
+// group.
 template <typename T, int NTM, typename Info, typename At, typename Done>
 __device__ __forceinline__ void stream_units(Ring &ring, int units, int K, int kc, float4 *red, int warp,
                                              int lane, Info info, At at, Done done) {

@@ -721,8 +721,9 @@ int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const 
  * others are left; a NaN or +inf logit, or SiLU(gate) * up that is not finite, makes its
  * own token's row NaN.  Weights that are not finite reach their experts' tokens only.
  * The kernel takes every SM (a cooperative launch with two grid barriers, each wait
- * limited to a second: MOE_DEV_TIMEOUT, after which out is undefined and
- * moe_workspace_init comes before the next call).
+ * limited to a second: MOE_DEV_TIMEOUT, after which out is undefined; when a barrier ran out,
+ * every later call on the workspace sets MOE_DEV_TIMEOUT and leaves its out as it was, also
+ * when the status has been cleared, until moe_workspace_init).
  *   ws: moe_decode_workspace_size bytes (of N tokens, or more), 256-byte aligned,
  *   initialised once by moe_workspace_init (its status block holds the barriers' 64-bit
  *   arrival count, which runs on from call to call); calls that may overlap, captured
@@ -736,7 +737,7 @@ int moe_ffn_decode(const void *x, int64_t x_stride, int dtype, const float *rout
 
 /* Failure-detection check of its first grid barrier: moe_ffn_decode with the barrier waiting for one more arrival
  * than there are CTAs, and a limit of limit_ms (1..1000).  Every CTA gives up, MOE_DEV_TIMEOUT is set, out is left as
- * it was and the context stays usable; moe_workspace_init comes before the workspace's next call. */
+ * it was and the context stays usable; later calls on the workspace are refused until moe_workspace_init. */
 int moe_debug_decode_barrier_timeout(const void *x, int64_t x_stride, int dtype, const float *routerW, const void *gate,
                                      const void *up, const void *down, int N, int D, int E, int F, int top_k, void *out,
                                      int64_t out_stride, int limit_ms, void *ws, size_t ws_bytes, cudaStream_t stream);

@@ -83,7 +83,10 @@ size_t list_bytes(int E, int N, int k) {
 }
 
 // Grid barrier of the consumer warps (a cooperative launch).  Arrivals are counted through, never reset: a call makes
-// two for each CTA, so the count is a multiple of that before every call.  False when the limit ran out.
+// two for each CTA, so the count is a multiple of that before every call.  False when the limit ran out, here or in
+// another CTA: the count is of no use then (some CTAs leave without their second arrival), so its top bit is set, which
+// lets every waiting CTA go at once and has later calls refused until the workspace is initialised anew.
+constexpr unsigned long long GIVEN_UP = 1ull << 63;
 __device__ bool grid_barrier(unsigned long long *arrived, unsigned long long target, unsigned *status,
                              unsigned long long limit_ns, int *ok_s) {
     consumer_sync();
@@ -91,20 +94,20 @@ __device__ bool grid_barrier(unsigned long long *arrived, unsigned long long tar
         unsigned long long n;  // releases what the CTA's threads wrote before their barrier above
         asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(n) : "l"(arrived) : "memory");
         ++n;
-        int ok = 1;
         if (n < target) {
             const unsigned long long t0 = tc::globaltimer();
             for (unsigned it = 1;; ++it) {
                 asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(n) : "l"(arrived) : "memory");
-                if (n >= target) break;
+                if (n >= target) break;  // or given up
                 if ((it & 31) == 0 && tc::globaltimer() - t0 > limit_ns) {
                     atomicOr(status, MOE_DEV_TIMEOUT);
-                    ok = 0;
+                    atomicOr(arrived, GIVEN_UP);
+                    n = GIVEN_UP;
                     break;
                 }
             }
         }
-        *ok_s = ok;
+        *ok_s = n < GIVEN_UP;
     }
     consumer_sync();
     return *ok_s != 0;
@@ -222,12 +225,17 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         tc::mbar_init(xbar, 1);
         init_rings(bar, a.stages);
         arrivals = *reinterpret_cast<volatile unsigned long long *>(a.arrived);
+        if (arrivals >= GIVEN_UP) {
+            atomicOr(a.status, MOE_DEV_TIMEOUT);
+            ok_s = 0;
+        }
         arrivals -= arrivals % (2u * (unsigned)G);
     }
     if (bid == 0 && tid < MAX_ROWS) a.amax[tid] = 0;
     if (tid < MAX_ROWS) amax_s[tid] = 0;
     for (int e = tid; e < E; e += THREADS) ls.mask[e] = 0;
     __syncthreads();
+    if (!ok_s) return;  // an earlier call gave up
 
     // ---- router: an expert's row (or the shared gate's) and 8 tokens at a time, 16 where 8 would take more rounds;
     // two rows where a CTA has two, so that both share the tokens' loads (one token 40 to 36 us).  Few rows: a CTA

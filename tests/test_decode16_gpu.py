@@ -332,3 +332,28 @@ def test_refusals(ops):
                 lambda: call(ops, s, 2, False, ws, residual=s["residual"][:2]), lambda: call(ops, dict(s, up=s["up"].cpu()), 2, False, ws)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("N", [3, 12])
+def test_a_workspace_whose_barrier_ran_out_is_refused(ops, N):
+    """Its arrival count says nothing any more: calls, captured ones among them, leave out alone and say so, also after
+    the status has been cleared, until the workspace is initialised."""
+    s = layer(N, 256, 8, 64, BF16, seed=17)
+    ws = ops.new_decode_workspace(N, 256, 8, 64, 2)
+    want = call(ops, s, 2, False, ws)
+    out = torch.full((N, 256), 4.0, dtype=BF16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(ops, s, 2, False, ws, out=out)
+    ops.moe_debug_decode_barrier_timeout(s["x"], s["routerW"], s["gate"], s["up"], s["down"], 2, out, 50, ws)
+    assert ops.moe_workspace_status(ws) == 4 and torch.all(out == 4)  # MOE_DEV_TIMEOUT; read and cleared
+    assert ops.moe_workspace_status(ws) == 0
+    call(ops, s, 2, False, ws, out=out)
+    assert ops.moe_workspace_status(ws) == 4 and torch.all(out == 4)
+    g.replay()
+    assert ops.moe_workspace_status(ws) == 4 and torch.all(out == 4)
+    ops.moe_workspace_init(ws)
+    for _ in range(3):
+        g.replay()
+        assert torch.equal(out, want) and torch.equal(call(ops, s, 2, False, ws), want)
+    assert ops.moe_workspace_status(ws) == 0

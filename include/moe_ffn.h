@@ -717,7 +717,7 @@ int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const 
  * E <= 1024, 1 <= N <= 32.
  * Sums are fp32; SiLU(gate) * up enters the second product with 16 significant bits
  * (bf16) or 22 and more (fp16); one rounding to out's type.  The order of the sums is
- * fixed for given sizes and device.  An expert whose logit is -inf is not chosen while
+ * fixed for given sizes and device, so a token's row does not depend on the other tokens.  An expert whose logit is -inf is not chosen while
  * others are left; a NaN or +inf logit, or SiLU(gate) * up that is not finite, makes its
  * own token's row NaN.  Weights that are not finite reach their experts' tokens only.
  * The kernel takes every SM (a cooperative launch with two grid barriers, each wait

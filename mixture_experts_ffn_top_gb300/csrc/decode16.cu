@@ -11,8 +11,9 @@
 //   2. gate and up: tiles of 8 gate and the same 8 up rows, the tiles of all touched experts dealt in turn;
 //      h = w_s SiLU(gate) up, in fp32, to the workspace; barrier;
 //   3. down: each CTA owns some output rows and walks all touched experts over them.  The routing weight is in h, so
-//      one accumulator takes the products of every expert and no partial rows are combined afterwards: sums go
-//      expert by expert (ascending; the shared one last), their order fixed.
+//      one accumulator takes the products of every expert and no partial rows are combined afterwards.  Which of the two
+//      groups of warps takes a stage hangs on expert and columns alone, and each walks its experts ascending, so that a
+//      token's sum has the same order whatever the other tokens chose (see Part).
 // The rings (stream16.cuh) run on through the second barrier: the first down tiles fly while it completes.
 // bf16, 64 experts of 1024 x 2048, top 8: one token 30 us (floor 14.9), eight tokens 95 us (82% of the copy rate); 32
 // tokens over 128 experts of 768 some of which are ahead 99 us (94%).  Of eight tokens' time the router takes 3.3 us,
@@ -50,13 +51,14 @@ struct DecodeArgs {
     unsigned long long barrier_ns;
     int extra_arrivals;  // failure-detection check: arrivals the first barrier waits for beyond the grid (0 normally)
     int kc, pitch, stages, x_pitch;  // x_pitch 0: the activations stay in global memory
+    int odd_pieces;                  // an expert's down rows are an odd number of stages
     int x_at, red_at, list_at;       // places in shared memory
 };
 
 // Small arrays of a CTA, behind one another from `p` on.
 struct Lists {
     unsigned *mask;  // [E] tokens that chose an expert
-    int *expert;     // [touched + 1] the touched experts, then E: the shared one
+    int *expert;     // [touched + 1] the touched experts, of several tokens' the even ones first, then E: the shared one
     int *first;      // [touched + 1] their first entry
     int *tok;        // [entries] token
     float *w;        // [entries] weight
@@ -173,6 +175,45 @@ __device__ __forceinline__ void route(const float *logits, int E, int k, int nor
     if (lane < k) w[lane] = bad ? __uint_as_float(0x7fffffffu) : norm ? __fdiv_rn(mine, sum) : mine;
 }
 
+// What a group of warps takes of the down part, in stages of kc columns of a listed expert's rows.  Of experts of one
+// stage the first group takes the even ones, the second the odd ones, which are listed behind them; of longer ones each
+// takes every second stage.  The shared expert comes last, to the second group if it is one stage.  So which warps add up
+// a stage hangs on its expert and columns alone.  Dealt to the groups in turn, as they come, a token's products would meet
+// in another order with each batch; but the groups would have as many stages, which even and odd experts share evenly but
+// for chance.  Six batches each, so and in turn: eight tokens of 64 experts 92.2 us and 90.4, five of 256 59.0 and 58.3,
+// 32 of 128 at skewed choice 97.6 and 97.2, at uniform choice 196 both.  (One token has no others: each group takes half
+// of its experts.)
+struct Part {
+    struct Stage {
+        int i, k0;  // place in the list of experts, first column
+    };
+    int group, touched, even, F, Fs, kc;
+    bool flip;  // experts of an odd number of stages: the odd ones' first goes to the second group
+    int past;   // the group's routed experts are before this place
+    int end;    // behind the place of its last stage
+    __device__ __forceinline__ Part(int group, int touched, int even, int F, int Fs, int kc, bool flip)
+        : group(group), touched(touched), even(min(even, touched)), F(F), Fs(Fs), kc(kc), flip(flip) {
+        past = F <= kc && group == 0 ? this->even : touched;
+        end = touched + (Fs > (group == 0 ? kc : 0));
+    }
+    __device__ __forceinline__ void settle(Stage &s) const {  // at the beginning of place i
+        if (s.i >= past) s.i = max(s.i, touched);
+        const int K = s.i >= touched ? Fs : F;
+        s.k0 = K <= kc ? 0 : (group ^ (flip && s.i >= even && s.i < touched)) * kc;
+    }
+    __device__ __forceinline__ Stage begin() const {
+        Stage s{F <= kc && group == 1 ? even : 0, 0};
+        settle(s);
+        return s;
+    }
+    __device__ __forceinline__ void next(Stage &s) const {
+        if ((s.k0 += 2 * kc) < (s.i >= touched ? Fs : F)) return;
+        ++s.i;
+        settle(s);
+    }
+};
+static_assert(GROUPS == 2);
+
 // 8 values times `scale` as 16-bit values, and as 16-bit values what those leave.
 template <typename T>
 __device__ __forceinline__ void split8(const uint4 &a, const uint4 &b, float scale, uint4 &hi, uint4 &lo) {
@@ -206,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     constexpr bool F16 = std::is_same_v<T, __half>, PACKED = NTM > 1;  // (see the down part)
     extern __shared__ __align__(1024) char smem[];
     __shared__ __align__(8) unsigned long long bars[GROUPS * 2 * MAX_STAGES + 1];
-    __shared__ int abort_flag, ok_s, touched_s;
+    __shared__ int abort_flag, ok_s, touched_s, even_s;
     __shared__ unsigned amax_s[MAX_ROWS];
     __shared__ float scale_s[MAX_ROWS], gate_s[MAX_ROWS];
     __shared__ float part[2][CONSUMERS][16];
@@ -327,28 +368,37 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         if (lane == 0) gate_s[t] = a.shexp_gate != nullptr ? __fdiv_rn(1.0f, 1.0f + expf(-__ldcg(l + E))) : 1.0f;
     }
     __syncthreads();
-    // ---- the touched experts and their entries, by expert, then token.  A thread lists its expert; how many there are
-    // before it every warp counts for itself.
+    // ---- the touched experts and their entries, by expert (the even ones first), then token.  A thread lists its expert;
+    // how many there are before it every warp counts for itself.
     const int groups = (E + 31) / 32;
-    int listed_before = 0, entries_before = 0, next_group = 0;
+    const unsigned evens = N == 1 ? 0xffffffffu : 0x55555555u;  // the lanes of the experts that come first
+    const bool even = evens >> lane & 1;
+    const int shift = even ? 0 : 16;
     for (int gr = warp; gr < groups; gr += CONSUMERS + GROUPS) {
-        for (; next_group < gr; ++next_group) {
-            const int e = next_group * 32 + lane;
-            const unsigned m = e < E ? ls.mask[e] : 0;
-            listed_before += __popc(__ballot_sync(0xffffffffu, m != 0));
-            entries_before += __reduce_add_sync(0xffffffffu, __popc(m));
+        // entries of either part in 16 bits (at most 32 x 32)
+        unsigned before = 0, all = 0;
+        int listed_before = 0;
+        for (int other = 0; other < groups; ++other) {
+            const int e = other * 32 + lane;
+            const unsigned m = e < E ? ls.mask[e] : 0, there = __ballot_sync(0xffffffffu, m != 0);
+            const unsigned sum = __reduce_add_sync(0xffffffffu, (unsigned)__popc(m) << shift);
+            if (other < gr) before += sum;
+            all += sum;
+            listed_before += __popc(there & (other < gr ? (even ? evens : 0xffffffffu) : even ? 0u : evens));
         }
         const int e = gr * 32 + lane;
         unsigned m = e < E ? ls.mask[e] : 0;
-        const int n = listed_before + __popc(__ballot_sync(0xffffffffu, m != 0) & ((1u << lane) - 1)), c = __popc(m);
-        int in = c;
+        const unsigned alike = (even ? evens : ~evens) & ((1u << lane) - 1);  // the lanes before this one in its part
+        const int n = listed_before + __popc(__ballot_sync(0xffffffffu, m != 0) & alike), c = __popc(m);
+        unsigned in = (unsigned)c << shift;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, in, o);
+            const unsigned v = __shfl_up_sync(0xffffffffu, in, o);
             if (lane >= o) in += v;
         }
+        in += before;
         if (m != 0) {
-            int at = entries_before + in - c;
+            int at = (int)(in >> shift & 0xffff) - c + (even ? 0 : (int)(all & 0xffff));
             ls.expert[n] = e;
             ls.first[n] = at;
             if (PACKED) {
@@ -367,14 +417,18 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
         }
     }
     if (warp == CONSUMERS + GROUPS - 1) {  // the shared expert, behind them
-        for (; next_group < groups; ++next_group) {
-            const int e = next_group * 32 + lane;
-            listed_before += __popc(__ballot_sync(0xffffffffu, e < E && ls.mask[e] != 0));
+        int listed_before = 0, first_part = 0;
+        for (int gr = 0; gr < groups; ++gr) {
+            const int e = gr * 32 + lane;
+            const unsigned there = __ballot_sync(0xffffffffu, e < E && ls.mask[e] != 0);
+            listed_before += __popc(there);
+            first_part += __popc(there & evens);
         }
         if (lane == 0) {
             ls.expert[listed_before] = E;
             ls.first[listed_before] = N * k;
             touched_s = listed_before;
+            even_s = first_part;
         }
         if (lane < N) {
             ls.tok[N * k + lane] = lane;
@@ -398,10 +452,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
     const int units = touched * upe + a.Fs / 8;
     const int group = consumer ? warp / GROUP_WARPS : warp - CONSUMERS;
     Ring ring(smem, bar, group, a.stages, a.pitch, &abort_flag, a.status);
+    auto part_of_down = [&]() { return Part(group, touched, N == 1 ? (listed + 1) / 2 : even_s, a.F, a.Fs, a.kc, a.odd_pieces); };
 
     if (!consumer) {  // the group's producer
         const Layout lay(D);
-        int issued = 0, turn = 0;
+        int issued = 0;
         bool ok = true;
         for (int u = first_unit(group); u < units && ok; u += unit_stride()) {
             const int i = min(u / upe, touched), e = ls.expert[i], r = (u - i * upe) * 8;
@@ -413,17 +468,14 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                 issued += ok;
             }
         }
+        const Part share = part_of_down();
         for (int rt = 0; rt < row_tiles && ok; ++rt) {
             const int r0 = row0 + (row1 - row0) * rt / row_tiles, r1 = row0 + (row1 - row0) * (rt + 1) / row_tiles;
-            for (int i = 0; i < listed && ok; ++i) {
-                const int e = ls.expert[i], K = e == E ? a.Fs : a.F, n = r1 - r0;
-                const T *src = static_cast<const T *>(e == E ? a.sh_down : a.down) + ((int64_t)(e == E ? 0 : e) * D + r0) * K;
-                const Layout lay(K);
-                for (int k0 = 0; k0 < K && ok; k0 += a.kc, turn = turn + 1 == GROUPS ? 0 : turn + 1) {
-                    if (turn != group) continue;
-                    ok = ring.produce(lane, lay, K, min(a.kc, K - k0), src + k0, min(n, 8), src + (int64_t)8 * K + k0, n - min(n, 8));
-                    issued += ok;
-                }
+            for (Part::Stage at = share.begin(); at.i < share.end && ok; share.next(at)) {
+                const int e = ls.expert[at.i], K = e == E ? a.Fs : a.F, n = r1 - r0;
+                const T *src = static_cast<const T *>(e == E ? a.sh_down : a.down) + ((int64_t)(e == E ? 0 : e) * D + r0) * K + at.k0;
+                ok = ring.produce(lane, Layout(K), K, min(a.kc, K - at.k0), src, min(n, 8), src + (int64_t)8 * K, n - min(n, 8));
+                issued += ok;
             }
         }
         if (lane == 0 && *reinterpret_cast<volatile int *>(&abort_flag)) drain(ring.bar, a.stages, issued);
@@ -517,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             if (!PACKED) mma_chunk<T>(rest_acc, lo, hi, rest);
         }
     };
-    int turn = 0;  // the stages go to the groups in turn
+    const Part share = part_of_down();
     for (int rt = 0; rt < row_tiles; ++rt) {
         const int r0 = row0 + (row1 - row0) * rt / row_tiles, r1 = row0 + (row1 - row0) * (rt + 1) / row_tiles;
         consumer_sync();  // the sums before these have been read
@@ -525,24 +577,20 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             for (int j = lane; j < 16 * own_pitch; j += 32) own[j] = 0.0f;
             __syncwarp();
         }
-        struct Place {
-            int i, k0, j, turn;
+        struct Place : Part::Stage {
+            int j;  // tile of entries
         };
-        auto next_stage = [&](Place &p) {  // the group's next stage
-            do {
-                if ((p.k0 += a.kc) >= length(p.i)) p.k0 = 0, ++p.i;
-                p.turn = p.turn + 1 == GROUPS ? 0 : p.turn + 1;
-            } while (p.i < listed && p.turn != group);
+        auto next_stage = [&](Place &p) {
+            share.next(p);
             p.j = 0;
         };
-        Place at{0, 0, 0, turn};
-        if (turn != group) next_stage(at);
+        Place at{share.begin(), 0};
         if constexpr (!PACKED) {
             float one[1][4] = {};
             Block f;
             auto fetch = [&](const Place &p) { load(ls.at[p.i * 8 + g], p.k0, min(a.kc, length(p.i) - p.k0), f); };
-            if (at.i < listed) fetch(at);
-            while (at.i < listed) {
+            if (at.i < share.end) fetch(at);
+            while (at.i < share.end) {
                 const int K = length(at.i), cols = min(a.kc, K - at.k0);
                 // a column without an entry stays out: 0 times a weight that is not finite
                 const short2 there = *reinterpret_cast<const short2 *>(ls.at + at.i * 8 + 2 * t4);
@@ -550,7 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                 ring.wait_full();
                 float acc[4] = {}, rests[4] = {};
                 products(Layout(K), cols, f, acc, rests);
-                if (at.i < listed) fetch(at);  // the next stage's, while the other group works
+                if (at.i < share.end) fetch(at);  // the next stage's, while the other group works
                 ring.release(lane);
                 ring.next();
 #pragma unroll
@@ -561,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
             float acc[4] = {};
             Place ahead = at;
             auto fetch = [&](Block &f) {  // and on to the tile behind it
-                if (ahead.i >= listed) return;
+                if (ahead.i >= share.end) return;
                 const int n = count(ahead.i), e = ahead.j * 4 + (g & 3);
                 load(e < n ? ls.first[ahead.i] + e : -1, ahead.k0, min(a.kc, length(ahead.i) - ahead.k0), f);
                 if (++ahead.j * 4 >= n) next_stage(ahead);
@@ -589,9 +637,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                     next_stage(at);
                 else
                     ++at.j;
-                return at.i < listed;
+                return at.i < share.end;
             };
-            if (at.i < listed) {
+            if (at.i < share.end) {
                 Block b0, b1, b2;
                 fetch(b0);
                 if constexpr (F16) {  // twice the registers: a tile ahead
@@ -602,7 +650,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode16_kernel(const DecodeArgs a
                 }
             }
         }
-        turn = at.turn;
         consumer_sync();
         if (!*reinterpret_cast<volatile int *>(&abort_flag))
             for (int j = tid; j < N * 16; j += CONSUMERS * 32) {
@@ -682,6 +729,7 @@ int launch_decode16(const Decode16Call &c, void *ws, cudaStream_t s, unsigned lo
     const int ntm = c.N <= 8 ? 1 : c.N <= 16 ? 2 : 4;
     a.kc = std::min(KC, (std::max({c.D, c.F, c.Fs}) + 31) / 32 * 32);
     a.pitch = pitch_of(a.kc);
+    a.odd_pieces = (c.F + a.kc - 1) / a.kc % 2;
     // the warps' sums, or each warp's rows x tokens
     const size_t red = std::max((size_t)CONSUMERS * 512 * ntm, (size_t)CONSUMERS * 64 * (c.N + 1));
     const size_t ring = (size_t)GROUPS * 16 * a.pitch, lists = list_bytes(c.E, c.N, c.top_k), most = SMEM_LIMIT - 5120;

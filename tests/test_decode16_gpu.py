@@ -357,3 +357,21 @@ def test_a_workspace_whose_barrier_ran_out_is_refused(ops, N):
         g.replay()
         assert torch.equal(out, want) and torch.equal(call(ops, s, 2, False, ws), want)
     assert ops.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("N,D,E,F,k,Fs", [(2, 512, 16, 96, 3, 0), (8, 2048, 64, 1024, 8, 0), (5, 1000, 40, 1544, 4, 72), (8, 5000, 9, 2056, 2, 0),
+                                          (9, 640, 24, 520, 4, 64), (32, 2048, 128, 768, 8, 0), (17, 5000, 9, 1096, 2, 1032)])
+def test_a_tokens_row_does_not_hang_on_the_others(ops, N, D, E, F, k, Fs, dtype):
+    """The order of a token's sums is its own: the same bits whatever the other rows hold and choose.  The residual takes
+    the rounded result away, so that what is left shows the sums' last bits."""
+    s = layer(N, D, E, F, dtype, Fs, Fs > 0, seed=21)
+    ws = ops.new_decode_workspace(N, D, E, F, k, Fs)
+    left = -call(ops, s, k, True, ws)
+    want = call(ops, s, k, True, ws, residual=left)
+    for i in range(6):
+        keep = (5 * i) % N
+        x = torch.randn((N, D), generator=gen(22 + i), device="cuda").to(dtype)
+        x[keep] = s["x"][keep]
+        got = call(ops, dict(s, x=x), k, True, ws, residual=left)
+        assert torch.equal(got[keep], want[keep]), f"{int((got[keep] != want[keep]).sum())} of {D} values, batch {i}"

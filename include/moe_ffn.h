@@ -688,7 +688,8 @@ int moe_rmsnorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t
  * (MOE_ERR_UNSUPPORTED_SHAPE, as for few rows with more than 2^30 pieces of work).
  * Products are exact and summed in fp32 by the tensor cores (in an order that
  * depends on the sizes, not on the other rows' values); the epilogue is fp32,
- * its activations within 2^-18 of their values; one rounding to y's type.
+ * SiLU within 2^-16 of its value, GELU within 2^-18 above -4 and 2^-15 below (values under
+ * 2^-126 may be 0); one rounding to y's type.
  * Few rows (at most 32 over experts; of one matrix 8, or up to 32 that fit beside the
  * weights in shared memory) run on a kernel that reads each touched expert's weights
  * once; more rows on tensor-core tiles of 256 weight rows x up to 256 rows.  What a

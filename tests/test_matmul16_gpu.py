@@ -261,3 +261,22 @@ def test_refusals(ops, ws):
                 lambda: ops.moe_matmul(x, w, ws, residual=x)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("n", [24, 2000])
+def test_activations_of_bf16_over_their_range(ops, ws, n):
+    """bf16 keeps the activations' far ends, down to 2^-126: SiLU's and GELU's values there are within 2^-15 (an exponent
+    near 126 whose roundings of 2^-24 each count 87-fold in the result), then half a step; nothing below 2^-126 is asked
+    for.  The normal distribution by erfc: 1 + erf has no digits left there."""
+    act_of = dict(ACT, gelu=lambda v: 0.5 * v * torch.erfc(v * -(0.5 ** 0.5)))
+    v = torch.cat((-torch.linspace(0, 120, 1500), torch.linspace(0, 120, 400), -torch.linspace(8, 14, 76),
+                   torch.tensor([-86.5, -87.0, -87.5, -88.0, -88.5, -89.0, -1e3, -1e5, -3e38, 1e5, 3e38, 1e-30, -1e-30, 2e-38, -2e-38, 0.0])))
+    v = torch.cat((v, torch.zeros(2000 - v.numel()))).to(BF16).cuda()
+    for lo in [0] if n == 2000 else range(1784, 2000, n):
+        x = torch.zeros((n, 8), dtype=BF16, device="cuda")
+        x[:, 0] = v[lo:lo + n]
+        w = torch.zeros((1, 1, 8), dtype=BF16, device="cuda")
+        w[..., 0] = 1
+        for act in ("relu", "silu", "gelu"):
+            ref = act_of[act](x[:, :1].double())
+            close(ops.moe_matmul(x, w, ws, act=act), ref, 2.0 ** -15 * ref.abs() + 2.0 ** -126)

@@ -716,11 +716,13 @@ int moe_matmul(const void *x, int64_t x_stride, int dtype, const void *w, const 
  * D, F and Fs multiples of 8, D <= 32768, F, Fs <= 65536; x, the weights, routerW and
  * shexp_gate 16-byte aligned, x_stride a multiple of 8 (or 0); 1 <= top_k <= min(E, 32),
  * E <= 1024, 1 <= N <= 32.
- * Sums are fp32; SiLU(gate) * up enters the second product with 16 significant bits
- * (bf16) or 22 and more (fp16); one rounding to out's type.  The order of the sums is
- * fixed for given sizes and device, so a token's row does not depend on the other tokens.  An expert whose logit is -inf is not chosen while
- * others are left; a NaN or +inf logit, or SiLU(gate) * up that is not finite, makes its
- * own token's row NaN.  Weights that are not finite reach their experts' tokens only.
+ * Sums are fp32; SiLU(gate) * up, with its weight, enters the second product with 16
+ * significant bits (bf16), or within 2^-22 of itself or 2^-39 of the token's largest,
+ * whichever is more (fp16); one rounding to out's type.  The order of the sums is fixed for
+ * given sizes and device, so a token's row does not depend on the other tokens.
+ * An expert whose logit is -inf is not chosen while others are left (and counts 0 then); a
+ * NaN or +inf logit, no logit above -inf, or SiLU(gate) * up that is not finite makes its own
+ * token's row NaN.  Weights that are not finite reach their experts' tokens only.
  * The kernel takes every SM (a cooperative launch with two grid barriers, each wait
  * limited to a second: MOE_DEV_TIMEOUT, after which out is undefined; when a barrier ran out,
  * every later call on the workspace sets MOE_DEV_TIMEOUT and leaves its out as it was, also

@@ -20,9 +20,9 @@
 // the first barrier 1.3, routing and lists 4.1, gate and up 55, the second barrier 4 to 5, down 30: what is left above
 // the bytes are the 9 us in which no weights fly and the barrier's wait for the slowest CTA.
 //
-// h enters the tensor cores as two 16-bit columns, its rounded value and the rest: 16 significant bits in bf16, at
-// least 22 in fp16, where a token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15 (a
-// fp16 h itself could overflow or vanish).
+// h enters the tensor cores as two 16-bit columns, its rounded value and the rest: 16 significant bits in bf16.  In fp16 a
+// token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15 (a fp16 h itself could overflow or
+// vanish): off by at most 2^-22 of itself, or by 2^-39 of the token's largest where that is more, 17 binades below it.
 #include <algorithm>
 
 #include "stream16.cuh"

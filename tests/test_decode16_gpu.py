@@ -375,3 +375,23 @@ def test_a_tokens_row_does_not_hang_on_the_others(ops, N, D, E, F, k, Fs, dtype)
         x[keep] = s["x"][keep]
         got = call(ops, dict(s, x=x), k, True, ws, residual=left)
         assert torch.equal(got[keep], want[keep]), f"{int((got[keep] != want[keep]).sum())} of {D} values, batch {i}"
+
+
+@pytest.mark.parametrize("N", [3, 20])
+@pytest.mark.parametrize("apart", [2.0 ** 10, 2.0 ** 18, 2.0 ** 24])
+def test_fp16_intermediates_far_apart(ops, N, apart):
+    """One power of two scales all of a token's h, so its smaller values are off by 2^-39 of the largest, or 2^-22 of
+    themselves (17 binades below the largest the first takes over).  The shared expert's h are the large ones; its down
+    rows are 0, so that what shows is the routed experts'."""
+    D, E, F, k = 256, 6, 64, 2
+    s = layer(N, D, E, F, F16, F, False, seed=18)
+    s["up"] = (s["up"].float() / 64).half()
+    s["shared"] = ((s["shared"][0].float() * 8).half(), (s["shared"][1].float() * (apart / 64 / 8)).half(), torch.zeros_like(s["shared"][2]))
+    assert torch.isfinite(s["shared"][1]).all()
+    y, tol = reference(s, k, True)
+    x = s["x"].double()
+    a, b = x @ s["shared"][0].double().t(), x @ s["shared"][1].double().t()
+    top = (a * torch.sigmoid(a) * b).abs().amax(dim=1, keepdim=True)
+    rows = s["down"].double().abs().sum(dim=2).amax(dim=0)  # the largest sum of a row of down, by output
+    ws = ops.new_decode_workspace(N, D, E, F, k, F)
+    close(call(ops, s, k, True, ws), y, tol + 2.0 ** -39 * top * k * rows)

@@ -395,3 +395,46 @@ def test_fp16_intermediates_far_apart(ops, N, apart):
     rows = s["down"].double().abs().sum(dim=2).amax(dim=0)  # the largest sum of a row of down, by output
     ws = ops.new_decode_workspace(N, D, E, F, k, F)
     close(call(ops, s, k, True, ws), y, tol + 2.0 ** -39 * top * k * rows)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("N,dtype", [(4, BF16), (4, F16), (12, BF16), (12, F16)])
+def test_tokens_with_fewer_experts_than_slots_and_with_none(ops, N, dtype, norm):
+    """Logits of one token overflow to -inf for all experts but two (four slots: those two count, the others 0), of another
+    for all experts (its row is NaN); the other tokens meet 0 times those weights."""
+    s = layer(N, 128, 10, 64, dtype, seed=19)
+    live = [2, 5]
+    dead = [e for e in range(10) if e not in live]
+    s["x"][:, :2] = 0
+    s["x"][1, 0] = s["x"][3, 1] = -4
+    s["routerW"][dead, 0] = 2e38
+    s["routerW"][:, 1] = 2e38
+    s["routerW"][live, 0] = 0.5
+    ws = ops.new_decode_workspace(N, 128, 10, 64, 4)
+    out = call(ops, s, 4, norm, ws)
+    assert torch.all(torch.isnan(out[3])) and ops.moe_workspace_status(ws) == 0
+    few = dict(s, x=s["x"][1:2], **{n: s[n][live].contiguous() for n in ("routerW", "gate", "up", "down")})
+    close(out[1:2], *reference(few, 2, norm))
+    rest = [t for t in range(N) if t not in (1, 3)]
+    close(out[rest], *reference(dict(s, x=s["x"][rest]), 4, norm))
+
+
+def test_gradient_of_a_blocks_norm(ops):
+    """The norm before the layer and its gradient on the same residual stream, as a block runs them, d_x and d_gamma
+    against float64.  fp32 sums of 512 random values: some 50 steps of 2^-24 of their magnitudes, under 2^-16 of the rows'
+    scale with all factors (a gamma of 1.5, r near 1, h below 5); then half a step."""
+    N, D, E, F, k = 24, 512, 16, 128, 4
+    s = layer(N, D, E, F, BF16, seed=9)
+    gamma, beta = torch.rand(D, generator=gen(10), device="cuda") + 0.5, torch.randn(D, generator=gen(11), device="cuda") * 0.1
+    stream, d_y = s["residual"], torch.randn((N, D), generator=gen(20), device="cuda").to(BF16)
+    x = ops.moe_layernorm(stream, gamma, beta, 1e-5)
+    call(ops, dict(s, x=x), k, True, ops.new_decode_workspace(N, D, E, F, k), residual=stream)
+    got = ops.moe_layernorm_grad(d_y, stream, gamma, 1e-5, ops.new_norm_workspace(N, D))
+    leaves = [t.double().requires_grad_() for t in (stream, gamma, beta)]
+    d = leaves[0] - leaves[0].mean(dim=1, keepdim=True)
+    y = d / torch.sqrt(d.square().mean(dim=1, keepdim=True) + 1e-5) * leaves[1] + leaves[2]
+    y.backward(d_y.double())
+    for a, leaf in zip(got, leaves):
+        ref = leaf.grad
+        half = HALF.get(a.dtype, U)
+        assert torch.all((a.double() - ref).abs() <= 2.0 ** -16 * ref.abs().amax() + half * ref.abs())

@@ -292,3 +292,44 @@ def test_refusals(ops):
                 lambda: ops.moe_layernorm(x.cpu(), gamma, None, EPS)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("D", [256, 1001, 2046, 9000, 20001])
+def test_layernorm_of_one_row_for_all(ops, D, dtype):
+    """x with row stride 0: the bits of rows written out (which lie on the same boundaries)."""
+    x = rows(1, D, dtype, 23)
+    gamma, beta = torch.randn(D, generator=gen(24), device="cuda"), torch.randn(D, generator=gen(25), device="cuda")
+    for N in (3, 700):
+        y = ops.moe_layernorm(x.expand(N, D), gamma, beta, EPS)
+        assert torch.equal(y, ops.moe_layernorm(x.repeat(N, 1), gamma, beta, EPS)) and torch.equal(y, y[:1].expand(N, D))
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("D", [8193, 12002, 16385, 32767])
+def test_gradients_of_long_rows_at_any_place(ops, D, dtype, rms):
+    """Rows longer than a tile of shared memory takes, more of them than CTAs, an odd number of elements apart.  Bounds as in
+    test_gradients."""
+    N = 700
+    gamma = torch.randn(D, generator=gen(6), device="cuda")
+    ws = ops.new_norm_workspace(N, D)
+    for pads, at in (((0, 0, 0), 0), ((1, 5, 3), 3)):
+        x, dy = rows(N, D, dtype, 26, pads[0], at), rows(N, D, dtype, 27, pads[1], at, off=0.05)
+        buf = torch.full((N * (D + pads[2]) + at + 9,), 5.0, dtype=dtype, device="cuda")
+        wide = buf[at:at + N * (D + pads[2])].view(N, D + pads[2])
+        got = (ops.moe_rmsnorm_grad if rms else ops.moe_layernorm_grad)(dy, x, gamma, EPS, ws, d_x=wide[:, :D])
+        h, r, dm, rel, e_h = statistics(x, rms, EPS)
+        d, gm = dy.double(), gamma.double()
+        g = d * gm
+        mgh, mg = (g * h).mean(dim=1, keepdim=True), torch.zeros_like(r) if rms else g.mean(dim=1, keepdim=True)
+        sizes = g.abs().sum(dim=1, keepdim=True)
+        e_mgh = r / D * (47 * U * (g * h / r).abs().sum(dim=1, keepdim=True) + sizes * dm) + mgh.abs() * (rel + 2 * U)
+        inner = g - mg - h * mgh
+        tol = r * (46 * U * sizes / D + h.abs() * e_mgh + mgh.abs() * e_h + 4 * U * (g.abs() + mg.abs() + (h * mgh).abs()))
+        close(got[0], r * inner, tol + (r * inner).abs() * (rel + 2 * U), dtype)
+        n_c = N / 152 + 64
+        close(got[1], (d * h).sum(0), (d.abs() * e_h).sum(0) + n_c * U * (d * h).abs().sum(0))
+        if not rms:
+            close(got[2], d.sum(0), n_c * U * d.abs().sum(0))
+        assert torch.all(wide[:, D:] == 5) and torch.all(buf[:at] == 5) and torch.all(buf[-9:] == 5)

@@ -690,9 +690,9 @@ int moe_rmsnorm_grad(const void *d_y, int64_t d_y_stride, const void *x, int64_t
  * depends on the sizes, not on the other rows' values); the epilogue is fp32,
  * SiLU within 2^-16 of its value, GELU within 2^-18 above -4 and 2^-15 below (values under
  * 2^-126 may be 0); one rounding to y's type.
- * Few rows (at most 32 over experts; of one matrix 8, or up to 32 that fit beside the
- * weights in shared memory) run on a kernel that reads each touched expert's weights
- * once; more rows on tensor-core tiles of 256 weight rows x up to 256 rows.  What a
+ * Few rows (8 an expert, 32 in all; up to 32 of fewer experts where their matrices are
+ * small) run on a kernel that reads each touched expert's weights once; more rows on
+ * tensor-core tiles of 256 weight rows x up to 256 rows.  What a
  * row holds reaches its own result only, what an expert's weights hold its own rows.
  *   ws: status word (256 bytes); calls on several streams may share it. */
 enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };

@@ -173,15 +173,35 @@ int tiles_of(int n_rows) { return n_rows <= 8 ? 1 : n_rows <= 16 ? 2 : 4; }
 size_t red_bytes(int n_rows) { return (size_t)CONSUMERS * tiles_of(n_rows) * 512; }
 int columns(int K) { return std::min(KC, (K + 31) / 32 * 32); }
 
+// Weight rows (gate and up: pairs) of a unit: 16 (8), fewer where that leaves SMs without one.
+int tile_of(const Matmul16Call &c) {
+    const int sms = std::max(1, device_sm_count());
+    const int64_t most_rows = (int64_t)std::min(c.E, c.n_rows) * c.R;
+    return (int)std::min<int64_t>(c.w_up != nullptr ? 8 : 16, (most_rows + sms - 1) / sms);
+}
+
 // The rows this kernel serves: 32 are four column tiles of its instructions, and beyond them it would read the weights
-// again.  Of one matrix 8, or all that can lie in shared memory: rows that every unit of weights fetches from L2 cost
-// as much as these.  In us, here and on tiles: 16 x 2048 x 2048 11.4 and 15.5, 32 of them 15.5 and 15.5, 16 x 16384 x
-// 2048 21.7 and 19.6; not in shared memory 32 x 16384 x 2048 38 and 20, 16 x 8192 x 8192 38 and 34, 32 of them 65 and
-// 34.
+// again.  Up to 8 an expert on average are one column tile: always.  More cost it what each unit of weights takes to
+// multiply with all of them (and to fetch them from L2, unless they lie in shared memory); tiles take a time of their own
+// that grows with K only.  In us from a graph, here and on tiles:
+//   one matrix        n = 12          16           24           32
+//   1000 x 4096      8.0 17.0     8.4 17.0    12.5 17.2    15.6 17.3    (143 units)
+//   2048 x 2048 *    5.9 10.9     6.1 10.9     8.4 11.0    10.2 11.0    (147; * in shared memory: 12 and 16 rows)
+//   2048 x 16384    24.9 51.6    25.0 51.7    41.8 51.6    54.8 51.7    (147)
+//   4096 x 4096     12.1 17.1    12.5 17.1    16.3 17.0    19.7 17.2    (256)
+//   8192 x 2048 *   10.2 11.6    10.5 11.6    16.6 11.8    19.9 11.7    (512)
+//   8192 x 8192     31.4 29.5    33.3 29.5    48.5 29.5    60.2 29.8    (512)
+//   16384 x 2048 *  16.1 15.5    16.2 15.5    27.9 15.6    33.2 15.7    (1024)
+//   by offsets, 8192 x 8192: 1 matrix 16 rows 33.9 34.7, 32 rows 60.7 34.9; 2 matrices 16 rows 46.9 50.5, 32 rows
+//   60.9 50.5; 3, 32 rows 84.7 81.5; 4, 32 rows 86.5 91.8; 1000 x 4096: 2, 32 rows 10.9 18.7; 3, 32 rows 11.3 19.0
+// (Where most of the rows are one expert's, which only the device knows, it is as with one matrix.)
 bool serves(const Matmul16Call &c) {
-    int stages;
     if (c.n_rows > MAX_ROWS) return false;
-    return c.expStart != nullptr || c.n_rows <= 8 || stage_rows(c, pitch_of(columns(c.K)), red_bytes(c.n_rows), &stages);
+    if (c.n_rows <= 8 * c.E) return true;
+    const int tile = tile_of(c);
+    const int64_t units = (c.R + tile - 1) / tile;
+    int stages;
+    return units * c.n_rows <= (stage_rows(c, pitch_of(columns(c.K)), red_bytes(c.n_rows), &stages) ? 8192 : 5600);
 }
 
 int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
@@ -190,10 +210,7 @@ int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
     a.status = status;
     const int sms = std::max(1, device_sm_count());
     const int ntm = tiles_of(c.n_rows);
-    const bool pair = c.w_up != nullptr;
-    // Units of 16 weight rows (8 pairs), fewer where that leaves SMs without one.
-    const int64_t most_rows = (int64_t)std::min(c.E, c.n_rows) * c.R;
-    a.tile = (int)std::min<int64_t>(pair ? 8 : 16, (most_rows + sms - 1) / sms);
+    a.tile = tile_of(c);
     a.tiles = (c.R + a.tile - 1) / a.tile;
     a.kc = columns(c.K);
     a.pitch = pitch_of(a.kc);

@@ -280,3 +280,22 @@ def test_activations_of_bf16_over_their_range(ops, ws, n):
         for act in ("relu", "silu", "gelu"):
             ref = act_of[act](x[:, :1].double())
             close(ops.moe_matmul(x, w, ws, act=act), ref, 2.0 ** -15 * ref.abs() + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("E", [1, 2, 3])
+@pytest.mark.parametrize("n", [9, 12, 16, 17, 24, 25, 31, 32])
+def test_some_rows_of_few_matrices(ops, ws, n, E, dtype):
+    """Where either kernel may serve, by the sizes of the matrices: the definition's results, with offsets (uneven ones,
+    one matrix among them) and without, gate and up, rows behind the last segment left alone."""
+    for R, K in ((40, 64), (2600, 72), (9000, 40)):
+        x, w, up = whole((n + 2, K), dtype, 1, 1), whole((E, R, K), dtype, 2, 1), whole((E, R, K), dtype, 3, 1)
+        for start in ([n * e // E for e in range(E + 1)], [0] + [n - 1] * (E - 1) + [n]):
+            offsets_ = torch.tensor(start, dtype=torch.int32, device="cuda")
+            for es, kw in ((offsets_, dict()), (offsets_, dict(w_up=up))) + (((None, dict()),) if E == 1 else ()):
+                rows = x[:n] if es is None else x
+                y = torch.full((rows.shape[0], R), 7.0, dtype=dtype, device="cuda")
+                ops.moe_matmul(rows, w, ws, expStart=es, y=y, **kw)
+                ref, _ = reference(rows, w, start, **kw)
+                assert torch.equal(y[:n], ref[:n].to(dtype)) and torch.all(y[n:] == 7)
+    assert ops.moe_workspace_status(ws) == 0

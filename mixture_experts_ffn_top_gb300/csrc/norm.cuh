@@ -372,27 +372,25 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) norm_kernel(const NormArgs a)
         if (RING) copies_wait<0>();
         __syncthreads();  // the shared memory serves the sums now
         float *sg = reinterpret_cast<float *>(smem), *sb = sg + cols;
-        for (int g = 0; g < groups; ++g) {  // the rows' groups one after the other
-            if (group == g)
+        // (the whole CTA works on a row: shorter ones go by tiles)
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (in(i))
+        for (int i = 0; i < NV; ++i)
+            if (in(i))
 #pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            const int c = vec_place<V>(at + i * apart + j, nvec);
-                            auto one = [&](const E *e) {
-                                if constexpr (V == 1) {
-                                    return e[i];
-                                } else {
-                                    const float2 v = values_of(e[i * P + j / 2]);
-                                    return j % 2 ? v.y : v.x;
-                                }
-                            };
-                            sg[c] = g ? sg[c] + one(dg) : one(dg);
-                            if constexpr (!RMS) sb[c] = g ? sb[c] + one(db) : one(db);
+                for (int j = 0; j < V; ++j) {
+                    const int c = vec_place<V>(at + i * apart + j, nvec);
+                    auto one = [&](const E *e) {
+                        if constexpr (V == 1) {
+                            return e[i];
+                        } else {
+                            const float2 v = values_of(e[i * P + j / 2]);
+                            return j % 2 ? v.y : v.x;
                         }
-            __syncthreads();
-        }
+                    };
+                    sg[c] = one(dg);
+                    if constexpr (!RMS) sb[c] = one(db);
+                }
+        __syncthreads();
         float *to = a.part ? a.part + (int64_t)(blockIdx.x / a.cluster) * 2 * a.D : a.d_gamma;
         float *to_b = a.part ? to + a.D : a.d_beta;
         for (int c = tid; c < cols; c += blockDim.x) {

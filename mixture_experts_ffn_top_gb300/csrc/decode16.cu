@@ -15,10 +15,12 @@
 //      groups of warps takes a stage hangs on expert and columns alone, and each walks its experts ascending, so that a
 //      token's sum has the same order whatever the other tokens chose (see Part).
 // The rings (stream16.cuh) run on through the second barrier: the first down tiles fly while it completes.
-// bf16, 64 experts of 1024 x 2048, top 8: one token 30 us (floor 14.9), eight tokens 95 us (82% of the copy rate); 32
-// tokens over 128 experts of 768 some of which are ahead 99 us (94%).  Of eight tokens' time the router takes 3.3 us,
-// the first barrier 1.3, routing and lists 4.1, gate and up 55, the second barrier 4 to 5, down 30: what is left above
-// the bytes are the 9 us in which no weights fly and the barrier's wait for the slowest CTA.
+// bf16, 64 experts of 1024 x 2048, top 8: one token 31.8 us (floor 14.9), eight tokens 94.8 us (43 experts touched, 84%
+// of the copy rate).  Of eight tokens' time 9 us pass until the first weights (router, barrier, routing, lists), gate and
+// up take 61, the second barrier 4 to 7, down 27: what is left above the bytes are the 9 us in which no weights fly and
+// the barrier's wait for the slowest CTA.  32 tokens over 128 experts of 768: at uniform choice (111 touched) 196 us, 79%;
+// where some are ahead (26 touched) 104 us, 34%: 43 us of them are down, where every CTA reads all of h from L2 (120 MB
+// beside 80 MB of weights) and a popular expert's 32 entries take eight tiles of instructions for one stage of weights.
 //
 // h enters the tensor cores as two 16-bit columns, its rounded value and the rest: 16 significant bits in bf16.  In fp16 a
 // token's h is first scaled by the power of two that brings its largest to 2^14 .. 2^15 (a fp16 h itself could overflow or

@@ -644,8 +644,9 @@ int launch(const Matmul16Call &c, unsigned *status, cudaStream_t s) {
             if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) return (int)MOE_ERR_CUDA;
             most_pairs[dev].store(pairs, std::memory_order_relaxed);
         }
-        // one matrix and few tiles: narrower ones, so that more SMs have one (256 to 1024 rows x 2048 x 2048 17 us,
-        // with whole tiles 22; nothing changes from 2048 x 4096 x 2048 on)
+        // one matrix and few tiles: narrower ones, so that more SMs have one.  In us from a graph, tiles 64, 128 and 256
+        // wide: 256 x 2048 x 2048 11.4 12.3 16.1, 1024 x 2048 x 2048 18.2 13.3 16.9, 2048 x 2048 x 2048 31.2 19.9 17.8,
+        // 256 x 8192 x 2048 18.4 14.2 17.6, 300 x 1000 x 4096 17.6 19.0 20.3
         a.width = TILE;
         while (c.expStart == nullptr && a.width > 64 && (int64_t)((c.n_rows + a.width / 2 - 1) / (a.width / 2)) * a.wtiles <= pairs) a.width /= 2;
         // token rows of a CTA's half tile, as its box brings them

@@ -13,9 +13,9 @@
 // anyway: nothing is saved by the forward pass.  The variance is summed from the deviations (a second sum over the
 // registers), not from squares: rows far off centre lose nothing.  Rows too long for a CTA are shared by a cluster of
 // CTAs, whose sums meet in distributed shared memory.
-// bf16, 8192 x 2048: forward 17 us, 3.9 TB/s of the reads and writes its results need (the 33 MB written stay in L2;
-// floor 9.9 us); gradient 32 us, 3.1 TB/s (14.8 us).  An SM takes 54 of these rows; what is left
-// above the floors is the first rows' latency, the last rows' tail, the second kernel, and instructions.
+// bf16, 8192 x 2048, from a graph: forward 15.4 us, 4.4 TB/s of the reads and writes its results need (the 33 MB written
+// stay in L2; floor 9.9 us); gradient 29.3 us, 3.4 TB/s (14.8 us).  An SM takes 54 of these rows; what is left above the
+// floors is the first rows' latency, the last rows' tail, the second kernel, and instructions.
 #pragma once
 
 #include <algorithm>
@@ -908,8 +908,14 @@ int launch_norm_width(NormArgs a, void *scratch, cudaStream_t s) {
         while ((per << l2) < a.D && l2 < 9) ++l2;
         return l2;
     };
-    // Forward, few rows answer soonest spread over many threads: bf16, 304 x 8192 12.4 us against 16.5, 608 x 8192 15.5
-    // against 19.6; 2432 x 8192 would be 29.9 against 27.8.  (Gradients gain nothing: 304 x 2048 14 against 12.)
+    // Forward, few rows answer soonest spread over many threads.  bf16, us from a graph, so and as many rows:
+    //   columns      512          1024         2048         4096         8192
+    //   152 rows   2.4  2.5     2.8  3.4     3.2  4.9     3.9  6.2     5.5  7.7
+    //   304        2.6  2.6     3.1  3.4     3.7  5.1     5.2  6.2     6.6  7.8
+    //   456        2.7  2.6     3.7  3.4     5.0  5.1     6.3  6.3     8.2  8.4
+    //   608        2.7  2.7     3.7  3.6     5.1  5.0     6.3  6.2     9.4  9.1
+    //   1216       3.4  2.6     5.1  3.4     6.3  5.2     8.9  7.7    14.7 13.3
+    // (Gradients gain nothing.)
     const bool small = !GRAD && ((int64_t)NS * V << threads_log2(NS * V)) >= a.D && a.N <= 4 * sms;
     if constexpr (GRAD) {
         if (a.D * 2 * (int)sizeof(T) <= TILE_MAX_BYTES && a.D <= TILE_MAX_D)

@@ -957,7 +957,8 @@ def moe_matmul(x, w, ws, expStart=None, w_up=None, bias=None, bias_up=None, act=
     """y [rows, R] = act(x w^T + bias) (* (x w_up^T + bias_up)) (+ residual) for float16 or bfloat16 rows x [rows, K].
     w, w_up [E, R, K] (or [R, K]: one matrix), bias, bias_up [E, R] (or [R]) float32; expStart [E+1] int32 as of
     moe_sort_tokens, or None for a single matrix.  Rows from expStart[E] on are left as they were (uninitialised when
-    `y` is not given).  residual may be y."""
+    `y` is not given).  residual may be y.  ws: any initialised workspace (new_sort_workspace(1, 1, 1) makes a small one);
+    only its status word is used."""
     if act not in ACTS:
         raise ValueError(f"unknown activation {act!r}")
     if w.dim() == 2:
